@@ -14,10 +14,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdf11.so")
-SOURCES = [os.path.join(CSRC, "df11_decode.cu"), os.path.join(CSRC, "df11_gpu_build.cu"),
-           os.path.join(CSRC, "df11_build.cpp")]
-HEADERS = [os.path.join(INCLUDE, "df11.h"), os.path.join(CSRC, "df11_codebook.h"),
-           os.path.join(CSRC, "df11_device_check.h")]
+SOURCES = [os.path.join(CSRC, f) for f in
+           ("df11_decode.cu", "df11_gpu_build.cu", "df11_build.cpp")]
+HEADERS = [os.path.join(INCLUDE, "df11.h")] + [os.path.join(CSRC, f) for f in
+           ("df11_codebook.h", "df11_device.cuh", "df11_device_check.h", "df11_launch.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -36,7 +36,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [NVCC, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
            "-Xcompiler", "-fPIC,-O3,-pthread", "-I", INCLUDE,
-           "--expt-relaxed-constexpr", *SOURCES, "-o", tmp, "-lpthread"]
+           "--expt-relaxed-constexpr", "--threads", "0", *SOURCES, "-o", tmp, "-lpthread"]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd), file=sys.stderr)
