@@ -155,6 +155,10 @@ def lib():
     L.df11_decode_gemm.argtypes = [ctypes.POINTER(TensorDesc), ctypes.POINTER(GemvOp),
                                    ctypes.c_int, vp, vp]
     L.df11_decode_gemm.restype = ctypes.c_int
+    L.df11_decode_linear.argtypes = [vp, vp, ctypes.c_int, vp, ctypes.c_size_t, vp, vp]
+    L.df11_decode_linear.restype = ctypes.c_int
+    L.df11_linear_workspace.argtypes = [vp, vp, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
+    L.df11_linear_workspace.restype = ctypes.c_int
     L.df11_exponent_histogram.argtypes = [vp, u64, vp, vp]
     L.df11_exponent_histogram.restype = ctypes.c_int
     L.df11_test_withhold_copies.argtypes = [ctypes.c_int, u32]
@@ -188,7 +192,8 @@ class Df11Host:
     sign_mantissa: np.ndarray  # uint8 (n rounded up to 16)
     chunk_counts: np.ndarray   # uint8, codewords starting in each chunk
     shape: tuple = ()
-    interleave: int = 1        # rows interleaved per 16 columns in the stream (1: row-major)
+    interleave: int = 1        # rows interleaved per 16 columns in the stream (1: row-major;
+                               # LINEAR_TILES: the linear product's tiles)
 
     @property
     def n(self) -> int:
@@ -300,7 +305,9 @@ class Df11Device:
     chunk_counts: Optional[torch.Tensor] = None
     shape: tuple = ()
     decode_table: Optional[torch.Tensor] = None  # df11_build_decode_table output
-    interleave: int = 1  # rows interleaved per 16 columns in the stream (1: row-major)
+    # rows interleaved per 16 columns in the stream (1: row-major; LINEAR_TILES:
+    # the linear product's tiles)
+    interleave: int = 1
 
     @classmethod
     def _in_block(cls, params: Params, block: torch.Tensor, offs: tuple, sizes: tuple,
@@ -714,3 +721,7 @@ def check_device_error(err: torch.Tensor):
     if code != 0:
         msg = lib().df11_device_error_string(code).decode()
         raise Df11Error(f"decode reported {DEV_ERRORS.get(code, code)}: {msg}")
+
+
+from .linear import (LINEAR_TILES, LinearOp, LinearPlan, compress_linear,  # noqa: E402,F401
+                     decode_linear, tile_linear, untile_linear)

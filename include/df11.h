@@ -245,6 +245,75 @@ df11_status df11_decode_gemv(const df11_tensor *tensors, const df11_gemv *ops, i
 df11_status df11_decode_gemm(const df11_tensor *tensors, const df11_gemv *ops, int count,
                              int32_t *d_err, df11_stream_t stream);
 
+/* ---------------------------------------------------------------------- */
+/* The linear product of a model's layer on compressed weights.           */
+
+/* Element types of the linear product's and the embedding's operands. */
+#define DF11_BF16 0
+#define DF11_F32 1
+
+/* Activations of the linear product. */
+#define DF11_ACT_NONE 0
+#define DF11_ACT_RELU 1      /* max(v, 0); NaN stays */
+#define DF11_ACT_GELU 2      /* v * Phi(v), Phi the normal distribution */
+#define DF11_ACT_GELU_TANH 3 /* v/2 * (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+#define DF11_ACT_SILU 4      /* v / (1 + exp(-v)) */
+
+/* Most tokens of one linear product. */
+#define DF11_LINEAR_MAX_BATCH (1u << 20)
+
+/* The linear product applied to one compressed weight:
+ * y[t][r] = act(sum over c of W[r][c] x[t][c] + bias[r]) * multiplier[t][r]
+ *           + residual[t][r]. */
+typedef struct df11_linear {
+  const uint16_t *x;      /* BF16 activations: `batch` rows of `cols` elements */
+  void *y;                /* outputs: `batch` rows of `rows` elements of y_type */
+  const void *bias;       /* `rows` elements of bias_type, or NULL */
+  const void *multiplier; /* `batch` rows of `rows` elements, or NULL */
+  const void *residual;   /* `batch` rows of `rows` elements, or NULL; may be y
+                             itself (same stride and type) */
+  uint32_t rows, cols;    /* of the weight as the model has it */
+  uint32_t batch;         /* tokens: 0 (nothing is done) .. DF11_LINEAR_MAX_BATCH */
+  uint32_t x_stride, y_stride, multiplier_stride, residual_stride; /* elements between rows */
+  int32_t activation;     /* DF11_ACT_* */
+  int32_t y_type, bias_type, multiplier_type, residual_type; /* DF11_BF16 or DF11_F32 */
+} df11_linear;
+
+/*
+ * The linear product of up to any number of weights, in launches of
+ * DF11_MAX_BATCH.  Each tensor holds a weight in the tile order of this
+ * product: rows padded with zeros to a multiple of 16 and columns to a
+ * multiple of 64, and for each block of 16 rows and each group of 64 columns the
+ * 16 rows' 64 elements one after another; params.n is the padded count.  Needs
+ * chunk counts, a decode table, T = 256 and C = 8, 16 or 24, one C per call;
+ * out_bf16 is not used (may be NULL).
+ *   Sums run in fp32 (products of BF16 are exact there) in an order that the
+ * sizes and the device fix, so a call repeats bit for bit; bias, activation,
+ * multiplier and residual are applied in fp32 and the result is rounded once.  A
+ * token's row of x with an infinity gives NaN or an infinity in every output of
+ * that token.  Up to 32 tokens (the most of the launch's tensors) the weights
+ * are decoded and multiplied in one kernel and never written; beyond, they are
+ * decoded into the workspace and multiplied on the tensor cores.
+ *   `workspace`: df11_linear_workspace bytes of device memory, 256-byte aligned,
+ * that no other work uses until this call's work is done; nothing is kept in
+ * it between calls.  y may not overlap x, the multiplier (unless it is the same
+ * memory with the same stride and type) or the workspace.
+ *   Same conventions as df11_decode_batched otherwise (asynchronous, no
+ * allocation, device-detected errors in d_err).  DF11_ERR_INVALID for sizes,
+ * strides, types or activations outside the rules and for a workspace that is
+ * too small, DF11_ERR_UNSUPPORTED for a tensor without counts or table or of
+ * another chunk size, DF11_ERR_TOO_LARGE above DF11_LINEAR_MAX_BATCH.
+ */
+df11_status df11_decode_linear(const df11_tensor *tensors, const df11_linear *ops, int count,
+                               void *workspace, size_t workspace_bytes, int32_t *d_err,
+                               df11_stream_t stream);
+
+/* Bytes of workspace that df11_decode_linear needs for this call on the current
+ * device (it depends on the sizes and on how many thread blocks the device holds;
+ * pointers are checked as in the call, but nothing is queued). */
+df11_status df11_linear_workspace(const df11_tensor *tensors, const df11_linear *ops, int count,
+                                  size_t *bytes);
+
 /*
  * Derive, on the device, the decode table of one tensor from its luts and
  * code_lengths (device pointers, as in df11_tensor) into `out` (device,
