@@ -39,6 +39,7 @@ STATUS = {
 DEV_ERRORS = {
     0: "DF11_DEV_OK", 1: "DF11_DEV_ERR_COUNT", 2: "DF11_DEV_ERR_OVERRUN",
     3: "DF11_DEV_ERR_TABLE", 4: "DF11_DEV_ERR_TIMEOUT", 5: "DF11_DEV_ERR_CAPACITY",
+    6: "DF11_DEV_ERR_INDEX",
 }
 
 
@@ -159,6 +160,12 @@ def lib():
     L.df11_decode_linear.restype = ctypes.c_int
     L.df11_linear_workspace.argtypes = [vp, vp, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
     L.df11_linear_workspace.restype = ctypes.c_int
+    L.df11_decode_embedding.argtypes = [vp, vp, vp, vp]
+    L.df11_decode_embedding.restype = ctypes.c_int
+    L.df11_embedding_gradient.argtypes = [vp, vp, ctypes.c_size_t, vp, vp]
+    L.df11_embedding_gradient.restype = ctypes.c_int
+    L.df11_embedding_gradient_workspace.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
+    L.df11_embedding_gradient_workspace.restype = ctypes.c_int
     L.df11_exponent_histogram.argtypes = [vp, u64, vp, vp]
     L.df11_exponent_histogram.restype = ctypes.c_int
     L.df11_test_withhold_copies.argtypes = [ctypes.c_int, u32]
@@ -725,3 +732,5 @@ def check_device_error(err: torch.Tensor):
 
 from .linear import (LINEAR_TILES, LinearOp, LinearPlan, compress_linear,  # noqa: E402,F401
                      decode_linear, tile_linear, untile_linear)
+from .embedding import (EmbeddingGradOp, EmbeddingOp, EmbeddingPlan,  # noqa: E402,F401
+                        decode_embedding, embedding_gradient)

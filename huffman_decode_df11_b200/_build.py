@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdf11.so")
 SOURCES = [os.path.join(CSRC, f) for f in
-           ("df11_decode.cu", "df11_linear.cu", "df11_gpu_build.cu", "df11_build.cpp")]
+           ("df11_decode.cu", "df11_linear.cu", "df11_embedding.cu", "df11_gpu_build.cu",
+            "df11_build.cpp")]
 HEADERS = [os.path.join(INCLUDE, "df11.h")] + [os.path.join(CSRC, f) for f in
            ("df11_codebook.h", "df11_device.cuh", "df11_device_check.h", "df11_launch.h")]
 

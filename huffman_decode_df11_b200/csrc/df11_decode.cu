@@ -1770,6 +1770,7 @@ const char *df11_device_error_string(int32_t code) {
     case DF11_DEV_ERR_TABLE: return "invalid lookup-table entry or zero code length";
     case DF11_DEV_ERR_TIMEOUT: return "shared-memory copy did not complete in time";
     case DF11_DEV_ERR_CAPACITY: return "block or chunk holds more elements than its parameters allow";
+    case DF11_DEV_ERR_INDEX: return "a token id outside the embedding table";
   }
   return "unknown device error";
 }

@@ -1,0 +1,857 @@
+// df11_embedding.cu -- the token embedding on a compressed table: lookup of
+// rows, and the table's gradient.
+//
+// Lookup (df11_decode_embedding): out[t] = scale * W[ids[t]].  The table is an
+// ordinary compressed tensor, row-major; only the chunks that hold a row are
+// decoded.  A warp takes a segment of a token's row: it finds the format block
+// that holds the segment's first element (the positions are close to even, so
+// 32 probes around the proportional guess nearly always hold it), the chunk in
+// it from the chunk counts, and walks 32 chunks at a time, one per lane, as the
+// decode kernel does.
+//
+// Gradient (df11_embedding_gradient): dW[v] = scale * sum of grad[t] over the
+// tokens t with ids[t] = v.  The tokens are sorted by id (a stable radix sort by one
+// cluster of thread blocks), so a row's tokens are a run of the sorted list.  The
+// list is cut into equal pieces; a thread block sums the runs of its piece, and
+// a run that crosses pieces is put together by a second kernel from the pieces'
+// partial sums, in order: nothing depends on scheduling, and a token that
+// half of the batch shares costs no more than any other.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "df11.h"
+#include "df11_device.cuh"
+#include "df11_device_check.h"
+#include "df11_launch.h"
+
+using namespace df11_internal;
+
+namespace {
+
+constexpr int kT = 256;
+constexpr int kWarps = 8;
+
+// fp32 to BF16, to nearest, ties to even; NaN stays NaN
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+  uint16_t r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// ---- lookup -------------------------------------------------------------------
+
+struct EmbedArgs {
+  KTensor k;
+  const void *ids;
+  void *out;
+  int32_t *err;
+  uint64_t out_stride;
+  uint32_t tokens, rows, dim;
+  uint32_t segs, seg_len;   // a row's segments, and elements per segment
+  uint32_t ids64, out_f32, scaled;
+  float scale;
+  uint32_t vec;             // rows of 16-element groups on 16-byte boundaries
+  uint32_t region_bytes;
+  uint32_t spin_limit;
+};
+
+__device__ __forceinline__ float scaled_value(const EmbedArgs &a, uint32_t bits) {
+  const float v = __uint_as_float(bits << 16);
+  return a.scaled ? v * a.scale : v;
+}
+
+__device__ __forceinline__ void embed_store(const EmbedArgs &a, size_t i, uint32_t bits) {
+  if (a.out_f32) static_cast<float *>(a.out)[i] = scaled_value(a, bits);
+  else static_cast<uint16_t *>(a.out)[i] =
+      (uint16_t)(a.scaled ? bf16_bits(scaled_value(a, bits)) : bits);
+}
+
+// the last format block whose first element is at or before element e
+__device__ uint32_t find_block(const KTensor &k, uint32_t e, int lane) {
+  const uint32_t guess = (uint32_t)((uint64_t)e * k.num_blocks / k.n);
+  const uint32_t lo = guess > 15u ? guess - 15u : 0u;
+  const uint32_t i = lo + (uint32_t)lane;
+  const bool at = i < k.num_blocks && __ldg(k.block_out_pos + i) <= e;
+  const uint32_t m = __ballot_sync(0xFFFFFFFFu, at);
+  const bool below = m == 0, above = m == 0xFFFFFFFFu && lo + 32u < k.num_blocks;
+  if (!below && !above) return lo + 31u - (uint32_t)__clz(m);
+  uint32_t first = below ? 0u : lo + 31u, last = below ? lo + 1u : k.num_blocks;
+  while (last - first > 1u) {
+    const uint32_t mid = first + ((last - first) >> 1);
+    if (__ldg(k.block_out_pos + mid) <= e) first = mid;
+    else last = mid;
+  }
+  return first;
+}
+
+template <int C>
+__global__ void __launch_bounds__(kWarps * 32)
+    df11_embedding_kernel(const __grid_constant__ EmbedArgs a) {
+  constexpr int NW = C / 4 + 1;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const KTensor &tk = a.k;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t *lens_s = smem + kOffLens;
+  uint32_t *lut0_s = reinterpret_cast<uint32_t *>(smem + kOffLut0);
+  const uint32_t wide = smem_addr(smem + kOffWide);
+  uint8_t *region_p = smem + kOffStages + warp * a.region_bytes;
+  const uint32_t region = smem_addr(region_p);
+  const uint32_t tbar = smem_addr(smem);
+  if (tid == 0) {
+    mbar_init(tbar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_arrive_expect_tx(tbar, DF11_DECODE_TABLE_BYTES);
+    bulk_g2s(smem_addr(lens_s), tk.decode_table, DF11_DECODE_TABLE_BYTES, tbar);
+  }
+  for (uint32_t i = lane; i < a.region_bytes / 16; i += 32)
+    reinterpret_cast<uint4 *>(region_p)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();  // the barrier is initialised
+  pdl_wait();       // the ids may come from the previous kernel, which may read the output
+  pdl_launch_dependents();
+  bool table = false;
+  const uint64_t items = (uint64_t)a.tokens * a.segs;
+  const uint64_t chunks = (uint64_t)tk.num_blocks * kT;
+  for (uint64_t item = blockIdx.x + (uint64_t)gridDim.x * warp; item < items;
+       item += (uint64_t)gridDim.x * kWarps) {
+    const uint32_t token = (uint32_t)(item / a.segs), seg = (uint32_t)(item - (uint64_t)token * a.segs);
+    const uint32_t c_first = seg * a.seg_len, c_last = min(c_first + a.seg_len, a.dim);
+    const int64_t id = a.ids64 ? static_cast<const int64_t *>(a.ids)[token]
+                               : static_cast<const int32_t *>(a.ids)[token];
+    const size_t out0 = (size_t)token * a.out_stride;
+    if (id < 0 || id >= (int64_t)a.rows) {
+      if (lane == 0) report(a.err, DF11_DEV_ERR_INDEX);
+      for (uint32_t c = c_first + lane; c < c_last; c += 32) {
+        if (a.out_f32) static_cast<float *>(a.out)[out0 + c] = 0.f;
+        else static_cast<uint16_t *>(a.out)[out0 + c] = 0;
+      }
+      continue;
+    }
+    const uint32_t row0 = (uint32_t)id * a.dim;  // elements of a tensor: below 2^32
+    const uint32_t e0 = row0 + c_first, e1 = row0 + c_last;
+    const uint32_t b = find_block(tk, e0, lane);
+    uint32_t P = __ldg(tk.block_out_pos + b), chunk0;
+    if (P > e0) {  // inconsistent positions
+      if (lane == 0) report(a.err, DF11_DEV_ERR_COUNT);
+      continue;
+    }
+    {
+      // the chunk of block b that holds e0: the last whose first element is at
+      // or before it
+      const uint2 cv = __ldg(reinterpret_cast<const uint2 *>(tk.chunk_counts + (size_t)b * kT) + lane);
+      const uint32_t sum = __dp4a(cv.x, 0x01010101u, __dp4a(cv.y, 0x01010101u, 0u));
+      uint32_t incl = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      const uint32_t off = e0 - P;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, incl - sum <= off);
+      const int src = 31 - __clz(m);  // lane 0's count before is 0: m is not 0
+      uint32_t before = incl - sum, j = 0;
+#pragma unroll
+      for (uint32_t i = 0; i < 7; ++i) {
+        const uint32_t c = ((i < 4 ? cv.x : cv.y) >> (8 * (i & 3))) & 0xFFu;
+        if (j == i && before + c <= off) {
+          before += c;
+          ++j;
+        }
+      }
+      P += __shfl_sync(0xFFFFFFFFu, before, src);
+      chunk0 = b * kT + 8u * src + __shfl_sync(0xFFFFFFFFu, j, src);
+    }
+    for (uint64_t c0 = chunk0; P < e1; c0 += 32) {
+      const uint64_t chunk = c0 + lane;
+      const bool here = chunk < chunks;
+      const uint32_t cnt = here ? __ldg(tk.chunk_counts + chunk) : 0u;
+      uint32_t incl = cnt;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      const uint32_t total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+      if (total == 0 || total > tk.n - P || __any_sync(0xFFFFFFFFu, cnt > tk.max_chunk_elems)) {
+        if (lane == 0) report(a.err, DF11_DEV_ERR_COUNT);
+        break;
+      }
+      const uint32_t E = P + incl - cnt, base = P & ~15u;
+      const bool need = cnt && E < e1 && E + cnt > e0;
+      int start = 0, end = 0, bad = 0;
+      uint32_t w[NW];
+      if (need) {
+        const uint2 *q = reinterpret_cast<const uint2 *>(tk.bitstream + chunk * C);
+#pragma unroll
+        for (int j = 0; j < NW / 2; ++j) {
+          const uint2 v = __ldg(q + j);
+          w[2 * j] = __byte_perm(v.x, 0, 0x0123);
+          w[2 * j + 1] = __byte_perm(v.y, 0, 0x0123);
+        }
+        w[NW - 1] = __byte_perm(__ldg(reinterpret_cast<const uint32_t *>(q + NW / 2)), 0, 0x0123);
+        const uint64_t gbit = 5ull * chunk;
+        const uint32_t *gp = reinterpret_cast<const uint32_t *>(tk.gaps) + (gbit >> 5);
+        const uint32_t v = __funnelshift_l(__byte_perm(__ldg(gp + 1), 0, 0x0123),
+                                           __byte_perm(__ldg(gp), 0, 0x0123), (uint32_t)gbit);
+        start = (int)(v >> 27);
+        end = C * 8 + (int)((v >> 22) & 31u);
+        const uint64_t bit0 = chunk * (C * 8);
+        if (bit0 >= tk.total_bits) start = end = 0;
+        else if ((uint64_t)end > tk.total_bits - bit0) end = (int)(tk.total_bits - bit0);
+        if (tk.masked) {
+#pragma unroll
+          for (int j = 0; j < NW; ++j)
+            w[j] |= __funnelshift_rc(0xFFFFFFFFu, 0u, (uint32_t)max(end - 32 * j, 0));
+        }
+      }
+      if (!table) {
+        table = __all_sync(0xFFFFFFFFu, mbar_wait(tbar, 0, a.spin_limit));
+        if (!table) {
+          if (lane == 0) report(a.err, DF11_DEV_ERR_TIMEOUT);
+          break;
+        }
+      }
+      if (need) {
+        const uint32_t d = E - base;
+        uint32_t got;
+        if (tk.masked) {
+          got = decode_counted<C>(w, start, end, wide, lut0_s, lens_s, tk.luts + 256, tk.num_luts,
+                                  region, d, cnt, bad);
+        } else {
+          got = decode_direct<kT, C, false>(w, start, end, wide, lut0_s, lens_s, tk.luts + 256,
+                                            tk.num_luts, region, d, region + ((d + cnt - 1u) & ~3u),
+                                            bad);
+        }
+        if (!bad && got != cnt) bad = DF11_DEV_ERR_COUNT;
+        if (bad) report(a.err, bad);
+      }
+      __syncwarp();
+      // elements [lo, hi) past `base` are the row's, element i at byte i of the region
+      const uint32_t lo = max(e0, P) - base, hi = min(e1 - base, P - base + total);
+      const uint8_t *sm = tk.sign_mantissa + base;
+      const size_t out_base = out0 + base - row0;  // may wrap below the row: base is before it
+      if (a.vec) {
+        for (uint32_t i = (lo & ~15u) + 16u * lane; i < hi; i += 512u) {
+          const uint4 rv = lds128(region + i);
+          const uint4 sv = __ldg(reinterpret_cast<const uint4 *>(sm + i));
+          const uint2 p0 = fuse4(sv.x, rv.x), p1 = fuse4(sv.y, rv.y);
+          const uint2 p2 = fuse4(sv.z, rv.z), p3 = fuse4(sv.w, rv.w);
+          const uint32_t u[8] = {p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+          const size_t o = out_base + i;
+          if (i >= lo && i + 16u <= hi) {
+            if (a.out_f32) {
+              float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                q[j] = make_float4(scaled_value(a, u[2 * j] & 0xFFFFu), scaled_value(a, u[2 * j] >> 16),
+                                   scaled_value(a, u[2 * j + 1] & 0xFFFFu),
+                                   scaled_value(a, u[2 * j + 1] >> 16));
+            } else {
+              uint32_t r[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                r[j] = a.scaled ? bf16_pair(scaled_value(a, u[j] & 0xFFFFu), scaled_value(a, u[j] >> 16))
+                                : u[j];
+              uint4 *q = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + o);
+              q[0] = make_uint4(r[0], r[1], r[2], r[3]);
+              q[1] = make_uint4(r[4], r[5], r[6], r[7]);
+            }
+          } else {  // a group that two passes share
+#pragma unroll
+            for (uint32_t j = 0; j < 16; ++j)
+              if (i + j >= lo && i + j < hi)
+                embed_store(a, o + j, (u[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+          }
+        }
+      } else {
+        for (uint32_t i = lo + lane; i < hi; i += 32)
+          embed_store(a, out_base + i, fuse1(__ldg(sm + i), lds8(region + i)));
+      }
+      __syncwarp();
+      // the region zero again (a walk over corrupt data may write 7 bytes more)
+      for (uint32_t i = lane; i < (P - base + total + 8u + 15u) >> 4; i += 32)
+        sts128_zero(region + 16u * i);
+      __syncwarp();
+      P += total;
+    }
+  }
+  // the table's copy has landed before the thread block ends
+  if (!table && tid == 0 && !mbar_wait(tbar, 0, a.spin_limit)) report(a.err, DF11_DEV_ERR_TIMEOUT);
+}
+
+// ---- gradient: sort by token ----------------------------------------------------
+
+constexpr int kSortThreads = 1024, kSortWarps = 32, kMaxDigits = 256;
+
+struct SortArgs {
+  const void *ids;
+  uint32_t *key[2], *tok[2];  // the sorted list ends in [passes & 1]
+  uint32_t *touched;          // a bit per row that has tokens; NULL: not wanted
+  int32_t *err;
+  uint32_t tokens, rows, passes, digit_bits, touched_words, ids64;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t v;
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n"
+               " ld.shared::cluster.u32 %0, [a];\n}\n"
+               : "=r"(v)
+               : "r"(addr), "r"(rank)
+               : "memory");
+  return v;
+}
+
+// One cluster sorts (id, token) by id, least significant digit first; every
+// warp keeps a contiguous part of the list, so equal ids stay in token order.
+// An id outside the table sorts behind every row.
+__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ uint32_t whist[kSortWarps][kMaxDigits];
+  __shared__ uint32_t own[kMaxDigits], base[kMaxDigits], warp_total[kMaxDigits / 32];
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  const uint32_t parts = ctas * kSortWarps;
+  const uint64_t per = (((uint64_t)a.tokens + parts - 1) / parts + 31) & ~31ull;
+  const uint64_t begin = per * (rank * kSortWarps + warp);
+  const uint64_t end = begin + per < a.tokens ? begin + per : a.tokens;
+  const uint32_t digits = 1u << a.digit_bits;
+  pdl_wait();  // the ids may come from the previous kernel; the workspace may still be read
+  if (a.touched)
+    for (uint32_t i = rank * kSortThreads + tid; i < a.touched_words; i += ctas * kSortThreads)
+      a.touched[i] = 0;
+  for (uint32_t p = 0; p < a.passes; ++p) {
+    const uint32_t shift = p * a.digit_bits;
+    const uint32_t *sk = a.key[p & 1], *st = a.tok[p & 1];
+    uint32_t *dk = a.key[(p + 1) & 1], *dt = a.tok[(p + 1) & 1];
+    auto load = [&](uint64_t i) -> uint32_t {
+      if (p) return __ldcg(sk + i);
+      const int64_t id = a.ids64 ? static_cast<const int64_t *>(a.ids)[i]
+                                 : static_cast<const int32_t *>(a.ids)[i];
+      return id < 0 || id >= (int64_t)a.rows ? a.rows : (uint32_t)id;
+    };
+    for (uint32_t d = lane; d < digits; d += 32) whist[warp][d] = 0;
+    __syncwarp();
+    for (uint64_t i = begin + lane; i - lane < end; i += 32) {
+      const bool act = i < end;
+      const uint32_t digit = act ? (load(i) >> shift) & (digits - 1u) : 0xFFFFFFFFu;
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, digit);
+      if (act && (peers >> lane) == 1u)  // the last of the peers
+        whist[warp][digit] += __popc(peers);
+      __syncwarp();
+    }
+    __syncthreads();
+    if (tid < digits) {  // counts of the warps before, and this thread block's
+      uint32_t sum = 0;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t v = whist[w][tid];
+        whist[w][tid] = sum;
+        sum += v;
+      }
+      own[tid] = sum;
+    }
+    cluster_sync();
+    if (tid < kMaxDigits) {  // where each digit's tokens of this thread block begin
+      uint32_t total = 0, before = 0;
+      if (tid < digits)
+        for (uint32_t r = 0; r < ctas; ++r) {
+          const uint32_t v = ld_cluster(smem_addr(&own[tid]), r);
+          if (r < rank) before += v;
+          total += v;
+        }
+      uint32_t incl = total;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= (uint32_t)d) incl += v;
+      }
+      base[tid] = incl - total + before;
+      if (lane == 31) warp_total[warp] = incl;
+    }
+    __syncthreads();
+    if (tid < kMaxDigits)
+      for (uint32_t w = 0; w < warp; ++w) base[tid] += warp_total[w];
+    __syncthreads();
+    for (uint64_t i = begin + lane; i - lane < end; i += 32) {
+      const bool act = i < end;
+      const uint32_t key = act ? load(i) : 0u;
+      const uint32_t digit = act ? (key >> shift) & (digits - 1u) : 0xFFFFFFFFu;
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, digit);
+      uint32_t at = 0;
+      if (act) at = base[digit] + whist[warp][digit] + __popc(peers & ((1u << lane) - 1u));
+      __syncwarp();
+      if (act && (peers >> lane) == 1u) whist[warp][digit] += __popc(peers);
+      __syncwarp();
+      if (act) {
+        dk[at] = key;
+        dt[at] = p ? __ldcg(st + i) : (uint32_t)i;
+        if (p == 0) {
+          if (key == a.rows) report(a.err, DF11_DEV_ERR_INDEX);
+          else if (a.touched) atomicOr(a.touched + (key >> 5), 1u << (key & 31u));
+        }
+      }
+    }
+    cluster_sync();  // the list is whole, and own[] read by everyone
+  }
+  pdl_launch_dependents();
+}
+
+// ---- gradient: sums of runs -------------------------------------------------------
+
+constexpr int kRunThreads = 128;
+constexpr uint32_t kMaxPiece = 32;  // tokens of the sorted list per thread block
+
+struct RunArgs {
+  const void *grad;
+  void *out;
+  const uint32_t *key, *tok;  // sorted
+  const uint32_t *touched;    // NULL: rows without tokens keep their values
+  float *head, *tail;         // per piece: sums of the run that began before it / that goes on
+  uint64_t grad_stride, out_stride;
+  uint32_t tokens, rows, dim, piece, pieces, col_tiles, part_stride;
+  uint32_t accumulate;
+  float scale;
+};
+
+template <typename G, int V>
+struct Row;
+template <>
+struct Row<float, 4> {
+  static __device__ __forceinline__ void load(const float *p, float (&v)[4]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+};
+template <>
+struct Row<uint16_t, 8> {
+  static __device__ __forceinline__ void load(const uint16_t *p, float (&v)[8]) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo(u[j]);
+      v[2 * j + 1] = bf16_hi(u[j]);
+    }
+  }
+};
+template <>
+struct Row<float, 1> {
+  static __device__ __forceinline__ void load(const float *p, float (&v)[1]) { v[0] = __ldg(p); }
+};
+template <>
+struct Row<uint16_t, 1> {
+  static __device__ __forceinline__ void load(const uint16_t *p, float (&v)[1]) {
+    v[0] = bf16_lo(__ldg(p));
+  }
+};
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(uint16_t v) { return bf16_lo(v); }
+__device__ __forceinline__ void narrow(float *p, float v) { *p = v; }
+__device__ __forceinline__ void narrow(uint16_t *p, float v) { *p = (uint16_t)bf16_bits(v); }
+
+// dW[row], columns col .. col + V - 1: scale * sum, added to what is there or not
+template <typename O, int V>
+__device__ __forceinline__ void write_row(const RunArgs &a, uint32_t row, uint32_t col,
+                                          const float (&s)[V]) {
+  O *p = static_cast<O *>(a.out) + (size_t)row * a.out_stride + col;
+  float v[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] = s[j] * a.scale;
+  if (a.accumulate) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] += widen(p[j]);
+  }
+  if constexpr (V == 1) {
+    narrow(p, v[0]);
+  } else if constexpr (sizeof(O) == 4) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4)
+      *reinterpret_cast<float4 *>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 4)
+      *reinterpret_cast<uint2 *>(p + j) =
+          make_uint2(bf16_pair(v[j], v[j + 1]), bf16_pair(v[j + 2], v[j + 3]));
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void write_part(float *p, const float (&s)[V]) {
+  if constexpr (V == 1) {
+    p[0] = s[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 4)
+      *reinterpret_cast<float4 *>(p + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+  }
+}
+
+// Thread blocks below pieces * col_tiles: the runs of one piece of the sorted
+// list, kRunThreads * V columns.  The others: 32 rows each, those without a token
+// set to zero.
+template <typename G, typename O, int V>
+__global__ void __launch_bounds__(kRunThreads) embedding_runs_kernel(const __grid_constant__ RunArgs a) {
+  __shared__ uint32_t key_s[kMaxPiece + 2], tok_s[kMaxPiece];
+  const uint32_t tid = threadIdx.x;
+  pdl_wait();
+  const uint32_t run_blocks = a.pieces * a.col_tiles;
+  if (blockIdx.x >= run_blocks) {
+    const uint32_t word = blockIdx.x - run_blocks;
+    const uint32_t bits = __ldg(a.touched + word);
+    for (uint32_t r = 0; r < 32; ++r) {
+      const uint32_t row = 32u * word + r;
+      if (row >= a.rows) break;
+      if ((bits >> r) & 1u) continue;
+      O *p = static_cast<O *>(a.out) + (size_t)row * a.out_stride;
+      if constexpr (V == 1) {
+        for (uint32_t c = tid; c < a.dim; c += kRunThreads) p[c] = O(0);
+      } else {
+        constexpr uint32_t per = 16 / sizeof(O);  // dim is a multiple of V, and of per
+        for (uint32_t c = tid * per; c < a.dim; c += kRunThreads * per)
+          *reinterpret_cast<uint4 *>(p + c) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    return;
+  }
+  const uint32_t piece = blockIdx.x / a.col_tiles, ct = blockIdx.x - piece * a.col_tiles;
+  const uint32_t i0 = piece * a.piece, i1 = min(i0 + a.piece, a.tokens), n = i1 - i0;
+  // key_s[0]: the key before the piece, then the piece, then the key after it
+  // (no row: beyond every key)
+  if (tid < n) {
+    key_s[tid + 1] = __ldcg(a.key + i0 + tid);
+    tok_s[tid] = __ldcg(a.tok + i0 + tid);
+  }
+  if (tid == 32) key_s[0] = i0 ? __ldcg(a.key + i0 - 1) : 0xFFFFFFFFu;
+  if (tid == 33) key_s[n + 1] = i1 < a.tokens ? __ldcg(a.key + i1) : 0xFFFFFFFFu;
+  __syncthreads();
+  const uint32_t col = (ct * kRunThreads + tid) * V;
+  if (col >= a.dim) return;
+  const G *g = static_cast<const G *>(a.grad) + col;
+  float acc[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) acc[j] = 0.f;
+  uint32_t run = 0;  // where the current run begins in the piece
+  constexpr uint32_t kAhead = 4;
+  for (uint32_t i = 0; i < n; i += kAhead) {
+    float v[kAhead][V];
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u)
+      if (i + u < n && key_s[i + u + 1] < a.rows)
+        Row<G, V>::load(g + (size_t)tok_s[i + u] * a.grad_stride, v[u]);
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u) {
+      if (i + u >= n) break;
+      const uint32_t key = key_s[i + u + 1];
+      if (key >= a.rows) break;  // ids outside the table, at the list's end
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] += v[u][j];
+      const bool last = i + u + 1 == n;
+      if (key_s[i + u + 2] == key && !last) continue;
+      const bool before = run == 0 && key_s[0] == key;
+      const bool after = last && key_s[n + 1] == key;
+      if (!before && !after) write_row<O, V>(a, key, col, acc);
+      else write_part<V>((before ? a.head : a.tail) + (size_t)piece * a.part_stride + col, acc);
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] = 0.f;
+      run = i + u + 1;
+    }
+  }
+}
+
+// A run that crosses pieces, by the piece where it begins: its tail there and
+// the heads of the pieces after it, in order.
+template <typename O, int V>
+__global__ void __launch_bounds__(kRunThreads) embedding_join_kernel(const __grid_constant__ RunArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint32_t piece = blockIdx.x / a.col_tiles, ct = blockIdx.x - piece * a.col_tiles;
+  const uint32_t i0 = piece * a.piece, i1 = i0 + a.piece;
+  if (i1 >= a.tokens) return;
+  const uint32_t key = __ldcg(a.key + i1 - 1);
+  if (key >= a.rows || __ldcg(a.key + i1) != key) return;
+  // begun before this piece: another thread block's
+  if (i0 && __ldcg(a.key + i0 - 1) == key) return;
+  uint32_t lo = i1, hi = a.tokens;  // the run's end: the first larger key
+  while (lo < hi) {
+    const uint32_t mid = lo + ((hi - lo) >> 1);
+    if (__ldcg(a.key + mid) == key) lo = mid + 1;
+    else hi = mid;
+  }
+  const uint32_t last = (lo - 1) / a.piece;
+  const uint32_t col = (ct * kRunThreads + threadIdx.x) * V;
+  if (col >= a.dim) return;
+  float s[V];
+  auto load = [&](const float *p, float (&v)[V]) {
+    if constexpr (V == 1) {
+      v[0] = __ldcg(p);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const float4 q = __ldcg(reinterpret_cast<const float4 *>(p + j));
+        v[j] = q.x; v[j + 1] = q.y; v[j + 2] = q.z; v[j + 3] = q.w;
+      }
+    }
+  };
+  load(a.tail + (size_t)piece * a.part_stride + col, s);
+  constexpr uint32_t kAhead = 4;
+  for (uint32_t p = piece + 1; p <= last; p += kAhead) {
+    float v[kAhead][V];
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u)
+      if (p + u <= last) load(a.head + (size_t)(p + u) * a.part_stride + col, v[u]);
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u)
+      if (p + u <= last) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] += v[u][j];
+      }
+  }
+  write_row<O, V>(a, key, col, s);
+}
+
+// ---- host side --------------------------------------------------------------------
+
+uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
+bool known_type(int32_t t) { return t == DF11_BF16 || t == DF11_F32; }
+uintptr_t type_bytes(int32_t t) { return t == DF11_F32 ? 4 : 2; }
+
+template <int C>
+df11_status launch_embedding(EmbedArgs &a, size_t smem, int instance, cudaStream_t s) {
+  auto kern = df11_embedding_kernel<C>;
+  uint64_t budget = 0;
+  const df11_status st = prepare(kern, kWarps * 32, smem, instance, budget);
+  if (st != DF11_OK) return st;
+  const uint64_t items = (uint64_t)a.tokens * a.segs;
+  return launch_pdl(kern, dim3((uint32_t)(items < budget ? items : budget)), kWarps * 32, smem, s, a);
+}
+
+struct GradPlan {
+  uint32_t piece, pieces, col_tiles, part_stride, passes, digit_bits, words;
+  uint64_t key[2], tok[2], touched, head, tail, bytes;
+  int v;  // columns per thread
+};
+
+// 16-byte accesses of gradients and table rows, when every row starts on such a
+// boundary and holds whole ones
+int columns_per_thread(const df11_embedding_grad &op) {
+  const uintptr_t gb = type_bytes(op.grad_type), ob = type_bytes(op.out_type);
+  const uint32_t v = (uint32_t)(16 / gb);
+  const bool ok = op.dim % 8 == 0 && aligned(op.grad, 16) && aligned(op.out, 16) &&
+                  op.grad_stride * gb % 16 == 0 && op.out_stride * ob % 16 == 0;
+  return ok ? (int)v : 1;
+}
+
+GradPlan grad_plan(const df11_embedding_grad &op) {
+  GradPlan p{};
+  p.v = columns_per_thread(op);
+  p.col_tiles = (uint32_t)((op.dim + kRunThreads * p.v - 1) / (kRunThreads * p.v));
+  // pieces of 32 tokens, shorter ones while that leaves SMs without work
+  p.piece = kMaxPiece;
+  while (p.piece > 4 && (uint64_t)op.tokens * p.col_tiles / p.piece < 592) p.piece /= 2;
+  p.pieces = (op.tokens + p.piece - 1) / p.piece;
+  p.part_stride = (uint32_t)round_up(op.dim, 8);
+  uint32_t bits = 1;
+  while ((op.rows >> bits) != 0) ++bits;  // keys 0 .. rows
+  p.passes = (bits + 7) / 8;
+  p.digit_bits = (bits + p.passes - 1) / p.passes;
+  p.words = (op.rows + 31) / 32;
+  uint64_t off = 0;
+  auto take = [&](uint64_t bytes) {
+    const uint64_t at = off;
+    off += round_up(bytes, 256);
+    return at;
+  };
+  for (int i = 0; i < 2; ++i) {
+    p.key[i] = take(4ull * op.tokens);
+    p.tok[i] = take(4ull * op.tokens);
+  }
+  p.touched = take(4ull * p.words);
+  p.head = take(4ull * p.pieces * p.part_stride);
+  p.tail = take(4ull * p.pieces * p.part_stride);
+  p.bytes = off;
+  return p;
+}
+
+df11_status check_grad(const df11_embedding_grad *op) {
+  if (!op) return DF11_ERR_NULL;
+  if (!known_type(op->grad_type) || !known_type(op->out_type) ||
+      (op->ids_type != DF11_IDS_I32 && op->ids_type != DF11_IDS_I64))
+    return DF11_ERR_INVALID;
+  if (op->rows == 0 || op->dim == 0) return DF11_ERR_INVALID;
+  if (op->rows >= (1u << 31) || op->tokens >= (1u << 31)) return DF11_ERR_TOO_LARGE;
+  if (op->out_stride < op->dim || (op->tokens && op->grad_stride < op->dim)) return DF11_ERR_INVALID;
+  if (!op->out || (op->tokens && (!op->ids || !op->grad))) return DF11_ERR_NULL;
+  if (!aligned(op->ids, op->ids_type == DF11_IDS_I64 ? 8 : 4) ||
+      !aligned(op->grad, type_bytes(op->grad_type)) || !aligned(op->out, type_bytes(op->out_type)))
+    return DF11_ERR_ALIGN;
+  return DF11_OK;
+}
+
+template <typename G, typename O, int V>
+df11_status launch_runs(const RunArgs &a, uint32_t zero_blocks, cudaStream_t s) {
+  const uint32_t runs = a.pieces * a.col_tiles;
+  if (runs + zero_blocks == 0) return DF11_OK;
+  df11_status st = launch_pdl(embedding_runs_kernel<G, O, V>, dim3(runs + zero_blocks), kRunThreads,
+                              0, s, a);
+  if (st != DF11_OK || a.pieces < 2) return st;
+  return launch_pdl(embedding_join_kernel<O, V>, dim3(runs), kRunThreads, 0, s, a);
+}
+
+template <typename O>
+df11_status launch_runs_for(const RunArgs &a, bool grad_f32, bool vec, uint32_t zero_blocks,
+                            cudaStream_t s) {
+  if (grad_f32)
+    return vec ? launch_runs<float, O, 4>(a, zero_blocks, s) : launch_runs<float, O, 1>(a, zero_blocks, s);
+  return vec ? launch_runs<uint16_t, O, 8>(a, zero_blocks, s)
+             : launch_runs<uint16_t, O, 1>(a, zero_blocks, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+df11_status df11_decode_embedding(const df11_tensor *table, const df11_embedding *op,
+                                  int32_t *d_err, df11_stream_t stream) {
+  if (!table || !op) return DF11_ERR_NULL;
+  const df11_params &p = table->params;
+  if (!known_type(op->out_type) || (op->ids_type != DF11_IDS_I32 && op->ids_type != DF11_IDS_I64))
+    return DF11_ERR_INVALID;
+  if (p.n >= (1ull << 32)) return DF11_ERR_TOO_LARGE;
+  if (op->rows == 0 || op->dim == 0 || (uint64_t)op->rows * op->dim != p.n) return DF11_ERR_INVALID;
+  if (op->tokens >= (1u << 31)) return DF11_ERR_TOO_LARGE;
+  if (d_err && !aligned(d_err, 4)) return DF11_ERR_ALIGN;
+  if (op->tokens == 0) return DF11_OK;
+  if (!op->ids || !op->out) return DF11_ERR_NULL;
+  if (op->out_stride < op->dim) return DF11_ERR_INVALID;
+  if (!aligned(op->ids, op->ids_type == DF11_IDS_I64 ? 8 : 4) ||
+      !aligned(op->out, type_bytes(op->out_type)))
+    return DF11_ERR_ALIGN;
+  df11_tensor v = *table;
+  v.out_bf16 = reinterpret_cast<uint16_t *>(16);  // not written; passes the output checks
+  df11_status st = validate(v);
+  if (st != DF11_OK) return st;
+  if (!table->chunk_counts || !table->decode_table || p.threads_per_block != kT ||
+      (p.chunk_bytes != 8 && p.chunk_bytes != 16 && p.chunk_bytes != 24))
+    return DF11_ERR_UNSUPPORTED;
+  const void *ptrs[] = {table->bitstream, table->sign_mantissa, table->decode_table, op->ids, op->out};
+  st = check_device_pointers(ptrs, 5);
+  if (st != DF11_OK) return st;
+  EmbedArgs a{};
+  fill_tensor(a.k, *table);
+  a.ids = op->ids;
+  a.out = op->out;
+  a.err = d_err;
+  a.out_stride = op->out_stride;
+  a.tokens = op->tokens;
+  a.rows = op->rows;
+  a.dim = op->dim;
+  a.ids64 = op->ids_type == DF11_IDS_I64;
+  a.out_f32 = op->out_type == DF11_F32;
+  a.scaled = op->scale != 1.0f;
+  a.scale = op->scale;
+  a.vec = op->dim % 16 == 0 && aligned(op->out, 16) &&
+          op->out_stride * type_bytes(op->out_type) % 16 == 0;
+  a.spin_limit = kSpinLimit;
+  // segments of a row that 32 chunks hold on average (30, since a row begins
+  // and ends inside a chunk), in whole 16-element groups
+  const uint64_t per_pass = 30 * p.n / ((uint64_t)p.num_blocks * kT) + 1;
+  const uint64_t segs = (op->dim + per_pass - 1) / per_pass;
+  a.seg_len = (uint32_t)round_up((op->dim + segs - 1) / segs, 16);
+  a.segs = (op->dim + a.seg_len - 1) / a.seg_len;
+  // 32 chunks from any chunk on: first element's offset, elements, the walk's slack
+  a.region_bytes = (uint32_t)round_up(15 + 32ull * p.max_chunk_elems + 8, 16);
+  const size_t smem = kOffStages + (size_t)kWarps * a.region_bytes;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (p.chunk_bytes == 24) return launch_embedding<24>(a, smem, 78, s);
+  if (p.chunk_bytes == 16) return launch_embedding<16>(a, smem, 79, s);
+  return launch_embedding<8>(a, smem, 80, s);
+}
+
+df11_status df11_embedding_gradient_workspace(const df11_embedding_grad *op, size_t *bytes) {
+  if (!bytes) return DF11_ERR_NULL;
+  *bytes = 0;
+  const df11_status st = check_grad(op);
+  if (st == DF11_OK) *bytes = grad_plan(*op).bytes;
+  return st;
+}
+
+df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspace,
+                                    size_t workspace_bytes, int32_t *d_err, df11_stream_t stream) {
+  df11_status st = check_grad(op);
+  if (st != DF11_OK) return st;
+  if (d_err && !aligned(d_err, 4)) return DF11_ERR_ALIGN;
+  const GradPlan p = grad_plan(*op);
+  if (!workspace) return DF11_ERR_NULL;
+  if (!aligned(workspace, 256)) return DF11_ERR_ALIGN;
+  if (workspace_bytes < p.bytes) return DF11_ERR_INVALID;
+  const void *ptrs[] = {op->ids, op->grad, op->out, workspace};
+  st = check_device_pointers(ptrs, 4);
+  if (st != DF11_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  SortArgs so{};
+  so.ids = op->ids;
+  for (int i = 0; i < 2; ++i) {
+    so.key[i] = reinterpret_cast<uint32_t *>(ws + p.key[i]);
+    so.tok[i] = reinterpret_cast<uint32_t *>(ws + p.tok[i]);
+  }
+  so.touched = op->accumulate ? nullptr : reinterpret_cast<uint32_t *>(ws + p.touched);
+  so.err = d_err;
+  so.tokens = op->tokens;
+  so.rows = op->rows;
+  so.passes = p.passes;
+  so.digit_bits = p.digit_bits;
+  so.touched_words = p.words;
+  so.ids64 = op->ids_type == DF11_IDS_I64;
+  // one thread block per 4096 tokens, up to a cluster of eight
+  uint32_t ctas = 1;
+  while (ctas < 8 && (uint64_t)ctas * 4096 < op->tokens) ctas *= 2;
+  st = launch_cluster(embedding_sort_kernel, ctas, kSortThreads, s, so);
+  if (st != DF11_OK) return st;
+  RunArgs r{};
+  r.grad = op->grad;
+  r.out = op->out;
+  r.key = so.key[p.passes & 1];
+  r.tok = so.tok[p.passes & 1];
+  r.touched = so.touched;
+  r.head = reinterpret_cast<float *>(ws + p.head);
+  r.tail = reinterpret_cast<float *>(ws + p.tail);
+  r.grad_stride = op->grad_stride;
+  r.out_stride = op->out_stride;
+  r.tokens = op->tokens;
+  r.rows = op->rows;
+  r.dim = op->dim;
+  r.piece = p.piece;
+  r.pieces = p.pieces;
+  r.col_tiles = p.col_tiles;
+  r.part_stride = p.part_stride;
+  r.accumulate = op->accumulate ? 1 : 0;
+  r.scale = op->scale;
+  const uint32_t zero_blocks = op->accumulate ? 0 : p.words;
+  const bool gf = op->grad_type == DF11_F32, vec = p.v > 1;
+  return op->out_type == DF11_F32 ? launch_runs_for<float>(r, gf, vec, zero_blocks, s)
+                                  : launch_runs_for<uint16_t>(r, gf, vec, zero_blocks, s);
+}
+
+}  // extern "C"

@@ -55,7 +55,7 @@ inline df11_status validate(const df11_tensor &t) {
 // kernels use 3 * i + mode with i = 3-8 (decode with counts), 12-14 (fused
 // matrix-vector product) and 15-20 (decode without counts); the
 // tensor-core product 64-65.
-constexpr int kInstances = 80;
+constexpr int kInstances = 96;
 struct DeviceInfo {
   int sms = 0;
   std::atomic<size_t> configured[kInstances];  // shared-memory limit set, per kernel instance
@@ -132,6 +132,25 @@ df11_status launch_pdl(void (*kern)(Args...), dim3 grid, uint32_t threads, size_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DF11_OK : DF11_ERR_CUDA;
+}
+
+// The same for a grid that is one cluster of `ctas` thread blocks (at most 8).
+template <typename... Args>
+df11_status launch_cluster(void (*kern)(Args...), uint32_t ctas, uint32_t threads, cudaStream_t s,
+                           Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DF11_OK : DF11_ERR_CUDA;
 }
 

@@ -977,26 +977,6 @@ df11_status for_groups(const df11_tensor *tensors, const df11_linear *ops, int c
   return DF11_OK;
 }
 
-void fill_tensor(KTensor &k, const df11_tensor &t) {
-  const df11_params &p = t.params;
-  k.bitstream = t.bitstream;
-  k.gaps = t.gaps;
-  k.chunk_counts = t.chunk_counts;
-  k.block_out_pos = t.block_out_pos;
-  k.luts = t.luts;
-  k.code_lengths = t.code_lengths;
-  k.sign_mantissa = t.sign_mantissa;
-  k.decode_table = t.decode_table;
-  k.total_bits = p.total_bits;
-  k.n = (uint32_t)p.n;
-  k.num_blocks = p.num_blocks;
-  k.num_luts = p.num_luts;
-  k.max_block_elems = p.max_block_elems;
-  k.max_chunk_elems = p.max_chunk_elems;
-  k.max_warp_elems = p.max_warp_elems;
-  k.masked = p.max_len > (uint32_t)kWideBits ? 1u : 0u;
-}
-
 df11_status launch_fused(const df11_tensor *ts, const df11_linear *ops, int count, const Plan &pl,
                          uint8_t *ws, const uint16_t *const *x, const uint32_t *x_stride,
                          const uint32_t *x_cols, int32_t *d_err, cudaStream_t s) {

@@ -93,6 +93,7 @@ typedef enum df11_status {
                                    did not complete in time */
 #define DF11_DEV_ERR_CAPACITY 5 /* a block holds more elements than
                                    max_block_elems */
+#define DF11_DEV_ERR_INDEX 6    /* a token id outside the embedding table */
 
 /* Largest number of tensors one df11_decode_batched launch takes. */
 #define DF11_MAX_BATCH 16
@@ -313,6 +314,68 @@ df11_status df11_decode_linear(const df11_tensor *tensors, const df11_linear *op
  * pointers are checked as in the call, but nothing is queued). */
 df11_status df11_linear_workspace(const df11_tensor *tensors, const df11_linear *ops, int count,
                                   size_t *bytes);
+
+/* ---------------------------------------------------------------------- */
+/* The token embedding on a compressed table, and the table's gradient.    */
+
+/* Types of token ids. */
+#define DF11_IDS_I32 0
+#define DF11_IDS_I64 1
+
+/* out[t][c] = scale * W[ids[t]][c]. */
+typedef struct df11_embedding {
+  const void *ids;     /* `tokens` ids of ids_type, each 0 .. rows - 1 */
+  void *out;           /* `tokens` rows of `dim` elements of out_type */
+  uint64_t out_stride; /* elements between output rows: >= dim */
+  uint32_t rows, dim;  /* of the table: rows * dim == n */
+  uint32_t tokens;     /* 0 .. 2^31 - 1 */
+  int32_t ids_type;    /* DF11_IDS_I32 or DF11_IDS_I64 */
+  int32_t out_type;    /* DF11_BF16 or DF11_F32 */
+  float scale;
+} df11_embedding;
+
+/*
+ * Rows of a compressed table (row-major: an ordinary df11_build tensor), without
+ * decoding the rest of it.  With scale 1 and BF16 outputs the words come back as they
+ * were encoded; otherwise a value is widened, multiplied in fp32 and rounded
+ * once.  An id outside the table gives a row of zeros and DF11_DEV_ERR_INDEX in
+ * d_err.  Needs chunk counts, a decode table, T = 256 and C = 8, 16 or 24;
+ * out_bf16 of the tensor is not used (may be NULL).  Same conventions as
+ * df11_decode_batched otherwise; the ids may be written by the previous kernel in
+ * the stream.
+ */
+df11_status df11_decode_embedding(const df11_tensor *table, const df11_embedding *op,
+                                  int32_t *d_err, df11_stream_t stream);
+
+/* out[v][c] (+)= scale * sum over the tokens t with ids[t] == v of grad[t][c]. */
+typedef struct df11_embedding_grad {
+  const void *ids;      /* `tokens` ids of ids_type */
+  const void *grad;     /* `tokens` rows of `dim` elements of grad_type */
+  void *out;            /* `rows` rows of `dim` elements of out_type */
+  uint64_t grad_stride, out_stride; /* elements between rows: >= dim */
+  uint32_t rows, dim;
+  uint32_t tokens;      /* 0 .. 2^31 - 1 */
+  int32_t ids_type, grad_type, out_type;
+  int32_t accumulate;   /* 0: every row of out is written, zeros where no token is;
+                           otherwise only the rows that have tokens, added to */
+  float scale;
+} df11_embedding_grad;
+
+/*
+ * The gradient of df11_decode_embedding's table, dense.  Tokens are sorted by id
+ * (stably) and each row's gradients summed in fp32 in an order that the sizes fix;
+ * the sum is scaled, added to what is there when accumulating, and rounded once:
+ * a call repeats bit for bit.  An id outside the table adds nothing and sets
+ * DF11_DEV_ERR_INDEX.  `workspace`: df11_embedding_gradient_workspace bytes of
+ * device memory, 256-byte aligned, that no other work uses until this call's
+ * work is done.  Asynchronous, no allocation, three launches.
+ */
+df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspace,
+                                    size_t workspace_bytes, int32_t *d_err, df11_stream_t stream);
+
+/* Bytes of workspace that df11_embedding_gradient needs (arguments are checked as in
+ * the call; host only). */
+df11_status df11_embedding_gradient_workspace(const df11_embedding_grad *op, size_t *bytes);
 
 /*
  * Derive, on the device, the decode table of one tensor from its luts and
