@@ -160,6 +160,14 @@ def lib():
     L.df11_decode_linear.restype = ctypes.c_int
     L.df11_linear_workspace.argtypes = [vp, vp, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
     L.df11_linear_workspace.restype = ctypes.c_int
+    L.df11_linear_sizes.argtypes = [u32, u32, ctypes.POINTER(u64), ctypes.POINTER(u64)]
+    L.df11_linear_sizes.restype = ctypes.c_int
+    L.df11_linear_weight_begin.argtypes = [vp, u32, u32, vp, vp, vp, vp]
+    L.df11_linear_weight_begin.restype = ctypes.c_int
+    L.df11_linear_weight_finish.argtypes = [vp, vp, vp]
+    L.df11_linear_weight_finish.restype = ctypes.c_int
+    L.df11_linear_unpack.argtypes = [vp, vp, vp, vp]
+    L.df11_linear_unpack.restype = ctypes.c_int
     L.df11_decode_embedding.argtypes = [vp, vp, vp, vp]
     L.df11_decode_embedding.restype = ctypes.c_int
     L.df11_embedding_gradient.argtypes = [vp, vp, ctypes.c_size_t, vp, vp]
@@ -199,8 +207,7 @@ class Df11Host:
     sign_mantissa: np.ndarray  # uint8 (n rounded up to 16)
     chunk_counts: np.ndarray   # uint8, codewords starting in each chunk
     shape: tuple = ()
-    interleave: int = 1        # rows interleaved per 16 columns in the stream (1: row-major;
-                               # LINEAR_TILES: the linear product's tiles)
+    interleave: int = 1        # rows interleaved per 16 columns in the stream (1: row-major)
 
     @property
     def n(self) -> int:
@@ -312,9 +319,7 @@ class Df11Device:
     chunk_counts: Optional[torch.Tensor] = None
     shape: tuple = ()
     decode_table: Optional[torch.Tensor] = None  # df11_build_decode_table output
-    # rows interleaved per 16 columns in the stream (1: row-major; LINEAR_TILES:
-    # the linear product's tiles)
-    interleave: int = 1
+    interleave: int = 1  # rows interleaved per 16 columns in the stream (1: row-major)
 
     @classmethod
     def _in_block(cls, params: Params, block: torch.Tensor, offs: tuple, sizes: tuple,
@@ -730,7 +735,7 @@ def check_device_error(err: torch.Tensor):
         raise Df11Error(f"decode reported {DEV_ERRORS.get(code, code)}: {msg}")
 
 
-from .linear import (LINEAR_TILES, LinearOp, LinearPlan, compress_linear,  # noqa: E402,F401
-                     decode_linear, tile_linear, untile_linear)
+from .linear import (LinearOp, LinearParams, LinearPlan, LinearWeight,  # noqa: E402,F401
+                     LinearWeightDesc, compress_linear, decode_linear, decode_weight)
 from .embedding import (EmbeddingGradOp, EmbeddingOp, EmbeddingPlan,  # noqa: E402,F401
                         decode_embedding, embedding_gradient)

@@ -1,30 +1,35 @@
 // df11_linear.cu -- the linear product of a model's layer on compressed weights:
 // y = act(W x + bias) * multiplier + residual, for any number of tokens.
 //
-// The weight is encoded in the tile order of this product: for each block of
-// 16 rows and each group of 64 columns, the 16 rows' 64 elements one after
-// another (rows and columns padded with zeros to whole tiles).  A tile is 64
-// groups of 16 elements, and lane l of a warp that takes groups l and l + 32 of
-// a tile holds, for rows l/4 and l/4 + 8, the 16 columns 16 (l mod 4) .. + 15:
-// the A fragments of four m16n8k16 products, with no exchange between lanes
-// and without a bank conflict on the way.
+// The weight has a compressed form of its own (df11_linear_weight_begin), with the same
+// code as the decode kernels' format (a Huffman code of the exponents, sign and mantissa
+// kept as a byte), but cut by elements instead of bits.  The matrix, padded with zeros
+// to whole tiles of 16 rows and 64 columns, is taken in units of up to four tiles along a
+// block of 16 rows.  One warp decodes a unit: lane l has a bitstream of its own
+// with the 32 elements of every tile that belong to it, rows l/4 and l/4 + 8 and the 16
+// columns from 16 (l mod 4) on.  Those are the A fragments of four m16n8k16 products,
+// so a decoded weight goes from the table to the tensor core in registers: no
+// chunk counts, scans, shared-memory exponents or exchange between lanes.  The
+// lanes' streams of a unit are stored word by word across the lanes, each padded to the
+// longest of the 32 (about 0.3 bits per weight; chunk counts and gaps cost 0.2).
 //
 // Two paths, chosen by the number of tokens (see kFusedMax):
-//   few tokens    one kernel decodes the weight and multiplies it from
-//                 registers; the warps' sums over their parts of a row block go
-//                 to a workspace, and a second kernel adds them in a fixed order
-//                 and applies the epilogue.
-//   more tokens   the weight is decoded into the workspace by the decode kernel
-//                 and multiplied by a tcgen05 kernel with the epilogue on its
-//                 accumulators.
-// Every sum runs in fp32 in an order that the sizes and the device fix, so a
-// call repeats bit for bit.  The result is rounded once, to the output's type.
+//   few tokens    one kernel decodes the weight and multiplies it from registers; the
+//                 warps' sums over their parts of a row block go to a workspace, and a
+//                 second kernel adds them in a fixed order and applies the epilogue.
+//   more tokens   the weight is decoded into the workspace and multiplied by a
+//                 tcgen05 kernel with the epilogue on its accumulators.
+// Every sum runs in fp32 in an order that the sizes and the device fix, so a call
+// repeats bit for bit.  The result is rounded once, to the output's type.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
+#include <vector>
 
 #include "df11.h"
+#include "df11_codebook.h"
 #include "df11_device.cuh"
 #include "df11_device_check.h"
 #include "df11_launch.h"
@@ -33,9 +38,37 @@ using namespace df11_internal;
 
 namespace {
 
-constexpr int kT = 256;            // chunks per format block
-constexpr int kWarps = kT / 32;    // consumer warps of the fused kernel
 constexpr uint32_t kTileRows = 16, kTileCols = 64, kTileElems = kTileRows * kTileCols;
+constexpr uint32_t kMaxUnitTiles = 4;
+constexpr int kWarps = 16;  // warps of a thread block: a group of 16 row blocks, one each
+constexpr int kThreads = 32 * kWarps;
+// Longest stream of a lane in a unit, in words, before the builder takes shorter
+// units: two units per warp are in shared memory (16 warps: 160 KB at most).
+constexpr uint32_t kMaxWords = 40;
+
+// ---- the decode table -----------------------------------------------------------
+//
+// Pair table, indexed by the next kPairBits bits: two codewords when both lie inside
+// (bits 0-4 their length together, bits 8-15 and 16-23 the exponents, rotated right by
+// one bit, bits 24-28 the first one's length); bit 31 alone: only the first one does;
+// bits 31 and 30: not even that.  After it, for those, the canonical code: per length
+// 1 .. 32 the first codeword, the count and the index of its first symbol, and the
+// symbols (rotated) in code order; and the code itself, for the builder.
+// Of Gaussian weights 0.4% of the pairs exceed 13 bits (0.7% 12 bits, 0.2% 14 bits).
+constexpr int kPairBits = 13;
+constexpr uint32_t kPairs = 1u << kPairBits;
+struct LinearTable {
+  uint32_t pair[kPairs];
+  uint32_t first[33];
+  uint32_t range[33];  // count << 16 | index of the first symbol
+  uint32_t pad[2];
+  uint8_t sym[256];
+  uint32_t code[256];    // by exponent: the codeword, left-aligned, and its length
+  uint32_t length[256];  // (for the builder)
+};
+static_assert(sizeof(LinearTable) == DF11_LINEAR_TABLE_BYTES, "table layout");
+
+constexpr uint32_t kBothFlag = 0x80000000u, kDeepFlag = 0x40000000u;
 
 // ---- epilogue ---------------------------------------------------------------
 
@@ -122,13 +155,273 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant_
   }
 }
 
-// ---- few tokens: decode and multiply in one kernel ----------------------------
+// ---- one lane's stream -------------------------------------------------------------
+
+struct LWeight {
+  const uint32_t *streams;        // rows of 32 words
+  const uint32_t *unit_rows;      // first row of each unit
+  const uint8_t *sign_mantissa;   // per tile: rows 0-7 (16 bytes per lane), rows 8-15
+  const LinearTable *table;
+  uint32_t rbs, ncg;              // row blocks, tiles per row block
+  uint32_t unit_tiles, upr;       // tiles per unit, units per row block
+  uint32_t max_words, stream_rows;
+};
+
+// Two words of the lane's stream with the next bit at bit 31 - (p & 31) of `a`, and
+// where the word after them is.  Bit 5 of p is zero between steps; the bits above it
+// are not kept clean.
+struct LaneBits {
+  uint32_t a, b, p, addr;
+  __device__ __forceinline__ void refill() {
+    a = b;
+    b = lds32(addr);
+    addr += 128u;
+  }
+};
+
+// A codeword longer than the pair table's index: canonical search by length.
+// No match (inconsistent data): length 1, and bit 31 set in the result.
+__device__ __noinline__ uint32_t deep_symbol(uint32_t win, const LinearTable *t) {
+  for (uint32_t len = kPairBits + 1; len <= 32; ++len) {
+    const uint32_t k = (win >> (32 - len)) - __ldg(t->first + len), r = __ldg(t->range + len);
+    if (k < (r >> 16)) return (uint32_t)__ldg(t->sym + (((r & 0xFFFFu) + k) & 255u)) | len << 8;
+  }
+  return 0x80000100u;
+}
+
+// Two symbols one after another, where the pair table has not both: the state moves on
+// past them, and the result has the pair's exponents with a length of zero.
+__device__ __forceinline__ uint32_t slow_pair(LaneBits &s, uint32_t pairs, const LinearTable *t,
+                                              uint32_t &bad) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t win = __funnelshift_l(s.b, s.a, s.p);
+    const uint32_t e = lds32(pairs + ((win >> (32 - kPairBits)) << 2));
+    uint32_t sym = (e >> 8) & 0xFFu, len = (e >> 24) & 31u;
+    if (e >= (kBothFlag | kDeepFlag)) {
+      const uint32_t d = deep_symbol(win, t);
+      bad |= d >> 31;
+      sym = d & 0xFFu;
+      len = (d >> 8) & 63u;
+    }
+    r |= sym << (8 * i + 8);
+    s.p = (s.p & 31u) + len;
+    if (s.p & 32u) {
+      s.refill();
+      s.p ^= 32u;
+    }
+  }
+  return r;
+}
+
+// The next four exponents (rotated), first in bits 0-7.  One 32-bit window serves both
+// lookups: two pairs take at most 26 bits.
+__device__ __forceinline__ uint32_t next4(LaneBits &s, uint32_t pairs, const LinearTable *t,
+                                          uint32_t &bad) {
+  const uint32_t w = __funnelshift_l(s.b, s.a, s.p);
+  uint32_t e1 = lds32(pairs + ((w >> (32 - kPairBits)) << 2));
+  uint32_t w2 = __funnelshift_l(0u, w, e1);  // shifts by the low five bits: the length
+  if ((int32_t)e1 < 0) {
+    e1 = slow_pair(s, pairs, t, bad);
+    w2 = __funnelshift_l(s.b, s.a, s.p);
+  }
+  uint32_t e2 = lds32(pairs + ((w2 >> (32 - kPairBits)) << 2));
+  if ((int32_t)e2 < 0) {
+    s.p = (s.p & 31u) + (e1 & 31u);
+    if (s.p & 32u) {
+      s.refill();
+      s.p ^= 32u;
+    }
+    e1 &= ~31u;
+    e2 = slow_pair(s, pairs, t, bad);
+  }
+  s.p += e1 + e2;
+  if (s.p & 32u) {
+    s.refill();
+    s.p ^= 32u;
+  }
+  return __byte_perm(e1, e2, 0x6521);
+}
+
+// A unit's streams from global memory into the warp's buffer `dst` (max_words rows);
+// false if the table of rows is inconsistent.
+__device__ __forceinline__ bool fetch_unit(const LWeight &w, uint32_t unit, uint32_t dst,
+                                           uint32_t bar) {
+  const uint32_t r0 = __ldg(w.unit_rows + unit), r1 = __ldg(w.unit_rows + unit + 1);
+  if (r1 < r0 || r1 - r0 > w.max_words || r1 > w.stream_rows) return false;
+  mbar_arrive_expect_tx(bar, (r1 - r0) * 128u);
+  if (r1 > r0) bulk_g2s(dst, w.streams + (size_t)r0 * 32u, (r1 - r0) * 128u, bar);
+  return true;
+}
+
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// 16 weights of a lane, two BF16 per word
+__device__ __forceinline__ void next16(LaneBits &s, uint32_t pairs, const LinearTable *t,
+                                       const uint4 &sm, uint32_t (&w)[8], uint32_t &bad) {
+  const uint32_t v[4] = {sm.x, sm.y, sm.z, sm.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint2 f = fuse4(v[j], next4(s, pairs, t, bad));
+    w[2 * j] = f.x;
+    w[2 * j + 1] = f.y;
+  }
+}
+
+// A warp's walk over its units: thread block `cta` of `ctas` has an equal, contiguous
+// share of the units in the order (group of 16 row blocks, unit along the rows, row block
+// of the group), and warp w of it those of the group's row block w.  So the warps of a
+// thread block are at the same columns of x at about the same time.
+struct UnitRange {
+  uint64_t begin, end;
+};
+__device__ __host__ __forceinline__ uint64_t first_unit(uint64_t cta, uint64_t units, uint64_t ctas) {
+  return cta * units / ctas;
+}
+// units in that order, row blocks past the last included
+__device__ __host__ __forceinline__ uint64_t ordered_units(uint32_t rbs, uint32_t upr) {
+  return (uint64_t)((rbs + kWarps - 1) / kWarps) * upr * kWarps;
+}
+
+// Shared memory: barriers (two per warp and the table's), the warps' buffers (two units
+// each), the table.  A lane of an inconsistent stream can run past its buffer by at
+// most 32 bits per symbol, 16 KB in all: less than the table behind the buffers.
+constexpr uint32_t kBarBytes = 384;
+static_assert(kBarBytes >= 8 * (2 * kWarps + 1) && kBarBytes % 128 == 0, "barriers");
+static_assert(4 * kPairs >= 128u * (kMaxUnitTiles * 32u), "overrun stays in the table");
+
+__device__ __host__ constexpr uint32_t decode_smem(uint32_t max_words) {
+  return kBarBytes + kWarps * 2u * max_words * 128u + 4u * kPairs;
+}
+
+// The decoding side of both kernels: `use(rb, cg, w0, w1, slot)` gets every tile of the
+// warp's units in order (w0: rows 0-7, w1: rows 8-15), `moved(group)` every group of
+// row blocks of the thread block's range once the warp's units there are done.
+template <typename Start, typename Use, typename Moved>
+__device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, uint32_t ctas,
+                                             int32_t *err, uint32_t spin_limit, uint8_t *smem,
+                                             Start start, Use use, Moved moved) {
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t bars = smem_addr(smem);
+  const uint32_t tbar = bars + 8u * (2 * kWarps), wbar = bars + 16u * warp;
+  const uint32_t bytes = lw.max_words * 128u;
+  const uint32_t buf = bars + kBarBytes + warp * 2u * bytes;
+  const uint32_t pairs = bars + kBarBytes + kWarps * 2u * bytes;
+  if (tid == 0) {
+    for (uint32_t i = 0; i < 2 * kWarps + 1; ++i) mbar_init(bars + 8u * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  if (tid == 0) {
+    mbar_arrive_expect_tx(tbar, 4u * kPairs);
+    bulk_g2s(pairs, lw.table->pair, 4u * kPairs, tbar);
+  }
+  const uint64_t units = ordered_units(lw.rbs, lw.upr);
+  const uint64_t o0 = first_unit(cta, units, ctas), o1 = first_unit(cta + 1, units, ctas);
+  const uint32_t per_group = lw.upr * kWarps;
+  const uint32_t g0 = (uint32_t)(o0 / per_group), g1 = (uint32_t)((o1 + per_group - 1) / per_group);
+  // this warp's units: steps q = group * upr + (unit along the rows), [q0, q1)
+  const uint64_t q0 = (o0 + kWarps - 1 - warp) / kWarps, q1 = (o1 + kWarps - 1 - warp) / kWarps;
+  uint32_t group = (uint32_t)(q0 / lw.upr), ku = (uint32_t)(q0 - (uint64_t)group * lw.upr);
+  uint32_t fetched_ok = 0;  // bit j & 1: the fetch of step j was made
+  // fetch ahead: the unit `d` steps on from (group, ku); row blocks past the last have none
+  auto fetch = [&](uint64_t j, uint32_t fg, uint32_t fk) {
+    const uint32_t rb = fg * kWarps + warp, i = (uint32_t)j & 1u;
+    bool ok = false;
+    if (rb < lw.rbs) {
+      if (lane == 0) {
+        ok = fetch_unit(lw, rb * lw.upr + fk, buf + i * bytes, wbar + 8u * i);
+        if (!ok) report(err, DF11_DEV_ERR_CAPACITY);
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    }
+    fetched_ok = (fetched_ok & ~(1u << i)) | ((ok ? 1u : 0u) << i);
+  };
+  uint32_t phase = 0;  // bit i: parity of buffer i's next wait
+  uint64_t j = 0;
+  if (q0 < q1) fetch(0, group, ku);
+  bool table = mbar_wait(tbar, 0, spin_limit);
+  if (!__all_sync(0xFFFFFFFFu, table)) {
+    if (lane == 0) report(err, DF11_DEV_ERR_TIMEOUT);
+    table = false;
+  }
+  start();
+  uint32_t done = g0;  // groups handed on
+  uint32_t bad = 0;
+  bool waiting = true;
+  for (uint64_t q = q0; q < q1 && waiting; ++q, ++j) {
+    while (done < group) moved(done++);
+    uint32_t ng = group, nk = ku + 1;
+    if (nk == lw.upr) {
+      nk = 0;
+      ++ng;
+    }
+    const uint32_t i = (uint32_t)j & 1u, rb = group * kWarps + warp;
+    const uint32_t cg0 = ku * lw.unit_tiles, nt = min(lw.unit_tiles, lw.ncg - cg0);
+    const uint8_t *smp = lw.sign_mantissa + ((size_t)rb * lw.ncg + cg0) * kTileElems + 16u * lane;
+    uint4 sm0, sm1;
+    const bool ok = (fetched_ok >> i) & 1u;
+    if (ok) {
+      sm0 = ldg_stream(smp);
+      sm1 = ldg_stream(smp + 512);
+    }
+    // the other buffer: every lane is done with it
+    __syncwarp();
+    if (q + 1 < q1) fetch(j + 1, ng, nk);
+    if (ok) {
+      waiting = __all_sync(0xFFFFFFFFu, mbar_wait(wbar + 8u * i, (phase >> i) & 1u, spin_limit));
+      phase ^= 1u << i;
+      if (!waiting) {
+        if (lane == 0) report(err, DF11_DEV_ERR_TIMEOUT);
+        break;
+      }
+    }
+    if (ok && table) {
+      const uint32_t row0 = buf + i * bytes + 4u * lane;
+      LaneBits s{lds32(row0), lds32(row0 + 128u), 0u, row0 + 256u};
+      for (uint32_t c = 0; c < nt; ++c) {
+        const uint4 v0 = sm0, v1 = sm1;
+        if (c + 1 < nt) {
+          smp += kTileElems;
+          sm0 = ldg_stream(smp);
+          sm1 = ldg_stream(smp + 512);
+        }
+        use.load(cg0 + c);
+        uint32_t w0[8], w1[8];
+        next16(s, pairs, lw.table, v0, w0, bad);
+        next16(s, pairs, lw.table, v1, w1, bad);
+        use(rb, cg0 + c, w0, w1);
+      }
+      // words used: the two in registers were read ahead
+      if ((s.addr - row0 - 256u) / 128u > lw.max_words) bad |= 2u;
+    }
+    group = ng;
+    ku = nk;
+  }
+  while (done < g1) moved(done++);
+  if (bad) report(err, bad & 1u ? DF11_DEV_ERR_TABLE : DF11_DEV_ERR_OVERRUN);
+  // no copy is in flight into this thread block's shared memory when it ends
+  if (!waiting && lane == 0)
+    for (uint32_t i = 0; i < 2; ++i)
+      if ((fetched_ok >> i) & 1u) mbar_wait(wbar + 8u * i, (phase >> i) & 1u, spin_limit);
+}
+
+// ---- few tokens: decode and multiply in one kernel ----------------------------------
 
 struct LTensor {
-  KTensor k;      // decode fields; x, x_stride, batch; cols: the columns that x holds
-  float *part;    // partial sums: [thread block][slot][warp][token][16 rows]
-  uint32_t ncg;   // 64-column groups per row block
-  uint32_t slots; // row blocks that one thread block's range can touch
+  LWeight w;
+  const uint16_t *x;
+  float *part;        // partial sums: [thread block][slot][warp][token][16 rows]
+  uint32_t x_stride, x_cols, batch;  // x_cols: the columns that x holds, a multiple of 16
+  uint32_t slots;     // groups of row blocks that one thread block's range can touch
+  uint32_t cta_begin;
 };
 
 struct LBatch {
@@ -136,13 +429,8 @@ struct LBatch {
   int32_t *err;
   int count;
   uint32_t cta_end;
-  uint32_t region_bytes;  // each warp's exponent region, and its sign/mantissa buffer
   uint32_t spin_limit;
 };
-
-__device__ __forceinline__ uint32_t first_block(uint32_t cta, uint32_t blocks, uint32_t ctas) {
-  return (uint32_t)((uint64_t)cta * blocks / ctas);
-}
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -153,355 +441,285 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// the bytes [lo, hi) of a 16-byte group kept, the others zero
-__device__ __forceinline__ uint4 keep_bytes(uint4 v, uint32_t lo, uint32_t hi) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t m = 0xFFFFFFFFu;
-    if (lo > 4u * j) m = lo >= 4u * j + 4u ? 0u : m << (8u * (lo - 4u * j));
-    if (hi < 4u * j + 4u) m = hi <= 4u * j ? 0u : m & (0xFFFFFFFFu >> (8u * (4u * j + 4u - hi)));
-    w[j] &= m;
+// The products of a tile: x as B fragments, token 8 j + lane / 4 and the lane's 16 columns
+template <int NB>
+struct Multiply {
+  const LTensor &lt;
+  float (&acc)[NB][4];
+  uint4 x0, x1;
+  const uint32_t g = (threadIdx.x & 31u) >> 2, c = 16u * (threadIdx.x & 3u);
+  __device__ __forceinline__ void load_x(uint32_t j, uint32_t cg) {
+    const uint32_t n = 8u * j + g, col = cg * kTileCols + c;
+    x0 = x1 = make_uint4(0, 0, 0, 0);
+    if (n < lt.batch && col < lt.x_cols) {
+      const uint4 *p = reinterpret_cast<const uint4 *>(lt.x + (size_t)n * lt.x_stride + col);
+      x0 = __ldg(p);
+      x1 = __ldg(p + 1);
+    }
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+  __device__ __forceinline__ void load(uint32_t cg) { load_x(0, cg); }
+  __device__ __forceinline__ void operator()(uint32_t, uint32_t cg, const uint32_t (&w0)[8],
+                                             const uint32_t (&w1)[8]) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      mma_bf16(acc[j], w0[0], w1[0], w0[1], w1[1], x0.x, x0.y);
+      mma_bf16(acc[j], w0[2], w1[2], w0[3], w1[3], x0.z, x0.w);
+      mma_bf16(acc[j], w0[4], w1[4], w0[5], w1[5], x1.x, x1.y);
+      mma_bf16(acc[j], w0[6], w1[6], w0[7], w1[7], x1.z, x1.w);
+      if (j + 1 < NB) load_x(j + 1, cg);
+    }
+  }
+};
 
-// One thread block decodes a contiguous range of one tensor's format blocks
-// with the decode kernel's warps (a producer warp that stages blocks, eight
-// consumer warps that each walk 32 chunks into their own exponent region), and
-// each consumer warp multiplies the groups of its part straight from
-// registers: 4 m16n8k16 products per tile and 8 tokens.  A warp's sums are for
-// one block of 16 rows at a time; when its range leaves a row block it writes
-// them to the block's slot of the workspace.
-template <int C, int NB>
-__global__ void __launch_bounds__(kT + 32, NB > 2 ? 2 : 3)
+template <int NB>
+__global__ void __launch_bounds__(kThreads, NB > 2 ? 1 : 2)
     df11_linear_kernel(const __grid_constant__ LBatch lb) {
-  using L = WsLayout<kT, C>;
-  constexpr int NW = C / 4 + 1;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem);  // full[2], empty[2], warp[8], table
-  uint8_t *lens_s = smem + kOffLens;
-  uint32_t *lut0_s = reinterpret_cast<uint32_t *>(smem + kOffLut0);
-  uint8_t *stages = smem + kOffStages;
-  uint8_t *regions = stages + kWsStages * L::head_bytes;
-  uint8_t *warp_sm = regions + kWarps * lb.region_bytes;
-
   int ti = 0;
   for (int i = 1; i < lb.count; ++i)
-    if (blockIdx.x >= lb.t[i].k.cta_begin) ti = i;
+    if (blockIdx.x >= lb.t[i].cta_begin) ti = i;
   const LTensor &lt = lb.t[ti];
-  const KTensor &tk = lt.k;
-  const uint32_t ctas = (ti + 1 < lb.count ? lb.t[ti + 1].k.cta_begin : lb.cta_end) - tk.cta_begin;
-  const uint32_t cta = blockIdx.x - tk.cta_begin;
-  const uint32_t b0 = first_block(cta, tk.num_blocks, ctas);
-  const uint32_t b1 = first_block(cta + 1, tk.num_blocks, ctas);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-  const uint32_t tbar = smem_addr(&bars[2 * kWsStages + kWarps]);
-  if (tid == 0) {
-    for (int i = 0; i < kWsStages; ++i) {
-      mbar_init(smem_addr(&bars[i]), 1);
-      mbar_init(smem_addr(&bars[kWsStages + i]), kWarps);
-    }
-    for (int i = 0; i < kWarps; ++i) mbar_init(smem_addr(&bars[2 * kWsStages + i]), 1);
-    mbar_init(tbar, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncthreads();
-  uint32_t issued = 0;
-  if (warp == kWarps && lane == 0) {
-    mbar_arrive_expect_tx(tbar, DF11_DECODE_TABLE_BYTES);
-    bulk_g2s(smem_addr(lens_s), tk.decode_table, DF11_DECODE_TABLE_BYTES, tbar);
-    for (uint32_t b = b0; b < b1 && issued < kWsStages; ++b, ++issued)
-      ws_issue<kT, C, kSmWarp, true>(tk, b, stages + issued * L::head_bytes,
-                                     smem_addr(&bars[issued]), 0);
-  }
-  for (uint32_t i = tid; i < kWarps * lb.region_bytes / 16; i += kT + 32)
-    reinterpret_cast<uint4 *>(regions)[i] = make_uint4(0, 0, 0, 0);
-  const bool tables_ok = mbar_wait(tbar, 0, lb.spin_limit);
-  if (!__syncthreads_and(tables_ok)) {
-    if (tid == 0) report(lb.err, DF11_DEV_ERR_TIMEOUT);
-    return;
-  }
-
-  if (warp == kWarps) {  // producer
-    if (lane == 0) {
-      uint32_t k = issued;
-      for (uint32_t b = b0 + issued; b < b1; ++b, ++k) {
-        const uint32_t s = k % kWsStages, par = (k / kWsStages) & 1u;
-        if (!mbar_wait(smem_addr(&bars[kWsStages + s]), par ^ 1u, lb.spin_limit)) {
-          report(lb.err, DF11_DEV_ERR_TIMEOUT);
-          break;
-        }
-        ws_issue<kT, C, kSmWarp, true>(tk, b, stages + s * L::head_bytes, smem_addr(&bars[s]), 0);
-      }
-      pdl_launch_dependents();
-      // no copy in flight into this thread block's shared memory when it ends
-      for (uint32_t j = k > kWsStages ? k - kWsStages : 0; j < k; ++j)
-        if (!mbar_wait(smem_addr(&bars[j % kWsStages]), (j / kWsStages) & 1u, lb.spin_limit))
-          report(lb.err, DF11_DEV_ERR_TIMEOUT);
-    }
-    return;
-  }
-
-  const uint32_t region = smem_addr(regions + warp * lb.region_bytes);
-  uint8_t *region_p = regions + warp * lb.region_bytes;
-  const uint32_t wide = smem_addr(smem + kOffWide);
-  const uint32_t wsm = smem_addr(warp_sm + warp * lb.region_bytes);
-  const uint32_t wbar = smem_addr(&bars[2 * kWsStages + warp]);
-  const uint32_t *sub = tk.luts + 256;
-  // this thread block's row blocks: slots 0 .. last of the workspace
-  const uint32_t rb_elems = lt.ncg * kTileElems;
-  const uint32_t rb0 = __ldg(tk.block_out_pos + b0) / rb_elems;
-  const uint32_t e_end = __ldg(tk.block_out_pos + b1);
-  const uint32_t last = min(e_end > rb0 * rb_elems ? (e_end - 1) / rb_elems - rb0 : 0u,
-                            lt.slots - 1);
-  float *part = lt.part + ((size_t)cta * lt.slots * kWarps + warp) * (16 * 8 * NB);
-  const int g = lane >> 2, t4 = lane & 3;
+  const uint32_t ctas = (ti + 1 < lb.count ? lb.t[ti + 1].cta_begin : lb.cta_end) - lt.cta_begin;
+  const uint32_t cta = blockIdx.x - lt.cta_begin;
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float acc[NB][4];
 #pragma unroll
   for (int j = 0; j < NB; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  uint32_t slot = 0;
-  // this warp's sums of the current slot to the workspace, [token][row]
-  auto flush = [&]() {
-    float *p = part + (size_t)slot * (kWarps * 16 * 8 * NB);
+  float *part = lt.part + ((size_t)cta * lt.slots * kWarps + warp) * (16 * 8 * NB);
+  // the warp's sums of a group's row block to the workspace, [token][row]
+  auto moved = [&](uint32_t) {
+    float *q = part + (2u * (lane & 3u)) * 16u + (lane >> 2);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      float *q = p + (8 * j + 2 * t4) * 16 + g;
-      q[0] = acc[j][0];
-      q[16] = acc[j][1];
-      q[8] = acc[j][2];
-      q[24] = acc[j][3];
+      q[128 * j] = acc[j][0];
+      q[128 * j + 16] = acc[j][1];
+      q[128 * j + 8] = acc[j][2];
+      q[128 * j + 24] = acc[j][3];
       acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
     }
-    ++slot;
+    part += kWarps * 16 * 8 * NB;
   };
-
-  uint32_t wph = 0, k = 0;
-  bool waited = false;
-  for (uint32_t b = b0; b < b1; ++b, ++k) {
-    const uint32_t s = k % kWsStages, par = (k / kWsStages) & 1u;
-    if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&bars[s]), par, lb.spin_limit))) {
-      if (lane == 0) report(lb.err, DF11_DEV_ERR_TIMEOUT);
-      return;  // whole warp
-    }
-    const uint32_t slot_sa = smem_addr(stages + s * L::head_bytes);
-    const uint32_t counts_sa = slot_sa + L::bits_bytes + L::gaps_bytes;
-    const uint4 m = lds128(counts_sa + L::counts_bytes);
-    const uint32_t P0 = m.x, expected = m.y - m.x;
-    const uint32_t release = smem_addr(&bars[kWsStages + s]);
-    int start, end;
-    {
-      const uint32_t bit = 5u * (uint32_t)tid;
-      const uint32_t ga = slot_sa + L::bits_bytes + 4u * (bit >> 5);
-      const uint32_t v = __funnelshift_l(__byte_perm(lds32(ga + 4u), 0, 0x0123),
-                                         __byte_perm(lds32(ga), 0, 0x0123), bit);
-      start = (int)(v >> 27);
-      end = C * 8 + (int)((v >> 22) & 31u);
-    }
-    uint32_t w[NW];
-#pragma unroll
-    for (int j = 0; j < NW; ++j)
-      w[j] = __byte_perm(lds32(slot_sa + (uint32_t)tid * C + 4u * j), 0, 0x0123);
-    const uint2 cv = lds64(counts_sa + 8u * lane);
-    const uint32_t lsum = __dp4a(cv.x, 0x01010101u, __dp4a(cv.y, 0x01010101u, 0u));
-    const uint32_t cnt = lds8(counts_sa + tid);
-    const uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp * 32 / kWarps ? lsum : 0u);
-    const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, lsum);
-    uint32_t incl = cnt;
-#pragma unroll
-    for (int dd = 1; dd < 32; dd <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, dd);
-      if (lane >= dd) incl += v;
-    }
-    const uint32_t warp_total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-    if (!m.z || total != expected || warp_total > tk.max_warp_elems ||
-        __any_sync(0xFFFFFFFFu, cnt > tk.max_chunk_elems)) {
-      if (lane == 0)
-        report(lb.err, m.z && total != expected ? DF11_DEV_ERR_COUNT : DF11_DEV_ERR_CAPACITY);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(release);
-      continue;
-    }
-    if (m.w != 0xFFFFFFFFu) {  // the block that holds the end of the stream
-      const uint32_t bit0 = (uint32_t)tid * (C * 8);
-      if (bit0 >= m.w) start = end = 0;
-      else if ((uint32_t)end > m.w - bit0) end = (int)(m.w - bit0);
-    }
-    if (tk.masked) {  // ones from bit `end` on
-      if (end >= C * 8) {
-        w[NW - 1] |= __funnelshift_rc(0xFFFFFFFFu, 0u, (uint32_t)(end - C * 8));
-      } else {
-#pragma unroll
-        for (int j = 0; j < NW; ++j)
-          w[j] |= __funnelshift_rc(0xFFFFFFFFu, 0u, (uint32_t)max(end - 32 * j, 0));
-      }
-    }
-    // the slot's bytes are in registers: it can be refilled
-    __syncwarp();
-    if (lane == 0) mbar_arrive(release);
-    const uint32_t G0 = P0 + before;
-    const uint32_t head = G0 & 15u, span = head + warp_total;
-    const uint32_t d = head + incl - cnt;
-    const uint32_t wsm_bytes = (span + 15u) & ~15u;
-    if (wsm_bytes && lane == 0) {
-      mbar_arrive_expect_tx(wbar, wsm_bytes);
-      bulk_g2s(wsm, tk.sign_mantissa + (G0 & ~15u), wsm_bytes, wbar);
-    }
-    int bad = 0;
-    uint32_t got;
-    if (tk.masked) {
-      got = decode_counted<C>(w, start, end, wide, lut0_s, lens_s, sub, tk.num_luts, region, d, cnt,
-                              bad);
-    } else {
-      const uint32_t limit = region + ((d + (cnt ? cnt : 1u) - 1u) & ~3u);
-      got = decode_direct<kT, C, false>(w, start, end, wide, lut0_s, lens_s, sub, tk.num_luts,
-                                        region, d, limit, bad);
-    }
-    if (!bad && got != cnt) bad = DF11_DEV_ERR_COUNT;
-    if (wsm_bytes) {
-      const bool landed = __all_sync(0xFFFFFFFFu, mbar_wait(wbar, wph & 1u, lb.spin_limit));
-      ++wph;
-      if (!landed) {
-        if (lane == 0) report(lb.err, DF11_DEV_ERR_TIMEOUT);
-        return;  // whole warp; the buffer may still be written
-      }
-    }
-    if (__any_sync(0xFFFFFFFFu, bad != 0)) {
-      if (bad) report(lb.err, bad);
-      __syncwarp();
-      for (uint32_t i = lane; i < (span + 8u + 15u) >> 4; i += 32)
-        reinterpret_cast<uint4 *>(region_p)[i] = make_uint4(0, 0, 0, 0);
-      __syncwarp();
-      continue;
-    }
-    __syncwarp();
-    if (!waited) {  // the previous kernel may have written x, or still read the workspace
-      pdl_wait();
-      waited = true;
-    }
-
-    // multiply: groups 0 .. ng-1 of the region are the stream's groups q0 ..
-    const uint32_t ng = (span + 15u) >> 4, q0 = G0 >> 4;
-    if (ng) {
-      uint32_t tile = q0 >> 6;
-      const uint32_t tile_end = (q0 + ng - 1u) >> 6;
-      uint32_t rb = tile / lt.ncg, cg = tile - rb * lt.ncg;
-      for (; tile <= tile_end; ++tile) {
-        // sums of the row blocks before this tile's; beyond the range only
-        // when the positions are inconsistent
-        if (rb - rb0 > last) {
-          if (lane == 0) report(lb.err, DF11_DEV_ERR_COUNT);
-          break;
-        }
-        while (slot < rb - rb0) flush();
-        const uint32_t col = cg * kTileCols + 16u * t4;
-        uint4 xv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if ((uint32_t)g < tk.batch && col < tk.cols) {
-          const uint4 *xp = reinterpret_cast<const uint4 *>(tk.x + (size_t)g * tk.x_stride + col);
-          xv[0] = __ldg(xp);
-          xv[1] = __ldg(xp + 1);
-        }
-        uint32_t wv[2][8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t gi = (tile << 6) + 32u * h + lane - q0;  // wraps below the range
-          uint4 sv = make_uint4(0, 0, 0, 0), rv = make_uint4(0, 0, 0, 0);
-          if (gi < ng) {
-            sv = lds128(wsm + 16u * gi);
-            rv = lds128(region + 16u * gi);
-            sts128_zero(region + 16u * gi);
-            // the first and last groups may hold neighbours' elements
-            if ((gi == 0 && head) || (gi == ng - 1 && (span & 15u)))
-              sv = keep_bytes(sv, gi == 0 ? head : 0u, gi == ng - 1 ? span - 16u * gi : 16u);
-          }
-          const uint2 a = fuse4(sv.x, rv.x), c = fuse4(sv.y, rv.y);
-          const uint2 e = fuse4(sv.z, rv.z), f = fuse4(sv.w, rv.w);
-          wv[h][0] = a.x; wv[h][1] = a.y; wv[h][2] = c.x; wv[h][3] = c.y;
-          wv[h][4] = e.x; wv[h][5] = e.y; wv[h][6] = f.x; wv[h][7] = f.y;
-        }
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          mma_bf16(acc[j], wv[0][0], wv[1][0], wv[0][1], wv[1][1], xv[0].x, xv[0].y);
-          mma_bf16(acc[j], wv[0][2], wv[1][2], wv[0][3], wv[1][3], xv[0].z, xv[0].w);
-          mma_bf16(acc[j], wv[0][4], wv[1][4], wv[0][5], wv[1][5], xv[1].x, xv[1].y);
-          mma_bf16(acc[j], wv[0][6], wv[1][6], wv[0][7], wv[1][7], xv[1].z, xv[1].w);
-          if (j + 1 < NB) {
-            xv[0] = xv[1] = make_uint4(0, 0, 0, 0);
-            const uint32_t n = 8u * (j + 1) + g;
-            if (n < tk.batch && col < tk.cols) {
-              const uint4 *xp = reinterpret_cast<const uint4 *>(tk.x + (size_t)n * tk.x_stride + col);
-              xv[0] = __ldg(xp);
-              xv[1] = __ldg(xp + 1);
-            }
-          }
-        }
-        if (++cg == lt.ncg) {
-          cg = 0;
-          ++rb;
-        }
-      }
-      __syncwarp();  // the region is zero again before the next walk
-    }
-  }
-  if (!waited) pdl_wait();
-  while (slot <= last) flush();
+  // x may come from the previous kernel, which may still read the workspace
+  auto start = [&]() {
+    pdl_wait();
+    pdl_launch_dependents();
+  };
+  decode_units(lt.w, cta, ctas, lb.err, lb.spin_limit, smem, start, Multiply<NB>{lt, acc}, moved);
 }
 
 // The warps' sums of every row block added in a fixed order, and the epilogue.
 struct FTensor {
   Epilogue e;
   const float *part;
-  const uint32_t *block_out_pos;
-  uint32_t num_blocks, ctas, slots, rb_elems;
+  uint32_t ctas, slots, rbs, upr;
   uint32_t rows, batch;
-  uint32_t rb_begin;  // first row block of this tensor in the grid
+  uint32_t block_begin;  // first thread block of this tensor in the grid
 };
 struct FBatch {
   FTensor t[DF11_MAX_BATCH];
   int count;
   uint32_t nb;  // groups of 8 tokens in the workspace's layout
 };
+constexpr int kFinishThreads = 128;
 
-// 128 threads per row block and group of 8 tokens: thread (n, r) is token n, row r
-__global__ void __launch_bounds__(128) df11_linear_finish_kernel(const __grid_constant__ FBatch fb) {
-  __shared__ uint32_t range[2];
+// a thread per output: 16 rows of a token next to each other, tokens of a row block next
+__global__ void __launch_bounds__(kFinishThreads)
+    df11_linear_finish_kernel(const __grid_constant__ FBatch fb) {
   int ti = 0;
   for (int i = 1; i < fb.count; ++i)
-    if (blockIdx.x >= fb.t[i].rb_begin) ti = i;
+    if (blockIdx.x >= fb.t[i].block_begin) ti = i;
   const FTensor &ft = fb.t[ti];
-  const uint32_t rb = blockIdx.x - ft.rb_begin;
-  const uint32_t token = 8u * blockIdx.y + (threadIdx.x >> 4), r = threadIdx.x & 15u;
-  // the thread blocks whose ranges touch this row block, from the positions at
-  // the ranges' ends (inputs of the call, so before the wait)
-  if (threadIdx.x < 2) {
-    const uint32_t e = threadIdx.x == 0 ? rb * ft.rb_elems : (rb + 1) * ft.rb_elems - 1u;
-    // the last thread block whose range starts at or before element e
-    uint32_t lo = 0, hi = ft.ctas;
-    while (hi - lo > 1) {
-      const uint32_t mid = (lo + hi) >> 1;
-      if (__ldg(ft.block_out_pos + first_block(mid, ft.num_blocks, ft.ctas)) <= e) lo = mid;
-      else hi = mid;
-    }
-    range[threadIdx.x] = lo;
-  }
-  __syncthreads();
+  // at most 2^26 rows and kFusedMax tokens: below 2^32
+  const uint32_t i = (blockIdx.x - ft.block_begin) * kFinishThreads + threadIdx.x;
+  const uint32_t r = i & 15u, rb = (i >> 4) / ft.batch;
+  const uint32_t token = (i >> 4) - rb * ft.batch, row = 16u * rb + r;
   pdl_wait();
   pdl_launch_dependents();
-  const uint32_t row = 16u * rb + r;
-  if (token >= ft.batch || row >= ft.rows) return;
+  if (rb >= ft.rbs || row >= ft.rows) return;
+  // the thread blocks that hold units of the row block's group
+  const uint64_t units = ordered_units(ft.rbs, ft.upr), per_group = (uint64_t)ft.upr * kWarps;
+  const uint64_t group = rb / kWarps;
+  auto holder = [&](uint64_t o) { return (uint32_t)(((o + 1) * ft.ctas - 1) / units); };
+  const uint32_t c0 = holder(group * per_group), c1 = holder((group + 1) * per_group - 1);
   const uint32_t per_warp = 16u * 8u * fb.nb;
+  const float *p = ft.part + (size_t)(rb % kWarps) * per_warp + token * 16u + r;
   float sum = 0.f;
-  for (uint32_t c = range[0]; c <= range[1]; ++c) {
-    const uint32_t rb0 =
-        __ldg(ft.block_out_pos + first_block(c, ft.num_blocks, ft.ctas)) / ft.rb_elems;
-    const uint32_t slot = rb - rb0;
-    if (slot >= ft.slots) continue;  // inconsistent positions, reported by the product kernel
-    const float *p = ft.part + ((size_t)c * ft.slots + slot) * kWarps * per_warp + token * 16u + r;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += __ldcg(p + w * per_warp);
-  }
+  // slot of the group in a thread block's part: 0 but for those that begin before it
+  sum = __ldcg(p + ((size_t)c0 * ft.slots + (group - first_unit(c0, units, ft.ctas) / per_group)) *
+                       kWarps * per_warp);
+#pragma unroll 4
+  for (uint32_t c = c0 + 1; c <= c1; ++c) sum += __ldcg(p + (size_t)c * ft.slots * kWarps * per_warp);
   store_any(ft.e, finish(ft.e, sum, token, row), token, row);
+}
+
+// ---- decoding into tiles --------------------------------------------------------------
+
+struct UArgs {
+  LWeight w[DF11_MAX_BATCH];
+  uint16_t *out[DF11_MAX_BATCH];  // tiles of 16 rows x 64 columns, along the rows
+  uint32_t cta_begin[DF11_MAX_BATCH + 1];
+  int32_t *err;
+  int count;
+  uint32_t spin_limit;
+};
+
+struct StoreTile {
+  uint16_t *out;
+  uint32_t ncg;
+  __device__ __forceinline__ void load(uint32_t) {}
+  __device__ __forceinline__ void operator()(uint32_t rb, uint32_t cg, const uint32_t (&w0)[8],
+                                             const uint32_t (&w1)[8]) {
+    uint4 *q = reinterpret_cast<uint4 *>(out + ((size_t)rb * ncg + cg) * kTileElems) +
+               2u * (threadIdx.x & 31u);
+    q[0] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+    q[1] = make_uint4(w0[4], w0[5], w0[6], w0[7]);
+    q[64] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+    q[65] = make_uint4(w1[4], w1[5], w1[6], w1[7]);
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 2) df11_linear_unpack_kernel(const __grid_constant__ UArgs ua) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  int ti = 0;
+  for (int i = 1; i < ua.count; ++i)
+    if (blockIdx.x >= ua.cta_begin[i]) ti = i;
+  auto start = [&]() {  // the previous kernel may still read the output
+    pdl_wait();
+    pdl_launch_dependents();
+  };
+  decode_units(ua.w[ti], blockIdx.x - ua.cta_begin[ti], ua.cta_begin[ti + 1] - ua.cta_begin[ti],
+               ua.err, ua.spin_limit, smem, start, StoreTile{ua.out[ti], ua.w[ti].ncg},
+               [](uint32_t) {});
+}
+
+// ---- building the compressed form --------------------------------------------------------
+
+struct PackWeight {
+  const uint16_t *w;       // rows x cols
+  const LinearTable *table;
+  uint32_t *unit_rows;
+  uint32_t *streams;
+  uint8_t *sign_mantissa;
+  uint32_t rows, cols, rbs, ncg, unit_tiles, upr;
+  uint32_t vec;            // rows of the weight on 16-byte boundaries
+};
+
+// a lane's 16 elements of a half tile, zeros past the matrix
+__device__ __forceinline__ void load_half(const PackWeight &a, uint32_t row, uint32_t col,
+                                          uint32_t (&v)[8]) {
+  const uint16_t *p = a.w + (size_t)row * a.cols + col;
+  if (a.vec && row < a.rows && col + 16u <= a.cols) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    return;
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < 8; ++j) {
+    const uint32_t lo = row < a.rows && col + 2 * j < a.cols ? p[2 * j] : 0u;
+    const uint32_t hi = row < a.rows && col + 2 * j + 1 < a.cols ? p[2 * j + 1] : 0u;
+    v[j] = lo | hi << 16;
+  }
+}
+
+// A warp per unit.  WRITE = false: the longest lane's words into unit_rows[unit];
+// WRITE: the lanes' streams from row unit_rows[unit] on, and the sign/mantissa bytes.
+template <bool WRITE>
+__global__ void __launch_bounds__(256) linear_encode_kernel(const __grid_constant__ PackWeight a) {
+  __shared__ uint32_t code_s[256], len_s[256];
+  for (uint32_t i = threadIdx.x; i < 256; i += 256) {
+    code_s[i] = a.table->code[i];
+    len_s[i] = a.table->length[i];
+  }
+  __syncthreads();
+  const uint32_t lane = threadIdx.x & 31;
+  const uint64_t units = (uint64_t)a.rbs * a.upr;
+  for (uint64_t u = (blockIdx.x * 256ull + threadIdx.x) >> 5; u < units; u += gridDim.x * 8ull) {
+    const uint32_t rb = (uint32_t)(u / a.upr), ku = (uint32_t)(u - (uint64_t)rb * a.upr);
+    const uint32_t cg0 = ku * a.unit_tiles, cg1 = min(cg0 + a.unit_tiles, a.ncg);
+    uint32_t bits = 0;
+    uint32_t row = WRITE ? a.unit_rows[u] : 0u;
+    const uint32_t end = WRITE ? a.unit_rows[u + 1] : 0u;
+    uint64_t buf = 0;  // the next bits, left-aligned; `bits` of them
+    for (uint32_t cg = cg0; cg < cg1; ++cg) {
+#pragma unroll 1
+      for (uint32_t h = 0; h < 2; ++h) {
+        uint32_t v[8], sm[4];
+        load_half(a, 16u * rb + 8u * h + (lane >> 2), 64u * cg + 16u * (lane & 3u), v);
+#pragma unroll
+        for (uint32_t j = 0; j < 16; ++j) {
+          const uint32_t e16 = (v[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+          const uint32_t exp = (e16 >> 7) & 0xFFu;
+          if (!WRITE) {
+            bits += len_s[exp];
+          } else {
+            const uint32_t byte = (e16 >> 8 & 0x80u) | (e16 & 0x7Fu);
+            sm[j >> 2] = (j & 3) ? sm[j >> 2] | byte << (8 * (j & 3)) : byte;
+            buf |= (uint64_t)code_s[exp] << 32 >> bits;
+            bits += len_s[exp];
+            if (bits >= 32) {
+              a.streams[(size_t)row * 32u + lane] = (uint32_t)(buf >> 32);
+              ++row;
+              buf <<= 32;
+              bits -= 32;
+            }
+          }
+        }
+        if (WRITE)
+          *reinterpret_cast<uint4 *>(a.sign_mantissa + ((size_t)rb * a.ncg + cg) * kTileElems +
+                                     512u * h + 16u * lane) = make_uint4(sm[0], sm[1], sm[2], sm[3]);
+      }
+    }
+    if constexpr (WRITE) {
+      for (; row < end; ++row) {
+        a.streams[(size_t)row * 32u + lane] = (uint32_t)(buf >> 32);
+        buf = 0;
+      }
+    } else {
+      const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, (bits + 31u) >> 5);
+      if (lane == 0) a.unit_rows[u] = most;
+    }
+  }
+}
+
+// unit_rows[0 .. units - 1] (words of each unit) to the units' first rows, unit_rows[units]
+// the total; result: the total and the longest unit.  One thread block.
+__global__ void __launch_bounds__(1024) linear_rows_kernel(uint32_t *unit_rows, uint64_t units,
+                                                           uint32_t *result) {
+  __shared__ uint32_t sums[32], most_s[32];
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t base = 0, most = 0;
+  for (uint64_t u0 = 0; u0 < units; u0 += 1024) {
+    const uint64_t u = u0 + tid;
+    const uint32_t v = u < units ? unit_rows[u] : 0u;
+    most = max(most, v);
+    uint32_t incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= (uint32_t)d) incl += o;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+    for (uint32_t w = 0; w < 32; ++w) {
+      if (w < warp) before += sums[w];
+      all += sums[w];
+    }
+    if (u < units) unit_rows[u] = base + before + incl - v;
+    base += all;
+    __syncthreads();
+  }
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if (lane == 0) most_s[warp] = most;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 0; w < 32; ++w) most = max(most, most_s[w]);
+    unit_rows[units] = base;
+    result[0] = base;
+    result[1] = most;
+  }
 }
 
 // ---- more tokens: tcgen05 product of the decoded tiles ------------------------
@@ -795,89 +1013,98 @@ constexpr uint32_t kFusedMax = 32;
 
 uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
-uint32_t region_bytes_for(uint32_t max_warp_elems) {
-  return (15u + max_warp_elems + 8u + 15u) & ~15u;
+// x as the kernels read it: 16-byte loads of whole 16-column groups
+bool needs_pack(const df11_linear &op, uint32_t cols) {
+  return cols % 16 || op.x_stride % 8 || !aligned(op.x, 16);
 }
 
-// x as the kernels read it: 16-byte loads of whole 16-column groups
-bool needs_pack(const df11_linear &op) {
-  return op.cols % 16 || op.x_stride % 8 || !aligned(op.x, 16);
+LWeight device_weight(const df11_linear_weight &w) {
+  const df11_linear_params &p = w.params;
+  LWeight l{};
+  l.streams = w.streams;
+  l.unit_rows = w.unit_rows;
+  l.sign_mantissa = w.sign_mantissa;
+  l.table = static_cast<const LinearTable *>(w.table);
+  l.rbs = (p.rows + kTileRows - 1) / kTileRows;
+  l.ncg = (p.cols + kTileCols - 1) / kTileCols;
+  l.unit_tiles = p.unit_tiles;
+  l.upr = (l.ncg + p.unit_tiles - 1) / p.unit_tiles;
+  l.max_words = p.max_words;
+  l.stream_rows = p.stream_rows;
+  return l;
+}
+
+uint64_t padded(const df11_linear_params &p) {
+  return round_up(p.rows, kTileRows) * round_up(p.cols, kTileCols);
+}
+
+// the thread blocks of a launch over its weights, by units
+df11_status split_units(const df11_linear_weight *ws, int count, uint64_t budget, uint64_t *ctas) {
+  uint32_t units[DF11_MAX_BATCH];
+  for (int i = 0; i < count; ++i) {
+    const LWeight l = device_weight(ws[i]);
+    units[i] = (uint32_t)ordered_units(l.rbs, l.upr);
+  }
+  split_blocks(units, count, budget, ctas);
+  return DF11_OK;
+}
+
+uint32_t longest_stream(const df11_linear_weight *ws, int count) {
+  uint32_t m = 1;
+  for (int i = 0; i < count; ++i) m = ws[i].params.max_words > m ? ws[i].params.max_words : m;
+  return m;
 }
 
 struct Plan {
   bool fused = false;
   uint32_t nb = 1;                       // groups of 8 tokens (fused)
-  uint64_t ctas[DF11_MAX_BATCH] = {};    // thread blocks per tensor (fused)
+  uint64_t ctas[DF11_MAX_BATCH] = {};    // thread blocks per weight (fused)
   uint32_t slots[DF11_MAX_BATCH] = {};
   uint64_t part[DF11_MAX_BATCH] = {};    // workspace offsets: partial sums or decoded weight
   uint64_t packed[DF11_MAX_BATCH] = {};  // packed activations
   uint64_t bytes = 0;
-  uint32_t region = 0;
   size_t smem = 0;
 };
 
-template <int C, int NB>
-void (*linear_kernel())(LBatch) { return df11_linear_kernel<C, NB>; }
-
 using LinearKernel = void (*)(LBatch);
-LinearKernel pick_kernel(uint32_t C, uint32_t nb, int &instance) {
-  const int ci = C == 8 ? 0 : (C == 16 ? 1 : 2), ni = nb == 1 ? 0 : (nb == 2 ? 1 : 2);
-  static const LinearKernel k[3][3] = {
-      {linear_kernel<8, 1>(), linear_kernel<8, 2>(), linear_kernel<8, 4>()},
-      {linear_kernel<16, 1>(), linear_kernel<16, 2>(), linear_kernel<16, 4>()},
-      {linear_kernel<24, 1>(), linear_kernel<24, 2>(), linear_kernel<24, 4>()}};
-  instance = 66 + 3 * ci + ni;
-  return k[ci][ni];
+LinearKernel pick_kernel(uint32_t nb, int &instance) {
+  instance = nb == 1 ? 66 : (nb == 2 ? 67 : 68);
+  return nb == 1 ? df11_linear_kernel<1> : (nb == 2 ? df11_linear_kernel<2> : df11_linear_kernel<4>);
 }
 
-// Everything a group of at most DF11_MAX_BATCH tensors needs from the
-// workspace.  `want_launch`: also query the kernel (needs a device).
-df11_status make_plan(const df11_tensor *ts, const df11_linear *ops, int count, Plan &pl) {
-  uint32_t max_batch = 0, max_warp = 0, C = 0;
+// What a group of at most DF11_MAX_BATCH weights needs from the workspace.
+df11_status make_plan(const df11_linear_weight *ws, const df11_linear *ops, int count, Plan &pl) {
+  uint32_t max_batch = 0;
   uint64_t off = 0;
   for (int i = 0; i < count; ++i) {
     max_batch = max_batch > ops[i].batch ? max_batch : ops[i].batch;
-    const df11_params &p = ts[i].params;
-    max_warp = max_warp > p.max_warp_elems ? max_warp : p.max_warp_elems;
-    C = p.chunk_bytes;
     pl.packed[i] = off;
-    if (needs_pack(ops[i]))
-      off += round_up(2ull * ops[i].batch * round_up(ops[i].cols, kTileCols), 256);
+    if (needs_pack(ops[i], ws[i].params.cols))
+      off += round_up(2ull * ops[i].batch * round_up(ws[i].params.cols, kTileCols), 256);
   }
   pl.fused = max_batch <= kFusedMax;
   if (!pl.fused) {
     for (int i = 0; i < count; ++i) {
       pl.part[i] = off;
-      off += round_up(2ull * ts[i].params.n, 256);
+      off += round_up(2ull * padded(ws[i].params), 256);
     }
     pl.bytes = off;
     return DF11_OK;
   }
   pl.nb = max_batch <= 8 ? 1 : (max_batch <= 16 ? 2 : 4);
-  pl.region = region_bytes_for(max_warp);
-  const size_t head = C == 8 ? WsLayout<kT, 8>::head_bytes
-                             : (C == 16 ? WsLayout<kT, 16>::head_bytes : WsLayout<kT, 24>::head_bytes);
-  pl.smem = kOffStages + kWsStages * head + 2ull * kWarps * pl.region;
-  if (pl.smem > 227 * 1024) return DF11_ERR_TOO_LARGE;
+  pl.smem = decode_smem(longest_stream(ws, count));
   int instance = 0;
   uint64_t budget = 0;
-  const LinearKernel kern = pick_kernel(C, pl.nb, instance);
-  const df11_status st = prepare(kern, kT + 32, pl.smem, instance, budget);
+  const LinearKernel kern = pick_kernel(pl.nb, instance);
+  const df11_status st = prepare(kern, kThreads, pl.smem, instance, budget);
   if (st != DF11_OK) return st;
-  // one wave, split so that the busiest thread block has as few format blocks
-  // as possible
-  uint32_t blocks[DF11_MAX_BATCH];
-  for (int i = 0; i < count; ++i) blocks[i] = ts[i].params.num_blocks;
-  split_blocks(blocks, count, budget, pl.ctas);
+  split_units(ws, count, budget, pl.ctas);
   for (int i = 0; i < count; ++i) {
-    const df11_params &p = ts[i].params;
-    const uint64_t per = (p.num_blocks + pl.ctas[i] - 1) / pl.ctas[i];
-    const uint64_t rb_elems = round_up(ops[i].cols, kTileCols) * kTileRows;
-    uint64_t elems = per * p.max_block_elems;
-    if (elems > p.n) elems = p.n;
-    uint64_t slots = (elems + rb_elems - 1) / rb_elems + 1;
-    const uint64_t all = p.n / rb_elems;
-    if (slots > all) slots = all;
+    const LWeight l = device_weight(ws[i]);
+    const uint64_t units = ordered_units(l.rbs, l.upr), per_group = (uint64_t)l.upr * kWarps;
+    const uint64_t per = (units + pl.ctas[i] - 1) / pl.ctas[i];
+    uint64_t slots = (per + per_group - 2) / per_group + 1;
+    if (slots > units / per_group) slots = units / per_group;
     pl.slots[i] = (uint32_t)slots;
     pl.part[i] = off;
     off += round_up(pl.ctas[i] * slots * kWarps * 16 * 8 * pl.nb * sizeof(float), 256);
@@ -905,71 +1132,76 @@ Epilogue make_epilogue(const df11_linear &op) {
 bool known_type(int32_t t) { return t == DF11_BF16 || t == DF11_F32; }
 uintptr_t type_bytes(int32_t t) { return t == DF11_F32 ? 4 : 2; }
 
-// One tensor and its operation; DF11_OK for one that does nothing, too.
-df11_status check_op(const df11_tensor &t, const df11_linear &op) {
-  const df11_params &p = t.params;
+df11_status check_shape(uint32_t rows, uint32_t cols) {
+  if (rows == 0 || cols == 0) return DF11_ERR_INVALID;
+  if (round_up(rows, kTileRows) * round_up(cols, kTileCols) >= (1ull << 32)) return DF11_ERR_TOO_LARGE;
+  return DF11_OK;
+}
+
+df11_status check_weight(const df11_linear_weight &w) {
+  const df11_linear_params &p = w.params;
+  const df11_status st = check_shape(p.rows, p.cols);
+  if (st != DF11_OK) return st;
+  if (!w.streams || !w.unit_rows || !w.sign_mantissa || !w.table) return DF11_ERR_NULL;
+  if (!aligned(w.streams, 16) || !aligned(w.sign_mantissa, 16) || !aligned(w.table, 16) ||
+      !aligned(w.unit_rows, 4))
+    return DF11_ERR_ALIGN;
+  if (p.unit_tiles < 1 || p.unit_tiles > kMaxUnitTiles || p.max_words < 1 || p.max_words > kMaxWords)
+    return DF11_ERR_FORMAT;
+  const LWeight l = device_weight(w);
+  if (p.stream_rows > (uint64_t)l.rbs * l.upr * p.max_words) return DF11_ERR_FORMAT;
+  return DF11_OK;
+}
+
+// One weight and its operation; DF11_OK for one that does nothing, too.
+df11_status check_op(const df11_linear_weight &w, const df11_linear &op) {
   if (op.activation < DF11_ACT_NONE || op.activation > DF11_ACT_SILU) return DF11_ERR_INVALID;
   if (!known_type(op.y_type) || (op.bias && !known_type(op.bias_type)) ||
       (op.multiplier && !known_type(op.multiplier_type)) ||
       (op.residual && !known_type(op.residual_type)))
     return DF11_ERR_INVALID;
-  if (p.n >= (1ull << 32)) return DF11_ERR_TOO_LARGE;
-  if (op.rows == 0 || op.cols == 0 ||
-      round_up(op.rows, kTileRows) * round_up(op.cols, kTileCols) != p.n)
-    return DF11_ERR_INVALID;
+  const df11_status st = check_weight(w);
+  if (st != DF11_OK) return st;
   if (op.batch == 0) return DF11_OK;
   if (op.batch > DF11_LINEAR_MAX_BATCH) return DF11_ERR_TOO_LARGE;
   if (!op.x || !op.y) return DF11_ERR_NULL;
-  if (op.x_stride < op.cols || op.y_stride < op.rows ||
-      (op.multiplier && op.multiplier_stride < op.rows) ||
-      (op.residual && op.residual_stride < op.rows))
+  const uint32_t rows = w.params.rows;
+  if (op.x_stride < w.params.cols || op.y_stride < rows ||
+      (op.multiplier && op.multiplier_stride < rows) || (op.residual && op.residual_stride < rows))
     return DF11_ERR_INVALID;
   if (!aligned(op.x, 2) || !aligned(op.y, type_bytes(op.y_type)) ||
       !aligned(op.bias, type_bytes(op.bias_type)) ||
       !aligned(op.multiplier, type_bytes(op.multiplier_type)) ||
       !aligned(op.residual, type_bytes(op.residual_type)))
     return DF11_ERR_ALIGN;
-  df11_tensor v = t;
-  v.out_bf16 = reinterpret_cast<uint16_t *>(16);  // not written; passes the output checks
-  const df11_status st = validate(v);
-  if (st != DF11_OK) return st;
-  if (!t.chunk_counts || !t.decode_table || p.threads_per_block != kT ||
-      (p.chunk_bytes != 8 && p.chunk_bytes != 16 && p.chunk_bytes != 24))
-    return DF11_ERR_UNSUPPORTED;
   return DF11_OK;
 }
 
-// The tensors of a call that have work, checked; groups of them are launched
-// together.
-df11_status check_call(const df11_tensor *tensors, const df11_linear *ops, int count) {
+df11_status check_call(const df11_linear_weight *ws, const df11_linear *ops, int count) {
   if (count < 0) return DF11_ERR_INVALID;
-  if (count && (!tensors || !ops)) return DF11_ERR_NULL;
-  uint32_t C = 0;
+  if (count && (!ws || !ops)) return DF11_ERR_NULL;
   for (int i = 0; i < count; ++i) {
-    const df11_status st = check_op(tensors[i], ops[i]);
+    const df11_status st = check_op(ws[i], ops[i]);
     if (st != DF11_OK) return st;
-    if (ops[i].batch == 0) continue;
-    if (C && C != tensors[i].params.chunk_bytes) return DF11_ERR_INVALID;
-    C = tensors[i].params.chunk_bytes;
   }
   return DF11_OK;
 }
 
-// calls f(tensors, ops, count) for the next group of at most DF11_MAX_BATCH
-// tensors with work, until one fails
+// calls f(weights, ops, count) for the next group of at most DF11_MAX_BATCH weights
+// with work, until one fails
 template <typename F>
-df11_status for_groups(const df11_tensor *tensors, const df11_linear *ops, int count, F f) {
-  df11_tensor ts[DF11_MAX_BATCH];
-  df11_linear os[DF11_MAX_BATCH];
+df11_status for_groups(const df11_linear_weight *ws, const df11_linear *ops, int count, F f) {
+  df11_linear_weight w[DF11_MAX_BATCH];
+  df11_linear o[DF11_MAX_BATCH];
   int m = 0;
   for (int i = 0; i < count; ++i) {
     if (ops[i].batch) {
-      ts[m] = tensors[i];
-      os[m] = ops[i];
+      w[m] = ws[i];
+      o[m] = ops[i];
       ++m;
     }
     if (m && (m == DF11_MAX_BATCH || i + 1 == count)) {
-      const df11_status st = f(ts, os, m);
+      const df11_status st = f(w, o, m);
       if (st != DF11_OK) return st;
       m = 0;
     }
@@ -977,48 +1209,71 @@ df11_status for_groups(const df11_tensor *tensors, const df11_linear *ops, int c
   return DF11_OK;
 }
 
-df11_status launch_fused(const df11_tensor *ts, const df11_linear *ops, int count, const Plan &pl,
-                         uint8_t *ws, const uint16_t *const *x, const uint32_t *x_stride,
-                         const uint32_t *x_cols, int32_t *d_err, cudaStream_t s) {
+// activations as the kernels read them: the caller's, or packed
+struct Activations {
+  const uint16_t *x;
+  uint32_t stride, cols;
+};
+
+df11_status launch_fused(const df11_linear_weight *ws, const df11_linear *ops, int count,
+                         const Plan &pl, uint8_t *work, const Activations *x, int32_t *d_err,
+                         cudaStream_t s) {
   LBatch lb{};
   FBatch fb{};
   lb.err = d_err;
   lb.count = fb.count = count;
-  lb.region_bytes = pl.region;
   lb.spin_limit = kSpinLimit;
   fb.nb = pl.nb;
-  uint32_t cta = 0, rbs = 0;
+  uint32_t cta = 0, blocks = 0;
   for (int i = 0; i < count; ++i) {
     LTensor &l = lb.t[i];
-    fill_tensor(l.k, ts[i]);
-    l.k.cta_begin = cta;
-    cta += (uint32_t)pl.ctas[i];
-    l.k.x = x[i];
-    l.k.x_stride = x_stride[i];
-    l.k.cols = x_cols[i];
-    l.k.batch = ops[i].batch;
-    l.ncg = (uint32_t)(round_up(ops[i].cols, kTileCols) / kTileCols);
+    l.w = device_weight(ws[i]);
+    l.x = x[i].x;
+    l.x_stride = x[i].stride;
+    l.x_cols = x[i].cols;
+    l.batch = ops[i].batch;
     l.slots = pl.slots[i];
-    l.part = reinterpret_cast<float *>(ws + pl.part[i]);
+    l.part = reinterpret_cast<float *>(work + pl.part[i]);
+    l.cta_begin = cta;
+    cta += (uint32_t)pl.ctas[i];
     FTensor &f = fb.t[i];
     f.e = make_epilogue(ops[i]);
     f.part = l.part;
-    f.block_out_pos = l.k.block_out_pos;
-    f.num_blocks = l.k.num_blocks;
     f.ctas = (uint32_t)pl.ctas[i];
     f.slots = l.slots;
-    f.rb_elems = l.ncg * kTileElems;
-    f.rows = ops[i].rows;
+    f.rbs = l.w.rbs;
+    f.upr = l.w.upr;
+    f.rows = ws[i].params.rows;
     f.batch = ops[i].batch;
-    f.rb_begin = rbs;
-    rbs += (ops[i].rows + 15u) / 16u;
+    f.block_begin = blocks;
+    blocks += (l.w.rbs * 16u * ops[i].batch + kFinishThreads - 1) / kFinishThreads;
   }
   lb.cta_end = cta;
   int instance = 0;
-  const LinearKernel kern = pick_kernel(ts[0].params.chunk_bytes, pl.nb, instance);
-  df11_status st = launch_pdl(kern, dim3(cta), kT + 32, pl.smem, s, lb);
+  const LinearKernel kern = pick_kernel(pl.nb, instance);
+  const df11_status st = launch_pdl(kern, dim3(cta), kThreads, pl.smem, s, lb);
   if (st != DF11_OK) return st;
-  return launch_pdl(df11_linear_finish_kernel, dim3(rbs, pl.nb), 128, 0, s, fb);
+  return launch_pdl(df11_linear_finish_kernel, dim3(blocks), kFinishThreads, 0, s, fb);
+}
+
+// the weights decoded into tiles, one launch
+df11_status launch_unpack(const df11_linear_weight *ws, int count, uint16_t *const *out,
+                          int32_t *d_err, cudaStream_t s) {
+  UArgs ua{};
+  const size_t smem = decode_smem(longest_stream(ws, count));
+  uint64_t budget = 0, ctas[DF11_MAX_BATCH];
+  const df11_status st = prepare(df11_linear_unpack_kernel, kThreads, smem, 69, budget);
+  if (st != DF11_OK) return st;
+  split_units(ws, count, budget, ctas);
+  ua.err = d_err;
+  ua.count = count;
+  ua.spin_limit = kSpinLimit;
+  for (int i = 0; i < count; ++i) {
+    ua.w[i] = device_weight(ws[i]);
+    ua.out[i] = out[i];
+    ua.cta_begin[i + 1] = ua.cta_begin[i] + (uint32_t)ctas[i];
+  }
+  return launch_pdl(df11_linear_unpack_kernel, dim3(ua.cta_begin[count]), kThreads, smem, s, ua);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -1051,8 +1306,8 @@ df11_status launch_gemm_bn(const CUtensorMap &mx, CUtensorMap mw, GemmArgs ga, i
   return launch_pdl(kern, dim3(grid), kGemmThreads, GemmLayout<BN>::smem, s, mx, mw, ga);
 }
 
-df11_status launch_gemm(const df11_linear &op, const uint16_t *w, const uint16_t *x,
-                        uint32_t x_stride, uint32_t x_cols, int32_t *d_err, cudaStream_t s) {
+df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, const uint16_t *w,
+                        const Activations &x, int32_t *d_err, cudaStream_t s) {
   const EncodeTiled encode = encode_tiled();
   if (!encode) return DF11_ERR_CUDA;
   int dev = 0;
@@ -1061,8 +1316,8 @@ df11_status launch_gemm(const df11_linear &op, const uint16_t *w, const uint16_t
   GemmArgs ga{};
   ga.e = make_epilogue(op);
   ga.tokens = op.batch;
-  ga.rows = op.rows;
-  ga.ncg = (uint32_t)(round_up(op.cols, kTileCols) / kTileCols);
+  ga.rows = rows;
+  ga.ncg = (uint32_t)(round_up(cols, kTileCols) / kTileCols);
   ga.tiles_m = (op.batch + kGemmTokens - 1) / kGemmTokens;
   ga.err = d_err;
   ga.spin_limit = kSpinLimit;
@@ -1077,7 +1332,7 @@ df11_status launch_gemm(const df11_linear &op, const uint16_t *w, const uint16_t
   uint32_t best = 64;
   uint64_t cost = ~0ull;
   for (uint32_t bn : {256u, 128u, 64u}) {
-    const uint64_t tiles = (uint64_t)ga.tiles_m * ((op.rows + bn - 1) / bn);
+    const uint64_t tiles = (uint64_t)ga.tiles_m * ((rows + bn - 1) / bn);
     const uint64_t c = (tiles + sms - 1) / sms * (bn + 32);
     if (c < cost) {
       cost = c;
@@ -1086,16 +1341,16 @@ df11_status launch_gemm(const df11_linear &op, const uint16_t *w, const uint16_t
   }
   CUtensorMap mx, mw;
   {
-    const cuuint64_t dims[2] = {x_cols, op.batch}, strides[1] = {2ull * x_stride};
+    const cuuint64_t dims[2] = {x.cols, op.batch}, strides[1] = {2ull * x.stride};
     const cuuint32_t box[2] = {64, kGemmTokens}, one[2] = {1, 1};
-    if (encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(x), dims, strides,
+    if (encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(x.x), dims, strides,
                box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
         CUDA_SUCCESS)
       return DF11_ERR_CUDA;
   }
   {
-    const cuuint64_t dims[4] = {64, 16, ga.ncg, (op.rows + 15u) / 16u};
+    const cuuint64_t dims[4] = {64, 16, ga.ncg, (rows + 15u) / 16u};
     const cuuint64_t strides[3] = {128, 2048, 2048ull * ga.ncg};
     const cuuint32_t box[4] = {64, 16, 1, best / 16}, one[4] = {1, 1, 1, 1};
     if (encode(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(w), dims, strides,
@@ -1109,32 +1364,189 @@ df11_status launch_gemm(const df11_linear &op, const uint16_t *w, const uint16_t
   return launch_gemm_bn<64>(mx, mw, ga, sms, 77, s);
 }
 
-df11_status check_linear_devices(const df11_tensor *ts, const df11_linear *ops, int count,
-                                 const void *ws) {
+df11_status check_linear_devices(const df11_linear_weight *ws, const df11_linear *ops, int count,
+                                 const void *work) {
   for (int i = 0; i < count; ++i) {
-    const void *ptrs[] = {ts[i].bitstream, ts[i].sign_mantissa, ts[i].decode_table,
-                          ops[i].x,        ops[i].y,            ops[i].bias,
-                          ops[i].multiplier, ops[i].residual,   i ? nullptr : ws};
+    const void *ptrs[] = {ws[i].streams, ws[i].unit_rows, ws[i].sign_mantissa, ws[i].table,
+                          ops[i].x,      ops[i].y,        ops[i].bias,         ops[i].multiplier,
+                          ops[i].residual, i ? nullptr : work};
     const df11_status st = check_device_pointers(ptrs, (int)(sizeof(ptrs) / sizeof(*ptrs)));
     if (st != DF11_OK) return st;
   }
   return DF11_OK;
 }
 
+// The decode table of a code: its lengths and (right-aligned, canonical) codewords.
+void make_table(const uint8_t len[256], const uint32_t code[256], LinearTable &t) {
+  std::memset(&t, 0, sizeof(t));
+  auto rot = [](uint32_t e) { return (e >> 1 | e << 7) & 0xFFu; };
+  uint32_t next = 0;
+  for (uint32_t l = 1; l <= 32; ++l) {
+    uint32_t count = 0, low = 0xFFFFFFFFu;
+    for (int e = 0; e < 256; ++e)
+      if (len[e] == l) {
+        ++count;
+        low = code[e] < low ? code[e] : low;
+      }
+    t.first[l] = count ? low : 0u;
+    t.range[l] = count << 16 | next;
+    for (int e = 0; e < 256; ++e)
+      if (len[e] == l) t.sym[next + (code[e] - low)] = (uint8_t)rot((uint32_t)e);
+    next += count;
+  }
+  for (int e = 0; e < 256; ++e) {
+    t.length[e] = len[e];
+    t.code[e] = len[e] ? code[e] << (32 - len[e]) : 0u;
+  }
+  // the codeword at the start of `bits` (kPairBits wide, left-aligned in 32), if it is
+  // at most `room` long
+  auto one = [&](uint32_t bits, uint32_t room, uint32_t &sym, uint32_t &l) {
+    for (l = 1; l <= room; ++l) {
+      const uint32_t k = (bits >> (32 - l)) - t.first[l];
+      if (k < t.range[l] >> 16) {
+        sym = t.sym[(t.range[l] & 0xFFFFu) + k];
+        return true;
+      }
+    }
+    return false;
+  };
+  for (uint32_t i = 0; i < kPairs; ++i) {
+    const uint32_t bits = i << (32 - kPairBits);
+    uint32_t s0 = 0, s1 = 0, l0 = 0, l1 = 0;
+    if (!one(bits, kPairBits, s0, l0)) t.pair[i] = kBothFlag | kDeepFlag;
+    else if (!one(bits << l0, kPairBits - l0, s1, l1)) t.pair[i] = kBothFlag | l0 << 24 | s0 << 8 | l0;
+    else t.pair[i] = l0 << 24 | s1 << 16 | s0 << 8 | (l0 + l1);
+  }
+}
+
+PackWeight pack_weight(const uint16_t *d_w, const df11_linear_params &p, uint32_t *unit_rows,
+                       const void *table) {
+  PackWeight a{};
+  a.w = d_w;
+  a.table = static_cast<const LinearTable *>(table);
+  a.unit_rows = unit_rows;
+  a.rows = p.rows;
+  a.cols = p.cols;
+  a.rbs = (p.rows + kTileRows - 1) / kTileRows;
+  a.ncg = (p.cols + kTileCols - 1) / kTileCols;
+  a.unit_tiles = p.unit_tiles;
+  a.upr = (a.ncg + a.unit_tiles - 1) / a.unit_tiles;
+  a.vec = p.cols % 8 == 0 && aligned(d_w, 16);
+  return a;
+}
+
+uint32_t encode_grid(const PackWeight &a) {
+  const uint64_t blocks = ((uint64_t)a.rbs * a.upr + 7) / 8;
+  return (uint32_t)(blocks < 148 * 8 ? blocks : 148 * 8);
+}
+
 }  // namespace
 
 extern "C" {
 
-df11_status df11_linear_workspace(const df11_tensor *tensors, const df11_linear *ops, int count,
-                                  size_t *bytes) {
+df11_status df11_linear_sizes(uint32_t rows, uint32_t cols, uint64_t *unit_rows_count,
+                              uint64_t *sign_mantissa_bytes) {
+  if (!unit_rows_count || !sign_mantissa_bytes) return DF11_ERR_NULL;
+  const df11_status st = check_shape(rows, cols);
+  if (st != DF11_OK) return st;
+  const uint64_t n = round_up(rows, kTileRows) * round_up(cols, kTileCols);
+  *unit_rows_count = n / kTileElems + 4;  // a unit per tile at most, the total, two results
+  *sign_mantissa_bytes = n;
+  return DF11_OK;
+}
+
+df11_status df11_linear_weight_begin(const uint16_t *d_w, uint32_t rows, uint32_t cols,
+                                     uint32_t *unit_rows, void *table, df11_linear_params *params,
+                                     df11_stream_t stream) {
+  if (!d_w || !unit_rows || !table || !params) return DF11_ERR_NULL;
+  df11_status st = check_shape(rows, cols);
+  if (st != DF11_OK) return st;
+  if (!aligned(d_w, 2) || !aligned(unit_rows, 4) || !aligned(table, 16)) return DF11_ERR_ALIGN;
+  const void *ptrs[] = {d_w, unit_rows, table};
+  st = check_device_pointers(ptrs, 3);
+  if (st != DF11_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  df11_linear_params p{};
+  p.rows = rows;
+  p.cols = cols;
+  const uint64_t n = (uint64_t)rows * cols;
+  uint64_t hist[256];
+  st = df11_exponent_histogram(d_w, n, hist, stream);
+  if (st != DF11_OK) return st;
+  hist[0] += padded(p) - n;
+  try {
+    uint8_t len[256];
+    uint32_t code[256];
+    std::vector<uint32_t> luts;
+    codebook(hist, len, code, luts);
+    std::vector<LinearTable> t(1);
+    make_table(len, code, t[0]);
+    if (cudaMemcpyAsync(table, t.data(), sizeof(LinearTable), cudaMemcpyHostToDevice, s) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+      return DF11_ERR_CUDA;
+  } catch (...) {
+    return DF11_ERR_NOMEM;
+  }
+  // the longest units whose streams stay within kMaxWords
+  for (p.unit_tiles = kMaxUnitTiles;; p.unit_tiles /= 2) {
+    PackWeight a = pack_weight(d_w, p, unit_rows, table);
+    const uint64_t units = (uint64_t)a.rbs * a.upr;
+    uint32_t *result = unit_rows + padded(p) / kTileElems + 1;
+    linear_encode_kernel<false><<<encode_grid(a), 256, 0, s>>>(a);
+    linear_rows_kernel<<<1, 1024, 0, s>>>(unit_rows, units, result);
+    uint32_t got[2] = {0, 0};
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyAsync(got, result, sizeof(got), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+      return DF11_ERR_CUDA;
+    p.stream_rows = got[0];
+    p.max_words = got[1];
+    if (p.max_words <= kMaxWords || p.unit_tiles == 1) break;
+  }
+  *params = p;
+  return DF11_OK;
+}
+
+df11_status df11_linear_weight_finish(const uint16_t *d_w, const df11_linear_weight *weight,
+                                      df11_stream_t stream) {
+  if (!d_w || !weight) return DF11_ERR_NULL;
+  df11_status st = check_weight(*weight);
+  if (st != DF11_OK) return st;
+  if (!aligned(d_w, 2)) return DF11_ERR_ALIGN;
+  const void *ptrs[] = {d_w, weight->streams, weight->unit_rows, weight->sign_mantissa, weight->table};
+  st = check_device_pointers(ptrs, 5);
+  if (st != DF11_OK) return st;
+  PackWeight a = pack_weight(d_w, weight->params, const_cast<uint32_t *>(weight->unit_rows),
+                             weight->table);
+  a.streams = const_cast<uint32_t *>(weight->streams);
+  a.sign_mantissa = const_cast<uint8_t *>(weight->sign_mantissa);
+  linear_encode_kernel<true><<<encode_grid(a), 256, 0, (cudaStream_t)stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? DF11_OK : DF11_ERR_CUDA;
+}
+
+df11_status df11_linear_unpack(const df11_linear_weight *weight, uint16_t *tiles, int32_t *d_err,
+                               df11_stream_t stream) {
+  if (!weight || !tiles) return DF11_ERR_NULL;
+  df11_status st = check_weight(*weight);
+  if (st != DF11_OK) return st;
+  if (!aligned(tiles, 16) || (d_err && !aligned(d_err, 4))) return DF11_ERR_ALIGN;
+  const void *ptrs[] = {tiles, weight->streams, weight->unit_rows, weight->sign_mantissa, weight->table};
+  st = check_device_pointers(ptrs, 5);
+  if (st != DF11_OK) return st;
+  return launch_unpack(weight, 1, &tiles, d_err, (cudaStream_t)stream);
+}
+
+df11_status df11_linear_workspace(const df11_linear_weight *weights, const df11_linear *ops,
+                                  int count, size_t *bytes) {
   if (!bytes) return DF11_ERR_NULL;
   *bytes = 0;
-  df11_status st = check_call(tensors, ops, count);
+  df11_status st = check_call(weights, ops, count);
   if (st != DF11_OK) return st;
   size_t most = 0;
-  st = for_groups(tensors, ops, count, [&](const df11_tensor *ts, const df11_linear *os, int m) {
+  st = for_groups(weights, ops, count, [&](const df11_linear_weight *w, const df11_linear *o, int m) {
     Plan pl;
-    const df11_status r = make_plan(ts, os, m, pl);
+    const df11_status r = make_plan(w, o, m, pl);
     if (r == DF11_OK && pl.bytes > most) most = pl.bytes;
     return r;
   });
@@ -1142,57 +1554,52 @@ df11_status df11_linear_workspace(const df11_tensor *tensors, const df11_linear 
   return st;
 }
 
-df11_status df11_decode_linear(const df11_tensor *tensors, const df11_linear *ops, int count,
+df11_status df11_decode_linear(const df11_linear_weight *weights, const df11_linear *ops, int count,
                                void *workspace, size_t workspace_bytes, int32_t *d_err,
                                df11_stream_t stream) {
-  df11_status st = check_call(tensors, ops, count);
+  df11_status st = check_call(weights, ops, count);
   if (st != DF11_OK) return st;
   if (d_err && !aligned(d_err, 4)) return DF11_ERR_ALIGN;
   cudaStream_t s = (cudaStream_t)stream;
   // checked for every group before anything is queued
-  st = for_groups(tensors, ops, count, [&](const df11_tensor *ts, const df11_linear *os, int m) {
+  st = for_groups(weights, ops, count, [&](const df11_linear_weight *w, const df11_linear *o, int m) {
     Plan pl;
-    df11_status r = make_plan(ts, os, m, pl);
+    df11_status r = make_plan(w, o, m, pl);
     if (r != DF11_OK) return r;
     if (!workspace) return DF11_ERR_NULL;
     if (!aligned(workspace, 256)) return DF11_ERR_ALIGN;
     if (pl.bytes > workspace_bytes) return DF11_ERR_INVALID;
-    return check_linear_devices(ts, os, m, workspace);
+    return check_linear_devices(w, o, m, workspace);
   });
   if (st != DF11_OK) return st;
-  return for_groups(tensors, ops, count, [&](const df11_tensor *ts, const df11_linear *os, int m) {
+  return for_groups(weights, ops, count, [&](const df11_linear_weight *w, const df11_linear *o, int m) {
     Plan pl;
-    df11_status r = make_plan(ts, os, m, pl);
+    df11_status r = make_plan(w, o, m, pl);
     if (r != DF11_OK) return r;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const uint16_t *x[DF11_MAX_BATCH];
-    uint32_t x_stride[DF11_MAX_BATCH], x_cols[DF11_MAX_BATCH];
+    uint8_t *work = static_cast<uint8_t *>(workspace);
+    Activations x[DF11_MAX_BATCH];
     for (int i = 0; i < m; ++i) {
-      x[i] = os[i].x;
-      x_stride[i] = os[i].x_stride;
-      x_cols[i] = os[i].cols;
-      if (!needs_pack(os[i])) continue;
+      const uint32_t cols = w[i].params.cols;
+      x[i] = Activations{o[i].x, o[i].x_stride, cols};
+      if (!needs_pack(o[i], cols)) continue;
       PackArgs pa{};
-      pa.x = os[i].x;
-      pa.out = reinterpret_cast<uint16_t *>(ws + pl.packed[i]);
-      pa.cols = os[i].cols;
-      pa.out_cols = x_stride[i] = x_cols[i] = (uint32_t)round_up(os[i].cols, kTileCols);
-      pa.batch = os[i].batch;
-      pa.x_stride = os[i].x_stride;
-      x[i] = pa.out;
+      pa.x = o[i].x;
+      pa.out = reinterpret_cast<uint16_t *>(work + pl.packed[i]);
+      pa.cols = cols;
+      pa.out_cols = (uint32_t)round_up(cols, kTileCols);
+      pa.batch = o[i].batch;
+      pa.x_stride = o[i].x_stride;
+      x[i] = Activations{pa.out, pa.out_cols, pa.out_cols};
       const uint64_t blocks = ((uint64_t)pa.batch * pa.out_cols + 255) / 256;
       r = launch_pdl(linear_pack_kernel, dim3((uint32_t)(blocks < 592 ? blocks : 592)), 256, 0, s, pa);
       if (r != DF11_OK) return r;
     }
-    if (pl.fused) return launch_fused(ts, os, m, pl, ws, x, x_stride, x_cols, d_err, s);
-    df11_tensor out[DF11_MAX_BATCH];
-    for (int i = 0; i < m; ++i) {
-      out[i] = ts[i];
-      out[i].out_bf16 = reinterpret_cast<uint16_t *>(ws + pl.part[i]);
-    }
-    r = df11_decode_batched(out, m, d_err, stream);
+    if (pl.fused) return launch_fused(w, o, m, pl, work, x, d_err, s);
+    uint16_t *tiles[DF11_MAX_BATCH];
+    for (int i = 0; i < m; ++i) tiles[i] = reinterpret_cast<uint16_t *>(work + pl.part[i]);
+    r = launch_unpack(w, m, tiles, d_err, s);
     for (int i = 0; i < m && r == DF11_OK; ++i)
-      r = launch_gemm(os[i], out[i].out_bf16, x[i], x_stride[i], x_cols[i], d_err, s);
+      r = launch_gemm(o[i], w[i].params.rows, w[i].params.cols, tiles[i], x[i], d_err, s);
     return r;
   });
 }

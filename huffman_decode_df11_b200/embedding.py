@@ -13,8 +13,8 @@ from typing import Optional
 
 import torch
 
-from . import Df11Device, _check, _stream_handle, lib
-from .linear import _aligned_empty, _on_stream, _weight_desc
+from . import Df11Device, TensorDesc, _check, _stream_handle, lib
+from .linear import _aligned_empty, _on_stream
 
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 _IDS = {torch.int32: 0, torch.int64: 1}
@@ -84,6 +84,12 @@ def _embedding_op(d: Df11Device, ids: torch.Tensor, out: torch.Tensor, scale) ->
                        dim, tokens, _IDS[ids.dtype], _TYPES[out.dtype], _check_scale(scale))
 
 
+def _table_desc(d: Df11Device) -> TensorDesc:
+    t = d.desc(torch.empty(0, device=d.device))
+    t.out_bf16 = None
+    return t
+
+
 class EmbeddingPlan:
     """A lookup into fixed buffers (a decode loop's token ids and hidden
     states), prepared once: run() is one library call, and reads the ids as they
@@ -92,7 +98,7 @@ class EmbeddingPlan:
 
     def __init__(self, d: Df11Device, ids: torch.Tensor, out: torch.Tensor, scale: float = 1.0):
         self._op = _embedding_op(d, ids, out, scale)
-        self._desc = _weight_desc(d)
+        self._desc = _table_desc(d)
         self._keep = (d, ids, out)
         self._args = (ctypes.byref(self._desc), ctypes.byref(self._op))
         self._lib = lib()

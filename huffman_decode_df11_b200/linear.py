@@ -9,88 +9,143 @@
 from __future__ import annotations
 
 import ctypes
-from typing import List, Optional, Sequence
+from dataclasses import dataclass
+from typing import List, Optional, Sequence, Union
 
 import numpy as np
 import torch
 
-from . import (Df11Device, TensorDesc, _check, _one_device, _stream_handle, compress,
-               compress_on_device, lib)
+from . import Df11Device, Df11Host, _check, _one_device, _stream_handle, decode, lib, to_device
 
-# Df11Device.interleave of a weight in the linear product's tile order.  Not a
-# row count that interleave_rows takes, so every other product refuses it.
-LINEAR_TILES = 16 * 256 + 64
 TILE_ROWS, TILE_COLS = 16, 64
+LINEAR_TABLE_BYTES = 4 * 8192 + 4 * (33 + 33 + 2) + 256 + 2048
 LINEAR_MAX_BATCH = 1 << 20
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
+class LinearParams(ctypes.Structure):
+    """df11_linear_params: shape and layout of a weight for the linear product."""
+    _fields_ = [(f, ctypes.c_uint32) for f in ("rows", "cols", "unit_tiles", "max_words",
+                                               "stream_rows")]
+
+
+class LinearWeightDesc(ctypes.Structure):
+    """df11_linear_weight: device pointers of a weight and its parameters."""
+    _fields_ = [("streams", ctypes.c_void_p), ("unit_rows", ctypes.c_void_p),
+                ("sign_mantissa", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("params", LinearParams)]
+
+
 class LinearOp(ctypes.Structure):
     """df11_linear: the linear product applied to one compressed weight."""
     _fields_ = ([(f, ctypes.c_void_p) for f in ("x", "y", "bias", "multiplier", "residual")]
-                + [(f, ctypes.c_uint32) for f in ("rows", "cols", "batch", "x_stride", "y_stride",
+                + [(f, ctypes.c_uint32) for f in ("batch", "x_stride", "y_stride",
                                                   "multiplier_stride", "residual_stride")]
                 + [(f, ctypes.c_int32) for f in ("activation", "y_type", "bias_type",
                                                  "multiplier_type", "residual_type")])
 
 
-def _padded(shape):
-    rows, cols = shape
-    return -(-rows // TILE_ROWS) * TILE_ROWS, -(-cols // TILE_COLS) * TILE_COLS
+@dataclass
+class LinearWeight:
+    """A weight (rows x cols) compressed for the linear product, in device
+    memory (compress_linear)."""
+    params: LinearParams
+    streams: torch.Tensor        # int32: the units' 32 bitstreams, word by word
+    unit_rows: torch.Tensor      # int32: first row of 32 words of each unit, and the total
+    sign_mantissa: torch.Tensor  # uint8, padded rows x padded columns
+    table: torch.Tensor          # uint8: decode table
+
+    @property
+    def shape(self) -> tuple:
+        return int(self.params.rows), int(self.params.cols)
+
+    @property
+    def device(self):
+        return self.streams.device
+
+    def compressed_bytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in
+                   (self.streams, self.unit_rows, self.sign_mantissa, self.table))
+
+    def to(self, device) -> "LinearWeight":
+        """The same weight with its buffers on `device` (host memory to keep it, say)."""
+        return LinearWeight(LinearParams.from_buffer_copy(self.params),
+                            *[t.to(device) for t in (self.streams, self.unit_rows,
+                                                     self.sign_mantissa, self.table)])
+
+    def desc(self) -> LinearWeightDesc:
+        return LinearWeightDesc(self.streams.data_ptr(), self.unit_rows.data_ptr(),
+                                self.sign_mantissa.data_ptr(), self.table.data_ptr(), self.params)
 
 
-def tile_linear(w):
-    """A rows x cols matrix (array or tensor of 2-byte words) in the linear
-    product's tile order, flat: padded with zeros to whole tiles of 16 rows and
-    64 columns, and tile after tile along the columns, then down the rows."""
+def compress_linear(w: Union[torch.Tensor, Df11Device, Df11Host], device=None,
+                    stream=None) -> LinearWeight:
+    """Compress a weight (rows x cols) for decode_linear, on the device
+    (df11_linear_weight_begin / _finish).  `w`: BF16 words (bfloat16, int16 or
+    uint16) in device or host memory, or a row-major compressed tensor (decoded on
+    the way); data in host memory go to `device` (default: the current CUDA device)
+    first.  Lossless, like every form of the format; decode_weight gives
+    the words back.  Synchronises the stream."""
+    with torch.cuda.stream(_on_stream(stream)):
+        if isinstance(w, Df11Host):
+            w = to_device(w, device or "cuda")
+        if isinstance(w, Df11Device):
+            if len(w.shape) != 2 or int(getattr(w, "interleave", 1)) != 1:
+                raise ValueError("compress_linear takes a 2-D weight (rows x cols), row-major")
+            with torch.cuda.device(w.device):
+                w = decode(w).view(w.shape)
+        if not isinstance(w, torch.Tensor):
+            w = torch.from_numpy(np.ascontiguousarray(w).view(np.int16))
+        if w.dim() != 2 or 0 in w.shape:
+            raise ValueError("compress_linear takes a 2-D weight (rows x cols)")
+        if w.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+            raise TypeError(f"expected BF16 words (bfloat16, int16 or uint16), got {w.dtype}")
+        if not w.is_cuda:
+            w = w.detach().to(device or "cuda")
+        with torch.cuda.device(w.device):
+            return _compress_linear(w.detach().contiguous(), stream)
+
+
+def _compress_linear(w: torch.Tensor, stream) -> LinearWeight:
     rows, cols = w.shape
-    pr, pc = _padded((rows, cols))
-    if isinstance(w, torch.Tensor):
-        p = w
-        if (pr, pc) != (rows, cols):
-            p = torch.zeros(pr, pc, dtype=w.dtype, device=w.device)
-            p[:rows, :cols] = w
-        v = p.reshape(pr // TILE_ROWS, TILE_ROWS, pc // TILE_COLS, TILE_COLS)
-        return v.permute(0, 2, 1, 3).reshape(-1)
-    p = np.zeros((pr, pc), w.dtype)
-    p[:rows, :cols] = w
-    v = p.reshape(pr // TILE_ROWS, TILE_ROWS, pc // TILE_COLS, TILE_COLS).transpose(0, 2, 1, 3)
-    return np.ascontiguousarray(v).reshape(-1)
+    L, sh, dev = lib(), _stream_handle(stream), w.device
+    if rows >= 1 << 32 or cols >= 1 << 32:
+        raise ValueError("weight too large")
+    units, sm = ctypes.c_uint64(0), ctypes.c_uint64(0)
+    _check(L.df11_linear_sizes(rows, cols, ctypes.byref(units), ctypes.byref(sm)),
+           "df11_linear_sizes")
+    p = LinearParams()
+    unit_rows = torch.empty(units.value, dtype=torch.int32, device=dev)
+    table = torch.empty(LINEAR_TABLE_BYTES, dtype=torch.uint8, device=dev)
+    _check(L.df11_linear_weight_begin(w.data_ptr(), rows, cols, unit_rows.data_ptr(),
+                                      table.data_ptr(), ctypes.byref(p), sh),
+           "df11_linear_weight_begin")
+    per_row = -(-(-(-cols // TILE_COLS)) // p.unit_tiles)
+    out = LinearWeight(
+        params=p, streams=torch.empty(p.stream_rows * 32, dtype=torch.int32, device=dev),
+        unit_rows=unit_rows[: -(-rows // TILE_ROWS) * per_row + 1].clone(),
+        sign_mantissa=torch.empty(sm.value, dtype=torch.uint8, device=dev), table=table)
+    d = out.desc()
+    _check(L.df11_linear_weight_finish(w.data_ptr(), ctypes.byref(d), sh),
+           "df11_linear_weight_finish")
+    return out
 
 
-def untile_linear(flat, shape):
-    """The inverse of tile_linear: the decoded words of a compressed weight in
-    tile order back to its rows x cols matrix."""
-    rows, cols = shape
-    pr, pc = _padded(shape)
-    v = flat.reshape(pr // TILE_ROWS, pc // TILE_COLS, TILE_ROWS, TILE_COLS)
-    v = v.permute(0, 2, 1, 3) if isinstance(v, torch.Tensor) else v.transpose(0, 2, 1, 3)
-    return v.reshape(pr, pc)[:rows, :cols]
-
-
-def compress_linear(w, chunk_bytes: int = 24, threads: int = 0, stream=None):
-    """Compress a weight (rows x cols BF16) for decode_linear, in its tile
-    order.  A CUDA tensor is compressed on its device (compress_on_device) and
-    gives a Df11Device; host data are compressed on the host (compress) and
-    give a Df11Host, which to_device takes on."""
-    if w.ndim != 2 or 0 in w.shape:
-        raise ValueError("compress_linear takes a 2-D weight (rows x cols)")
-    shape = tuple(int(n) for n in w.shape)
-    if isinstance(w, torch.Tensor) and w.is_cuda:
-        if stream is None:
-            d = compress_on_device(tile_linear(w), chunk_bytes=chunk_bytes)
-        else:
-            with torch.cuda.stream(stream):
-                d = compress_on_device(tile_linear(w), chunk_bytes=chunk_bytes, stream=stream)
-    else:
-        if isinstance(w, torch.Tensor):
-            w = w.detach().contiguous().view(torch.int16).numpy()
-        d = compress(tile_linear(np.asarray(w)), chunk_bytes, threads=threads)
-    d.shape = shape
-    d.interleave = LINEAR_TILES
-    return d
+def decode_weight(d: LinearWeight, err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The BF16 matrix (rows x cols) of a weight compressed by compress_linear, bit for
+    bit (df11_linear_unpack).  Asynchronous on `stream` (default: the current stream)."""
+    rows, cols = d.shape
+    pr, pc = -(-rows // TILE_ROWS) * TILE_ROWS, -(-cols // TILE_COLS) * TILE_COLS
+    with torch.cuda.device(d.device), torch.cuda.stream(_on_stream(stream)):
+        tiles = torch.empty(pr * pc, dtype=torch.bfloat16, device=d.device)
+        desc = d.desc()
+        _check(lib().df11_linear_unpack(ctypes.byref(desc), tiles.data_ptr(),
+                                        err.data_ptr() if err is not None else None,
+                                        _stream_handle(stream)), "df11_linear_unpack")
+        v = tiles.view(pr // TILE_ROWS, pc // TILE_COLS, TILE_ROWS, TILE_COLS)
+        return v.permute(0, 2, 1, 3).reshape(pr, pc)[:rows, :cols].contiguous()
 
 
 def _operand(name, t, shape, device, dtypes):
@@ -109,9 +164,9 @@ def _operand(name, t, shape, device, dtypes):
     return t.data_ptr(), stride
 
 
-def _linear_op(d: Df11Device, x, y, bias, activation, multiplier, residual) -> LinearOp:
-    if int(getattr(d, "interleave", 1)) != LINEAR_TILES:
-        raise ValueError("decode_linear needs weights compressed by compress_linear")
+def _linear_op(d: LinearWeight, x, y, bias, activation, multiplier, residual) -> LinearOp:
+    if not isinstance(d, LinearWeight):
+        raise TypeError("decode_linear needs weights compressed by compress_linear")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation {activation!r}: expected one of {', '.join(ACTIVATIONS)}")
     rows, cols = d.shape
@@ -120,7 +175,7 @@ def _linear_op(d: Df11Device, x, y, bias, activation, multiplier, residual) -> L
     tokens, wide = x.shape[0], tuple(_TYPES)
     if tokens > LINEAR_MAX_BATCH:
         raise ValueError(f"at most {LINEAR_MAX_BATCH} tokens per call")
-    op = LinearOp(rows=rows, cols=cols, batch=tokens, activation=ACTIVATIONS[activation])
+    op = LinearOp(batch=tokens, activation=ACTIVATIONS[activation])
     op.x, op.x_stride = _operand("x", x, (tokens, cols), d.device, (torch.bfloat16, torch.int16))
     op.y, op.y_stride = _operand("y", y, (tokens, rows), d.device, wide)
     op.y_type = _TYPES[y.dtype]
@@ -167,7 +222,7 @@ class LinearPlan:
     and must not overlap on the GPU; plans on several streams at once are
     plans of their own."""
 
-    def __init__(self, ds: Sequence[Df11Device], xs: Sequence[torch.Tensor],
+    def __init__(self, ds: Sequence[LinearWeight], xs: Sequence[torch.Tensor],
                  ys: Sequence[torch.Tensor], biases=None, activations=None, multipliers=None,
                  residuals=None):
         n = len(ds)
@@ -178,7 +233,7 @@ class LinearPlan:
         ops = [_linear_op(*a) for a in zip(ds, xs, ys, bs, acts, ms, rs)]
         self._n = n
         self._keep = (list(ds), list(xs), list(ys), bs, ms, rs)
-        self._descs = (TensorDesc * max(n, 1))(*[_weight_desc(d) for d in ds])
+        self._descs = (LinearWeightDesc * max(n, 1))(*[d.desc() for d in ds])
         self._ops = (LinearOp * max(n, 1))(*ops)
         self._lib = lib()
         self._device = _one_device(ds) if n else None
@@ -213,12 +268,6 @@ class LinearPlan:
         return self._keep[2]
 
 
-def _weight_desc(d: Df11Device) -> TensorDesc:
-    t = d.desc(torch.empty(0, device=d.device))
-    t.out_bf16 = None
-    return t
-
-
 def _on_stream(stream):
     """A torch stream to allocate a call's buffers on (None: the current one)."""
     if stream is None or hasattr(stream, "cuda_stream"):
@@ -226,7 +275,7 @@ def _on_stream(stream):
     return torch.cuda.ExternalStream(int(stream))
 
 
-def decode_linear(ds: Sequence[Df11Device], xs: Sequence[torch.Tensor],
+def decode_linear(ds: Sequence[LinearWeight], xs: Sequence[torch.Tensor],
                   ys: Optional[Sequence[torch.Tensor]] = None, biases=None, activations=None,
                   multipliers=None, residuals=None, out_dtype: torch.dtype = torch.bfloat16,
                   err: Optional[torch.Tensor] = None, stream=None) -> List[torch.Tensor]:

@@ -263,6 +263,61 @@ df11_status df11_decode_gemm(const df11_tensor *tensors, const df11_gemv *ops, i
 /* Most tokens of one linear product. */
 #define DF11_LINEAR_MAX_BATCH (1u << 20)
 
+/* Bytes of a weight's decode table. */
+#define DF11_LINEAR_TABLE_BYTES (4 * 8192 + 4 * (33 + 33 + 2) + 256 + 2048)
+
+/* A weight (rows x cols) in the compressed form of the linear product, written
+ * by df11_linear_weight_begin and _finish: the same coding as the other tensors' (a canonical
+ * Huffman code of the exponents, sign and mantissa kept as a byte), but cut by
+ * elements, so that 32 streams of a fixed number of elements lie side by
+ * side.  The matrix, padded with zeros, is cut into tiles of 16 rows and 64
+ * columns, and each block of 16 rows into units of unit_tiles tiles (the last may be
+ * shorter).  Stream l (0 .. 31) of a unit codes, tile after tile, the 16 columns from
+ * 16 (l mod 4) on of row l/4 and then of row l/4 + 8. */
+typedef struct df11_linear_params {
+  uint32_t rows, cols;
+  uint32_t unit_tiles;  /* tiles per unit: 4, 2 or 1 */
+  uint32_t max_words;   /* 32-bit words of the longest stream */
+  uint32_t stream_rows; /* rows of 32 words (one per stream) in `streams` */
+} df11_linear_params;
+
+typedef struct df11_linear_weight {
+  const uint32_t *streams;      /* 16-byte aligned, stream_rows * 32 words: a unit's streams word
+                                   by word, first bit = bit 31 */
+  const uint32_t *unit_rows;    /* first row of each unit, and the total at the end */
+  const uint8_t *sign_mantissa; /* 16-byte aligned: per tile 16 bytes of each stream for rows
+                                   0 .. 7, then for rows 8 .. 15 */
+  const void *table;            /* 16-byte aligned, DF11_LINEAR_TABLE_BYTES */
+  df11_linear_params params;
+} df11_linear_weight;
+
+/* Sizes of a rows x cols weight's buffers that do not depend on its values:
+ * elements (uint32) of unit_rows and bytes of sign_mantissa. */
+df11_status df11_linear_sizes(uint32_t rows, uint32_t cols, uint64_t *unit_rows_count,
+                              uint64_t *sign_mantissa_bytes);
+
+/*
+ * Compress a weight on the device, in two calls.  d_w: rows x cols BF16 words,
+ * contiguous (2-byte aligned; 16-byte alignment and columns in eights are read
+ * faster).  The first call counts the exponents, computes the code, writes
+ * unit_rows and the table (device buffers, sizes above) and fills *params; it
+ * synchronises the stream.  The second one, with a weight whose buffers have the
+ * sizes that params gives, writes streams and sign_mantissa, asynchronously.
+ * DF11_ERR_INVALID for an empty matrix, DF11_ERR_TOO_LARGE for 2^32 elements or
+ * more after padding.
+ */
+df11_status df11_linear_weight_begin(const uint16_t *d_w, uint32_t rows, uint32_t cols,
+                                     uint32_t *unit_rows, void *table, df11_linear_params *params,
+                                     df11_stream_t stream);
+df11_status df11_linear_weight_finish(const uint16_t *d_w, const df11_linear_weight *weight,
+                                      df11_stream_t stream);
+
+/* Decode a weight into its tiles (BF16, bit-identical): for each block of 16 rows
+ * and each group of 64 columns the 16 rows' 64 elements one after another, padding
+ * included.  `tiles`: 16-byte aligned device memory.  Asynchronous. */
+df11_status df11_linear_unpack(const df11_linear_weight *weight, uint16_t *tiles, int32_t *d_err,
+                               df11_stream_t stream);
+
 /* The linear product applied to one compressed weight:
  * y[t][r] = act(sum over c of W[r][c] x[t][c] + bias[r]) * multiplier[t][r]
  *           + residual[t][r]. */
@@ -273,7 +328,6 @@ typedef struct df11_linear {
   const void *multiplier; /* `batch` rows of `rows` elements, or NULL */
   const void *residual;   /* `batch` rows of `rows` elements, or NULL; may be y
                              itself (same stride and type) */
-  uint32_t rows, cols;    /* of the weight as the model has it */
   uint32_t batch;         /* tokens: 0 (nothing is done) .. DF11_LINEAR_MAX_BATCH */
   uint32_t x_stride, y_stride, multiplier_stride, residual_stride; /* elements between rows */
   int32_t activation;     /* DF11_ACT_* */
@@ -281,20 +335,13 @@ typedef struct df11_linear {
 } df11_linear;
 
 /*
- * The linear product of up to any number of weights, in launches of
- * DF11_MAX_BATCH.  Each tensor holds a weight in the tile order of this
- * product: rows padded with zeros to a multiple of 16 and columns to a
- * multiple of 64, and for each block of 16 rows and each group of 64 columns the
- * 16 rows' 64 elements one after another; params.n is the padded count.  Needs
- * chunk counts, a decode table, T = 256 and C = 8, 16 or 24, one C per call;
- * out_bf16 is not used (may be NULL).
+ * The linear product of any number of weights, in launches of DF11_MAX_BATCH.
  *   Sums run in fp32 (products of BF16 are exact there) in an order that the
  * sizes and the device fix, so a call repeats bit for bit; bias, activation,
- * multiplier and residual are applied in fp32 and the result is rounded once.  A
- * token's row of x with an infinity gives NaN or an infinity in every output of
- * that token.  Up to 32 tokens (the most of the launch's tensors) the weights
- * are decoded and multiplied in one kernel and never written; beyond, they are
- * decoded into the workspace and multiplied on the tensor cores.
+ * multiplier and residual are applied in fp32 and the result is rounded once.  Up
+ * to 32 tokens (the most of the launch's weights) the weights are decoded
+ * and multiplied in one kernel and never written; beyond, they are decoded into
+ * the workspace and multiplied on the tensor cores.
  *   `workspace`: df11_linear_workspace bytes of device memory, 256-byte aligned,
  * that no other work uses until this call's work is done; nothing is kept in
  * it between calls.  y may not overlap x, the multiplier (unless it is the same
@@ -302,18 +349,18 @@ typedef struct df11_linear {
  *   Same conventions as df11_decode_batched otherwise (asynchronous, no
  * allocation, device-detected errors in d_err).  DF11_ERR_INVALID for sizes,
  * strides, types or activations outside the rules and for a workspace that is
- * too small, DF11_ERR_UNSUPPORTED for a tensor without counts or table or of
- * another chunk size, DF11_ERR_TOO_LARGE above DF11_LINEAR_MAX_BATCH.
+ * too small, DF11_ERR_FORMAT for parameters that no weight has,
+ * DF11_ERR_TOO_LARGE above DF11_LINEAR_MAX_BATCH.
  */
-df11_status df11_decode_linear(const df11_tensor *tensors, const df11_linear *ops, int count,
+df11_status df11_decode_linear(const df11_linear_weight *weights, const df11_linear *ops, int count,
                                void *workspace, size_t workspace_bytes, int32_t *d_err,
                                df11_stream_t stream);
 
 /* Bytes of workspace that df11_decode_linear needs for this call on the current
  * device (it depends on the sizes and on how many thread blocks the device holds;
  * pointers are checked as in the call, but nothing is queued). */
-df11_status df11_linear_workspace(const df11_tensor *tensors, const df11_linear *ops, int count,
-                                  size_t *bytes);
+df11_status df11_linear_workspace(const df11_linear_weight *weights, const df11_linear *ops,
+                                  int count, size_t *bytes);
 
 /* ---------------------------------------------------------------------- */
 /* The token embedding on a compressed table, and the table's gradient.    */

@@ -107,8 +107,8 @@ def test_refusals_of_the_binding():
         with pytest.raises(exc, match=match):
             embedding._embedding_op(d, ids, out, scale)
 
-    tiles = df11.to_device(df11.compress_linear(w), "cpu", decode_table=False)
-    bad(ValueError, "row-major", d=tiles)
+    rows = df11.compress(torch.randn(32, 64).to(bf), interleave=16)
+    bad(ValueError, "row-major", d=df11.to_device(rows, "cpu", decode_table=False))
     flat = df11.to_device(df11.compress(w.view(-1)), "cpu", decode_table=False)
     bad(ValueError, "2-D", d=flat)
     bad(TypeError, "ids", ids=ids.to(torch.int16))

@@ -100,15 +100,6 @@ def test_product_alone(rows, cols, tokens):
         _check(w, x, y)
 
 
-@pytest.mark.parametrize("chunk_bytes", [8, 16, 24])
-@pytest.mark.parametrize("tokens", [1, 12, 30, 40])
-def test_chunk_sizes(chunk_bytes, tokens):
-    w = _bf16((200, 1000), 0.02, 3)
-    x = _bf16((tokens, 1000), 1.0, 4).cuda()
-    y, = _run([df11.compress_linear(w.cuda(), chunk_bytes)], [x], out_dtype=torch.float32)
-    _check(w, x, y)
-
-
 @pytest.mark.parametrize("activation", ["none", "relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("tokens", [2, 70])
 @pytest.mark.parametrize("rows", [320, 333])
@@ -282,31 +273,159 @@ def test_two_plans_at_once_on_two_streams():
         _check(w, x, p.outs[0])
 
 
-@pytest.mark.parametrize("tokens", [4, 40])
-def test_corrupt_counts_are_flagged_and_the_next_call_is_right(tokens):
-    w = _bf16((256, 1024), 0.03, 1)
-    d = df11.compress_linear(w.cuda())
-    x = _bf16((tokens, 1024), 1.0, 2).cuda()
-    good = int(d.chunk_counts[40])
-    d.chunk_counts[40] = good + 1
+@pytest.mark.parametrize("tokens", [2, 40])
+def test_infinities_follow_the_formula(tokens):
+    # an infinite activation reaches every output of its token with the sign of its weight,
+    # NaN where the weight is zero, and no other token
+    w = _bf16((80, 200), 0.1, 1)
+    w[7, 130] = 0.0
+    x = _bf16((tokens, 200), 1.0, 2)
+    x[1, 130] = float("inf")
+    y, = _run([df11.compress_linear(w.cuda())], [x.cuda()], out_dtype=torch.float32)
+    y = y.cpu()
+    assert torch.isnan(y[1, 7])
+    rest = [r for r in range(80) if r != 7]
+    assert torch.equal(y[1, rest], torch.sign(w[rest, 130].float()) * float("inf"))
+    assert torch.isfinite(y[[t for t in range(tokens) if t != 1]]).all()
+
+
+def _lane_streams(w):
+    """The streams of a compressed weight decoded one codeword at a time, in plain
+    Python: the words (padded rows x padded columns) they stand for."""
+    p = w.params
+    rows, cols = -(-p.rows // 16) * 16, -(-p.cols // 64) * 64
+    words = w.streams.cpu().numpy().view(np.uint32).reshape(-1, 32)
+    first = w.unit_rows.cpu().numpy()
+    sm = w.sign_mantissa.cpu().numpy().reshape(rows // 16, cols // 64, 2, 32, 16)
+    # the code, from its stored codewords and lengths
+    tail = w.table.cpu().numpy()[-2048:].view(np.uint32)
+    book = {(int(tail[256 + e]), int(tail[e]) >> (32 - int(tail[256 + e]))): e
+            for e in range(256) if tail[256 + e]}
+    out = np.zeros((rows, cols), np.uint16)
+    per_row = -(-(cols // 64) // p.unit_tiles)
+    assert len(first) == rows // 16 * per_row + 1 and first[-1] == p.stream_rows
+    assert np.diff(first).max() == p.max_words
+    for u in range(len(first) - 1):
+        rb, k = divmod(u, per_row)
+        for lane in range(32):
+            bits = "".join(f"{x:032b}" for x in words[first[u]:first[u + 1], lane])
+            at = 0
+            for cg in range(k * p.unit_tiles, min((k + 1) * p.unit_tiles, cols // 64)):
+                for h in range(2):
+                    for j in range(16):
+                        n = 1
+                        while (n, int(bits[at:at + n], 2)) not in book:
+                            n += 1
+                        e = book[n, int(bits[at:at + n], 2)]
+                        at += n
+                        b = int(sm[rb, cg, h, lane, j])
+                        out[16 * rb + 8 * h + lane // 4, 64 * cg + 16 * (lane % 4) + j] = \
+                            (b & 0x80) << 8 | e << 7 | b & 0x7F
+            assert "1" not in bits[at:] and len(bits) - at >= 0
+    return out
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (20, 300), (48, 130)])
+def test_the_compressed_form_is_the_stated_one(rows, cols):
+    w = _bf16((rows, cols), 0.05, rows)
+    c = df11.compress_linear(w.cuda())
+    got = _lane_streams(c)
+    want = np.zeros(got.shape, np.uint16)
+    want[:rows, :cols] = w.view(torch.int16).numpy().view(np.uint16)
+    assert np.array_equal(got, want)
+
+
+ROUND_TRIPS = ["gaussian", "one exponent", "mix", "every word", "long codes", "uneven rows"]
+
+
+@pytest.mark.parametrize("kind", ROUND_TRIPS)
+@pytest.mark.parametrize("rows,cols", [(16, 64), (1, 1), (33, 1000), (513, 4160), (300, 65)])
+def test_round_trip(kind, rows, cols):
+    n = rows * cols
+    if kind == "gaussian":
+        w = _bf16((n,), 0.02, 1)
+    elif kind == "every word":
+        w = torch.arange(n, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    elif kind == "long codes":      # codewords up to 32 bits
+        w = workloads.fibonacci_exponents(seed=2)[:n].clone().view(torch.bfloat16)
+    elif kind == "uneven rows":     # rows whose streams are far longer than others'
+        w = torch.ones(n, dtype=torch.bfloat16)
+        w[n // 2:] = workloads.gaussian_bf16(n - n // 2, 1.0, 4).view(torch.bfloat16)
+    else:
+        w = _words(kind, n)
+    w = w.view(rows, cols)
+    c = df11.compress_linear(w.cuda())
     err = df11.new_error_word()
-    df11.decode_linear([d], [x], err=err)
+    got = df11.decode_weight(c, err=err)
     torch.cuda.synchronize()
-    with pytest.raises(df11.Df11Error):
-        df11.check_device_error(err)
-    d.chunk_counts[40] = good
-    y, = _run([d], [x], out_dtype=torch.float32)
+    df11.check_device_error(err)
+    assert torch.equal(got.cpu().view(torch.int16), w.view(torch.int16))
+    assert c.shape == (rows, cols) and c.params.max_words <= 40
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_long_codes_in_the_product(tokens):
+    w = workloads.fibonacci_exponents(seed=2)[:208 * 1280].clone().view(torch.bfloat16)
+    w = w.view(208, 1280)
+    w = torch.where(w.float().abs() < 1e15, w, torch.zeros_like(w))   # finite sums
+    x = _bf16((tokens, 1280), 1.0, 2).cuda()
+    y, = _run([df11.compress_linear(w.cuda())], [x], out_dtype=torch.float32)
     _check(w, x, y)
 
 
-def test_decoding_the_tiles_gives_the_weight_back():
+def test_sources_of_a_weight():
     w = _bf16((77, 150), 0.03, 1)
-    d = df11.compress_linear(w.cuda())
-    out = df11.decode(d)
-    assert torch.equal(df11.untile_linear(out.view(torch.int16), (77, 150)).cpu(),
-                       w.view(torch.int16))
-    h = df11.compress_linear(w)                       # on the host: the same tensor
-    assert h.shape == (77, 150) and h.interleave == df11.LINEAR_TILES
-    assert np.array_equal(h.bitstream, d.bitstream.cpu().numpy())
-    y, = _run([df11.to_device(h)], [_bf16((2, 150), 1.0, 5).cuda()])
-    _check(w, _bf16((2, 150), 1.0, 5), y)
+    ref = df11.compress_linear(w.cuda())
+    for other in (w, w.cuda().view(torch.int16), w.cuda().t().contiguous().t(),
+                  df11.compress(w), df11.compress_on_device(w.cuda()),
+                  w.view(torch.int16).numpy()):
+        c = df11.compress_linear(other)
+        assert c.shape == (77, 150)
+        assert torch.equal(c.streams, ref.streams) and torch.equal(c.table, ref.table)
+        assert torch.equal(c.unit_rows, ref.unit_rows)
+        assert torch.equal(c.sign_mantissa, ref.sign_mantissa)
+    # kept in host memory and back
+    x = _bf16((2, 150), 1.0, 5)
+    y, = _run([ref.to("cpu").to("cuda")], [x.cuda()])
+    _check(w, x, y)
+    # a view that is not 16-byte aligned
+    buf = torch.zeros(77 * 160 + 1, dtype=torch.bfloat16, device="cuda")
+    odd = buf[1:1 + 77 * 150].view(77, 150)
+    odd.copy_(w)
+    assert torch.equal(df11.compress_linear(odd).streams, ref.streams)
+
+
+def test_size_is_about_eleven_bits_per_weight():
+    c = df11.compress_linear(_bf16((2048, 4096), 1 / 64, 3).cuda())
+    bits = 8 * c.compressed_bytes() / (2048 * 4096)
+    assert 10.5 < bits < 11.3, bits
+
+
+@pytest.mark.parametrize("tokens", [4, 40])
+@pytest.mark.parametrize("field", ["unit_rows", "table", "streams"])
+def test_corrupt_weights_are_flagged_and_the_next_call_is_right(tokens, field):
+    # rows of units out of order, a table of codewords that do not exist, streams of
+    # the longest codewords: every one is caught by a check of the kernel's own
+    w = workloads.adversarial_mix(256 * 1024, seed=5).view(torch.bfloat16).view(256, 1024)
+    c = df11.compress_linear(w.cuda())
+    assert int(c.params.unit_tiles) == 4
+    x = _bf16((tokens, 1024), 1.0, 2).cuda()
+    good = c.table.clone(), c.unit_rows.clone(), c.streams.clone()
+    if field == "unit_rows":
+        c.unit_rows[5] = 1 << 28
+    elif field == "table":
+        t = c.table.view(torch.int32)
+        t[:8192] = -(1 << 30)                 # every lookup a long codeword
+        t[8192 + 33:8192 + 66] = 0            # and no codeword of any length
+    else:
+        c.streams.fill_(-1)                   # the longest codeword, all along
+    err = df11.new_error_word()
+    df11.decode_linear([c], [x], err=err)
+    torch.cuda.synchronize()
+    with pytest.raises(df11.Df11Error):
+        df11.check_device_error(err)
+    c.table.copy_(good[0])
+    c.unit_rows.copy_(good[1])
+    c.streams.copy_(good[2])
+    y, = _run([c], [x], out_dtype=torch.float32)
+    _check(w, x, y)
