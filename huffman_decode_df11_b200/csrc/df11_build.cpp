@@ -253,11 +253,17 @@ std::vector<uint32_t> build_tables(const uint8_t len[256], const uint32_t code[2
 
 }  // namespace
 
+int df11_internal::limited_code(const uint64_t hist[256], int limit, uint8_t len[256],
+                                uint32_t code[256]) {
+  int longest = huffman_depths(hist, len);
+  if (longest > limit) longest = package_merge(hist, limit, len);
+  canonical(len, code);
+  return longest;
+}
+
 int df11_internal::codebook(const uint64_t hist[256], uint8_t len[256], uint32_t code[256],
                             std::vector<uint32_t> &luts) {
-  int longest = huffman_depths(hist, len);
-  if (longest > kMaxLen) longest = package_merge(hist, kMaxLen, len);
-  canonical(len, code);
+  const int longest = limited_code(hist, kMaxLen, len, code);
   luts = build_tables(len, code);
   return longest;
 }

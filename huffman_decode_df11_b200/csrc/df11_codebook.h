@@ -14,4 +14,8 @@ namespace df11_internal {
 int codebook(const uint64_t hist[256], uint8_t len[256], uint32_t code[256],
              std::vector<uint32_t> &luts);
 
+// Code lengths and canonical codewords alone, limited to `limit` bits (8 at least, so
+// that any 256 symbols have a code).  Returns the longest code length.
+int limited_code(const uint64_t hist[256], int limit, uint8_t len[256], uint32_t code[256]);
+
 }  // namespace df11_internal

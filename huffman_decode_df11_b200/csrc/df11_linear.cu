@@ -1,11 +1,11 @@
 // df11_linear.cu -- the linear product of a model's layer on compressed weights:
 // y = act(W x + bias) * multiplier + residual, for any number of tokens.
 //
-// The weight has a compressed form of its own (df11_linear_weight_begin), with the same
-// code as the decode kernels' format (a Huffman code of the exponents, sign and mantissa
-// kept as a byte), but cut by elements instead of bits.  The matrix, padded with zeros
-// to whole tiles of 16 rows and 64 columns, is taken in units of up to four tiles along a
-// block of 16 rows.  One warp decodes a unit: lane l has a bitstream of its own
+// The weight has a compressed form of its own (df11_linear_weight_begin): like the decode
+// kernels' format a Huffman code of the exponents, with sign and mantissa kept as a byte,
+// but limited to 8-bit codewords and cut by elements instead of bits.  The matrix, padded with zeros
+// to whole tiles of 16 rows and 64 columns, is taken in units of four tiles along a
+// block of 16 rows (the last one may be shorter).  One warp decodes a unit: lane l has a bitstream of its own
 // with the 32 elements of every tile that belong to it, rows l/4 and l/4 + 8 and the 16
 // columns from 16 (l mod 4) on.  Those are the A fragments of four m16n8k16 products,
 // so a decoded weight goes from the table to the tensor core in registers: no
@@ -39,36 +39,31 @@ using namespace df11_internal;
 namespace {
 
 constexpr uint32_t kTileRows = 16, kTileCols = 64, kTileElems = kTileRows * kTileCols;
-constexpr uint32_t kMaxUnitTiles = 4;
+constexpr uint32_t kUnitTiles = 4;
 constexpr int kWarps = 16;  // warps of a thread block: a group of 16 row blocks, one each
 constexpr int kThreads = 32 * kWarps;
-// Longest stream of a lane in a unit, in words, before the builder takes shorter
-// units: two units per warp are in shared memory (16 warps: 160 KB at most).
-constexpr uint32_t kMaxWords = 40;
 
-// ---- the decode table -----------------------------------------------------------
+// ---- the code and its decode table ------------------------------------------------
 //
-// Pair table, indexed by the next kPairBits bits: two codewords when both lie inside
-// (bits 0-4 their length together, bits 8-15 and 16-23 the exponents, rotated right by
-// one bit, bits 24-28 the first one's length); bit 31 alone: only the first one does;
-// bits 31 and 30: not even that.  After it, for those, the canonical code: per length
-// 1 .. 32 the first codeword, the count and the index of its first symbol, and the
-// symbols (rotated) in code order; and the code itself, for the builder.
-// Of Gaussian weights 0.4% of the pairs exceed 13 bits (0.7% 12 bits, 0.2% 14 bits).
-constexpr int kPairBits = 13;
+// Codewords of at most 8 bits: 0.08 bits longer on average than the unlimited code of
+// Gaussian weights, but two codewords nearly always lie inside kPairBits bits.  Pair table,
+// indexed by the next kPairBits bits: both when they do (bits 0-4 their length
+// together, bits 8-15 and 16-23 the exponents, rotated right by one bit, bits 24-27 the
+// first one's length); otherwise bit 31 is set and only the first one is there (bits 0-4
+// its length).  0.03% of the pairs of Gaussian weights exceed 13 bits, 0.08% 12 bits;
+// with unlimited codewords 0.2% and 0.4%, and a warp waits for any of its 32 lanes.
+constexpr int kMaxLength = 8;
+constexpr int kPairBits = 12;
 constexpr uint32_t kPairs = 1u << kPairBits;
+constexpr uint32_t kFirstOnly = 0x80000000u;
+// Words of a lane's stream in a unit, at most.
+constexpr uint32_t kMaxWords = kUnitTiles * 32u * kMaxLength / 32u;
 struct LinearTable {
   uint32_t pair[kPairs];
-  uint32_t first[33];
-  uint32_t range[33];  // count << 16 | index of the first symbol
-  uint32_t pad[2];
-  uint8_t sym[256];
   uint32_t code[256];    // by exponent: the codeword, left-aligned, and its length
   uint32_t length[256];  // (for the builder)
 };
 static_assert(sizeof(LinearTable) == DF11_LINEAR_TABLE_BYTES, "table layout");
-
-constexpr uint32_t kBothFlag = 0x80000000u, kDeepFlag = 0x40000000u;
 
 // ---- epilogue ---------------------------------------------------------------
 
@@ -162,97 +157,61 @@ struct LWeight {
   const uint32_t *unit_rows;      // first row of each unit
   const uint8_t *sign_mantissa;   // per tile: rows 0-7 (16 bytes per lane), rows 8-15
   const LinearTable *table;
-  uint32_t rbs, ncg;              // row blocks, tiles per row block
-  uint32_t unit_tiles, upr;       // tiles per unit, units per row block
+  uint32_t rbs, ncg, upr;         // row blocks, tiles and units per row block
   uint32_t max_words, stream_rows;
 };
 
 // Two words of the lane's stream with the next bit at bit 31 - (p & 31) of `a`, and
-// where the word after them is.  Bit 5 of p is zero between steps; the bits above it
-// are not kept clean.
+// where the word after them is.  Bit 5 of p is zero between steps; bits 8 and up are
+// not kept clean (the table's entries are added whole).
 struct LaneBits {
   uint32_t a, b, p, addr;
+  // past a word: without a branch, since in most steps some lane has reached its end
   __device__ __forceinline__ void refill() {
-    a = b;
-    b = lds32(addr);
-    addr += 128u;
+    asm volatile(
+        "{\n .reg .pred q;\n .reg .b32 t;\n"
+        " and.b32 t, %2, 32;\n setp.ne.b32 q, t, 0;\n"
+        " @q mov.b32 %0, %1;\n @q ld.shared.b32 %1, [%3];\n"
+        " @q add.s32 %3, %3, 128;\n @q xor.b32 %2, %2, 32;\n}\n"
+        : "+r"(a), "+r"(b), "+r"(p), "+r"(addr));
   }
+  __device__ __forceinline__ uint32_t window() const { return __funnelshift_l(b, a, p); }
 };
 
-// A codeword longer than the pair table's index: canonical search by length.
-// No match (inconsistent data): length 1, and bit 31 set in the result.
-__device__ __noinline__ uint32_t deep_symbol(uint32_t win, const LinearTable *t) {
-  for (uint32_t len = kPairBits + 1; len <= 32; ++len) {
-    const uint32_t k = (win >> (32 - len)) - __ldg(t->first + len), r = __ldg(t->range + len);
-    if (k < (r >> 16)) return (uint32_t)__ldg(t->sym + (((r & 0xFFFFu) + k) & 255u)) | len << 8;
-  }
-  return 0x80000100u;
+// A value that the compiler keeps in a register instead of computing it again: it would
+// take the shared-memory window's base anew for every lookup.
+__device__ __forceinline__ uint32_t keep(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
 }
 
-// Two symbols one after another, where the pair table has not both: the state moves on
-// past them, and the result has the pair's exponents with a length of zero.
-__device__ __forceinline__ uint32_t slow_pair(LaneBits &s, uint32_t pairs, const LinearTable *t,
-                                              uint32_t &bad) {
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t win = __funnelshift_l(s.b, s.a, s.p);
-    const uint32_t e = lds32(pairs + ((win >> (32 - kPairBits)) << 2));
-    uint32_t sym = (e >> 8) & 0xFFu, len = (e >> 24) & 31u;
-    if (e >= (kBothFlag | kDeepFlag)) {
-      const uint32_t d = deep_symbol(win, t);
-      bad |= d >> 31;
-      sym = d & 0xFFu;
-      len = (d >> 8) & 63u;
-    }
-    r |= sym << (8 * i + 8);
-    s.p = (s.p & 31u) + len;
-    if (s.p & 32u) {
-      s.refill();
-      s.p ^= 32u;
-    }
-  }
-  return r;
+// The pair table's entry of a window; the table starts at a multiple of its size, so that
+// its address takes no addition.
+__device__ __forceinline__ uint32_t look_up(uint32_t pairs, uint32_t window) {
+  return lds32(((window >> (30 - kPairBits)) & (4u * kPairs - 4u)) | pairs);
 }
 
 // The next four exponents (rotated), first in bits 0-7.  One 32-bit window serves both
-// lookups: two pairs take at most 26 bits.
-__device__ __forceinline__ uint32_t next4(LaneBits &s, uint32_t pairs, const LinearTable *t,
-                                          uint32_t &bad) {
-  const uint32_t w = __funnelshift_l(s.b, s.a, s.p);
-  uint32_t e1 = lds32(pairs + ((w >> (32 - kPairBits)) << 2));
-  uint32_t w2 = __funnelshift_l(0u, w, e1);  // shifts by the low five bits: the length
-  if ((int32_t)e1 < 0) {
-    e1 = slow_pair(s, pairs, t, bad);
-    w2 = __funnelshift_l(s.b, s.a, s.p);
-  }
-  uint32_t e2 = lds32(pairs + ((w2 >> (32 - kPairBits)) << 2));
-  if ((int32_t)e2 < 0) {
-    s.p = (s.p & 31u) + (e1 & 31u);
-    if (s.p & 32u) {
-      s.refill();
-      s.p ^= 32u;
-    }
-    e1 &= ~31u;
-    e2 = slow_pair(s, pairs, t, bad);
-  }
-  s.p += e1 + e2;
-  if (s.p & 32u) {
+// lookups: two pairs take at most 2 kPairBits bits.
+__device__ __forceinline__ uint32_t next4(LaneBits &s, uint32_t pairs) {
+  const uint32_t w = s.window();
+  const uint32_t e1 = look_up(pairs, w);
+  // shifts by the low five bits: the length
+  const uint32_t e2 = look_up(pairs, __funnelshift_l(0u, w, e1));
+  if ((int32_t)(e1 | e2) >= 0) {
+    s.p += e1 + e2;
     s.refill();
-    s.p ^= 32u;
+    return __byte_perm(e1, e2, 0x6521);
   }
-  return __byte_perm(e1, e2, 0x6521);
-}
-
-// A unit's streams from global memory into the warp's buffer `dst` (max_words rows);
-// false if the table of rows is inconsistent.
-__device__ __forceinline__ bool fetch_unit(const LWeight &w, uint32_t unit, uint32_t dst,
-                                           uint32_t bar) {
-  const uint32_t r0 = __ldg(w.unit_rows + unit), r1 = __ldg(w.unit_rows + unit + 1);
-  if (r1 < r0 || r1 - r0 > w.max_words || r1 > w.stream_rows) return false;
-  mbar_arrive_expect_tx(bar, (r1 - r0) * 128u);
-  if (r1 > r0) bulk_g2s(dst, w.streams + (size_t)r0 * 32u, (r1 - r0) * 128u, bar);
-  return true;
+  uint32_t r = 0;  // one by one
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t e = look_up(pairs, s.window());
+    r = __funnelshift_r(r, e >> 8, 8);
+    s.p += (e >> 24) & 15u;
+    s.refill();
+  }
+  return r;
 }
 
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
@@ -264,12 +223,12 @@ __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
 }
 
 // 16 weights of a lane, two BF16 per word
-__device__ __forceinline__ void next16(LaneBits &s, uint32_t pairs, const LinearTable *t,
-                                       const uint4 &sm, uint32_t (&w)[8], uint32_t &bad) {
+__device__ __forceinline__ void next16(LaneBits &s, uint32_t pairs, const uint4 &sm,
+                                       uint32_t (&w)[8]) {
   const uint32_t v[4] = {sm.x, sm.y, sm.z, sm.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint2 f = fuse4(v[j], next4(s, pairs, t, bad));
+    const uint2 f = fuse4(v[j], next4(s, pairs));
     w[2 * j] = f.x;
     w[2 * j + 1] = f.y;
   }
@@ -279,9 +238,6 @@ __device__ __forceinline__ void next16(LaneBits &s, uint32_t pairs, const Linear
 // share of the units in the order (group of 16 row blocks, unit along the rows, row block
 // of the group), and warp w of it those of the group's row block w.  So the warps of a
 // thread block are at the same columns of x at about the same time.
-struct UnitRange {
-  uint64_t begin, end;
-};
 __device__ __host__ __forceinline__ uint64_t first_unit(uint64_t cta, uint64_t units, uint64_t ctas) {
   return cta * units / ctas;
 }
@@ -291,31 +247,41 @@ __device__ __host__ __forceinline__ uint64_t ordered_units(uint32_t rbs, uint32_
 }
 
 // Shared memory: barriers (two per warp and the table's), the warps' buffers (two units
-// each), the table.  A lane of an inconsistent stream can run past its buffer by at
-// most 32 bits per symbol, 16 KB in all: less than the table behind the buffers.
+// each) on both sides of the table, which starts at a multiple of its size, and room for
+// what a lane of an inconsistent stream can read past its buffer before a tile's check
+// stops it (32 symbols of up to 31 bits, two words ahead).
 constexpr uint32_t kBarBytes = 384;
+constexpr uint32_t kOverrun = 128u * (32u + 2u);
 static_assert(kBarBytes >= 8 * (2 * kWarps + 1) && kBarBytes % 128 == 0, "barriers");
-static_assert(4 * kPairs >= 128u * (kMaxUnitTiles * 32u), "overrun stays in the table");
 
 __device__ __host__ constexpr uint32_t decode_smem(uint32_t max_words) {
-  return kBarBytes + kWarps * 2u * max_words * 128u + 4u * kPairs;
+  // the space before the table is below the table's size, and holds all buffers or leaves
+  // less than one warp's free
+  const uint32_t buffers = (kWarps + 1) * 2u * max_words * 128u;
+  return kBarBytes + (buffers > 4u * kPairs ? buffers : 4u * kPairs) + 4u * kPairs + kOverrun;
 }
 
-// The decoding side of both kernels: `use(rb, cg, w0, w1, slot)` gets every tile of the
-// warp's units in order (w0: rows 0-7, w1: rows 8-15), `moved(group)` every group of
-// row blocks of the thread block's range once the warp's units there are done.
+// The decoding side of both kernels: `use.load(cg)` and `use(rb, cg, w0, w1)` get every
+// tile of the warp's units in order, before and after it is decoded (w0: rows 0-7, w1: rows
+// 8-15), `moved()` is called for every group of row blocks of the thread block's range once
+// the warp's units there are done, and `start()` once before anything is used.
+// A unit's streams are copied into one of the warp's two buffers while it decodes the
+// other; the rows of the unit after that, and the next tile's sign/mantissa bytes, are
+// loaded ahead.
 template <typename Start, typename Use, typename Moved>
 __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, uint32_t ctas,
                                              int32_t *err, uint32_t spin_limit, uint8_t *smem,
                                              Start start, Use use, Moved moved) {
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t bars = smem_addr(smem);
+  const uint32_t bars = keep(smem_addr(smem));
   const uint32_t tbar = bars + 8u * (2 * kWarps), wbar = bars + 16u * warp;
   const uint32_t bytes = lw.max_words * 128u;
-  const uint32_t buf = bars + kBarBytes + warp * 2u * bytes;
-  const uint32_t pairs = bars + kBarBytes + kWarps * 2u * bytes;
-  if (tid == 0) {
-    for (uint32_t i = 0; i < 2 * kWarps + 1; ++i) mbar_init(bars + 8u * i, 1);
+  const uint32_t pairs = keep((bars + kBarBytes + 4u * kPairs - 1u) & ~(4u * kPairs - 1u));
+  const uint32_t before = min((pairs - bars - kBarBytes) / (2u * bytes), (uint32_t)kWarps);
+  const uint32_t buf = keep(warp < before ? bars + kBarBytes + warp * 2u * bytes
+                                          : pairs + 4u * kPairs + (warp - before) * 2u * bytes);
+  if (tid < 2 * kWarps + 1) {
+    mbar_init(bars + 8u * tid, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -327,90 +293,122 @@ __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, ui
   const uint64_t o0 = first_unit(cta, units, ctas), o1 = first_unit(cta + 1, units, ctas);
   const uint32_t per_group = lw.upr * kWarps;
   const uint32_t g0 = (uint32_t)(o0 / per_group), g1 = (uint32_t)((o1 + per_group - 1) / per_group);
-  // this warp's units: steps q = group * upr + (unit along the rows), [q0, q1)
-  const uint64_t q0 = (o0 + kWarps - 1 - warp) / kWarps, q1 = (o1 + kWarps - 1 - warp) / kWarps;
-  uint32_t group = (uint32_t)(q0 / lw.upr), ku = (uint32_t)(q0 - (uint64_t)group * lw.upr);
-  uint32_t fetched_ok = 0;  // bit j & 1: the fetch of step j was made
-  // fetch ahead: the unit `d` steps on from (group, ku); row blocks past the last have none
-  auto fetch = [&](uint64_t j, uint32_t fg, uint32_t fk) {
-    const uint32_t rb = fg * kWarps + warp, i = (uint32_t)j & 1u;
-    bool ok = false;
-    if (rb < lw.rbs) {
-      if (lane == 0) {
-        ok = fetch_unit(lw, rb * lw.upr + fk, buf + i * bytes, wbar + 8u * i);
-        if (!ok) report(err, DF11_DEV_ERR_CAPACITY);
-      }
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-    }
-    fetched_ok = (fetched_ok & ~(1u << i)) | ((ok ? 1u : 0u) << i);
+  // this warp's units: q = group * upr + (unit along the rows), [q0, q1), without those of
+  // row blocks past the last
+  const uint32_t q0 = (uint32_t)((o0 + kWarps - 1 - warp) / kWarps);
+  const uint32_t mine = warp < lw.rbs ? ((lw.rbs - 1 - warp) / kWarps + 1) * lw.upr : 0u;
+  const uint32_t q1 = min((uint32_t)((o1 + kWarps - 1 - warp) / kWarps), mine);
+  uint32_t group = q0 / lw.upr, ku = q0 - group * lw.upr;
+  // rows [r0, r1) of the unit to fetch next
+  uint32_t r0 = 0, r1 = 0;
+  auto rows_of = [&](uint32_t grp, uint32_t k) {
+    const uint32_t *p = lw.unit_rows + (grp * kWarps + warp) * lw.upr + k;
+    r0 = __ldg(p);
+    r1 = __ldg(p + 1);
   };
-  uint32_t phase = 0;  // bit i: parity of buffer i's next wait
-  uint64_t j = 0;
-  if (q0 < q1) fetch(0, group, ku);
+  // into buffer i; returns the words, 0 when the table of rows is inconsistent
+  auto fetch = [&](uint32_t i) -> uint32_t {
+    const uint32_t n = r1 - r0;
+    if (r1 < r0 || n > lw.max_words || n == 0 || r1 > lw.stream_rows) {
+      if (lane == 0) report(err, DF11_DEV_ERR_CAPACITY);
+      return 0u;
+    }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(wbar + 8u * i, n * 128u);
+      bulk_g2s(buf + i * bytes, lw.streams + (size_t)r0 * 32u, n * 128u, wbar + 8u * i);
+    }
+    return n;
+  };
+  uint32_t words = 0, phase = 0;  // phase bit i: parity of buffer i's next wait
+  const uint8_t *smp = lw.sign_mantissa + 16u * lane;
+  uint4 sm0 = make_uint4(0, 0, 0, 0), sm1 = sm0;
+  auto tile_at = [&](uint32_t grp, uint32_t k) {
+    smp = lw.sign_mantissa + 16u * lane +
+          ((size_t)(grp * kWarps + warp) * lw.ncg + k * kUnitTiles) * kTileElems;
+  };
+  uint32_t ng = group, nk = ku;  // the unit after the current one
+  auto advance = [&]() {
+    if (++nk == lw.upr) {
+      nk = 0;
+      ++ng;
+    }
+  };
+  if (q0 < q1) {
+    rows_of(group, ku);
+    tile_at(group, ku);
+    sm0 = ldg_stream(smp);
+    sm1 = ldg_stream(smp + 512);
+    words = fetch(0);
+    advance();
+    if (q0 + 1 < q1) rows_of(ng, nk);
+  }
   bool table = mbar_wait(tbar, 0, spin_limit);
   if (!__all_sync(0xFFFFFFFFu, table)) {
     if (lane == 0) report(err, DF11_DEV_ERR_TIMEOUT);
     table = false;
   }
   start();
-  uint32_t done = g0;  // groups handed on
-  uint32_t bad = 0;
-  bool waiting = true;
-  for (uint64_t q = q0; q < q1 && waiting; ++q, ++j) {
-    while (done < group) moved(done++);
-    uint32_t ng = group, nk = ku + 1;
-    if (nk == lw.upr) {
-      nk = 0;
-      ++ng;
+  uint32_t done = g0, bad = 0, i = 0;
+  for (uint32_t q = q0; q < q1; ++q, i ^= 1u) {
+    while (done < group) {
+      moved();
+      ++done;
     }
-    const uint32_t i = (uint32_t)j & 1u, rb = group * kWarps + warp;
-    const uint32_t cg0 = ku * lw.unit_tiles, nt = min(lw.unit_tiles, lw.ncg - cg0);
-    const uint8_t *smp = lw.sign_mantissa + ((size_t)rb * lw.ncg + cg0) * kTileElems + 16u * lane;
-    uint4 sm0, sm1;
-    const bool ok = (fetched_ok >> i) & 1u;
-    if (ok) {
-      sm0 = ldg_stream(smp);
-      sm1 = ldg_stream(smp + 512);
+    const uint32_t cg0 = ku * kUnitTiles, nt = min(kUnitTiles, lw.ncg - cg0);
+    const uint32_t rb = group * kWarps + warp;
+    group = ng;
+    ku = nk;
+    const bool more = q + 1 < q1;
+    uint32_t next_words = 0;
+    __syncwarp();  // every lane is done with the other buffer
+    if (more) {
+      next_words = fetch(i ^ 1u);
+      advance();
+      if (q + 2 < q1) rows_of(ng, nk);
     }
-    // the other buffer: every lane is done with it
-    __syncwarp();
-    if (q + 1 < q1) fetch(j + 1, ng, nk);
+    bool ok = words != 0;
     if (ok) {
-      waiting = __all_sync(0xFFFFFFFFu, mbar_wait(wbar + 8u * i, (phase >> i) & 1u, spin_limit));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(wbar + 8u * i, (phase >> i) & 1u, spin_limit));
       phase ^= 1u << i;
-      if (!waiting) {
-        if (lane == 0) report(err, DF11_DEV_ERR_TIMEOUT);
+      if (!ok) {
+        // the copy may still come: leave, once the other one has landed or not
+        if (lane == 0) {
+          report(err, DF11_DEV_ERR_TIMEOUT);
+          if (next_words) mbar_wait(wbar + 8u * (i ^ 1u), (phase >> (i ^ 1u)) & 1u, spin_limit);
+        }
         break;
       }
     }
-    if (ok && table) {
-      const uint32_t row0 = buf + i * bytes + 4u * lane;
-      LaneBits s{lds32(row0), lds32(row0 + 128u), 0u, row0 + 256u};
-      for (uint32_t c = 0; c < nt; ++c) {
-        const uint4 v0 = sm0, v1 = sm1;
-        if (c + 1 < nt) {
-          smp += kTileElems;
-          sm0 = ldg_stream(smp);
-          sm1 = ldg_stream(smp + 512);
-        }
+    const uint32_t row0 = buf + i * bytes + 4u * lane;
+    LaneBits s{lds32(row0), lds32(row0 + 128u), 0u, row0 + 256u};
+    for (uint32_t c = 0; c < nt; ++c) {
+      const uint4 v0 = sm0, v1 = sm1;
+      if (c + 1 < nt) smp += kTileElems;
+      else if (more) tile_at(group, ku);
+      sm0 = ldg_stream(smp);
+      sm1 = ldg_stream(smp + 512);
+      if (s.addr - row0 > bytes + 256u) {  // read past the unit's words
+        bad = 1u;
+        s.addr = row0;
+      }
+      if (ok && table) {
         use.load(cg0 + c);
         uint32_t w0[8], w1[8];
-        next16(s, pairs, lw.table, v0, w0, bad);
-        next16(s, pairs, lw.table, v1, w1, bad);
+        next16(s, pairs, v0, w0);
+        next16(s, pairs, v1, w1);
         use(rb, cg0 + c, w0, w1);
       }
-      // words used: the two in registers were read ahead
-      if ((s.addr - row0 - 256u) / 128u > lw.max_words) bad |= 2u;
     }
-    group = ng;
-    ku = nk;
+    // the longest stream ends in the unit's last word
+    const uint32_t used = ((s.addr - row0 - 256u) >> 7) + ((s.p & 31u) ? 1u : 0u);
+    if (__reduce_max_sync(0xFFFFFFFFu, used) != words) bad |= words;
+    words = next_words;
   }
-  while (done < g1) moved(done++);
-  if (bad) report(err, bad & 1u ? DF11_DEV_ERR_TABLE : DF11_DEV_ERR_OVERRUN);
-  // no copy is in flight into this thread block's shared memory when it ends
-  if (!waiting && lane == 0)
-    for (uint32_t i = 0; i < 2; ++i)
-      if ((fetched_ok >> i) & 1u) mbar_wait(wbar + 8u * i, (phase >> i) & 1u, spin_limit);
+  while (done < g1) {
+    moved();
+    ++done;
+  }
+  if (bad) report(err, DF11_DEV_ERR_COUNT);
 }
 
 // ---- few tokens: decode and multiply in one kernel ----------------------------------
@@ -444,15 +442,24 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 // The products of a tile: x as B fragments, token 8 j + lane / 4 and the lane's 16 columns
 template <int NB>
 struct Multiply {
-  const LTensor &lt;
   float (&acc)[NB][4];
+  const uint16_t *x;  // the lane's token and columns
+  uint64_t step;      // bytes from token n to token n + 8
+  uint32_t tiles;     // tiles in which x has the lane's columns
+  uint32_t tokens;    // of the lane: n = lane / 4 + 8 j, j below this
   uint4 x0, x1;
-  const uint32_t g = (threadIdx.x & 31u) >> 2, c = 16u * (threadIdx.x & 3u);
+  __device__ __forceinline__ Multiply(const LTensor &lt, uint32_t lane, float (&a)[NB][4]) : acc(a) {
+    const uint32_t n = lane >> 2, c = 16u * (lane & 3u);
+    x = lt.x + (size_t)n * lt.x_stride + c;
+    step = 16ull * lt.x_stride;
+    tiles = lt.x_cols > c ? (lt.x_cols - c + kTileCols - 1) / kTileCols : 0u;
+    tokens = lt.batch > n ? (lt.batch - n + 7u) / 8u : 0u;
+  }
   __device__ __forceinline__ void load_x(uint32_t j, uint32_t cg) {
-    const uint32_t n = 8u * j + g, col = cg * kTileCols + c;
     x0 = x1 = make_uint4(0, 0, 0, 0);
-    if (n < lt.batch && col < lt.x_cols) {
-      const uint4 *p = reinterpret_cast<const uint4 *>(lt.x + (size_t)n * lt.x_stride + col);
+    if (j < tokens && cg < tiles) {
+      const uint4 *p = reinterpret_cast<const uint4 *>(
+          reinterpret_cast<const uint8_t *>(x) + j * step + cg * (2u * kTileCols));
       x0 = __ldg(p);
       x1 = __ldg(p + 1);
     }
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, NB > 2 ? 1 : 2)
   for (int j = 0; j < NB; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
   float *part = lt.part + ((size_t)cta * lt.slots * kWarps + warp) * (16 * 8 * NB);
   // the warp's sums of a group's row block to the workspace, [token][row]
-  auto moved = [&](uint32_t) {
+  auto moved = [&]() {
     float *q = part + (2u * (lane & 3u)) * 16u + (lane >> 2);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -504,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, NB > 2 ? 1 : 2)
     pdl_wait();
     pdl_launch_dependents();
   };
-  decode_units(lt.w, cta, ctas, lb.err, lb.spin_limit, smem, start, Multiply<NB>{lt, acc}, moved);
+  decode_units(lt.w, cta, ctas, lb.err, lb.spin_limit, smem, start, Multiply<NB>(lt, lane, acc), moved);
 }
 
 // The warps' sums of every row block added in a fixed order, and the epilogue.
@@ -565,12 +572,12 @@ struct UArgs {
 
 struct StoreTile {
   uint16_t *out;
-  uint32_t ncg;
+  uint32_t ncg, lane;
   __device__ __forceinline__ void load(uint32_t) {}
   __device__ __forceinline__ void operator()(uint32_t rb, uint32_t cg, const uint32_t (&w0)[8],
                                              const uint32_t (&w1)[8]) {
     uint4 *q = reinterpret_cast<uint4 *>(out + ((size_t)rb * ncg + cg) * kTileElems) +
-               2u * (threadIdx.x & 31u);
+               2u * lane;
     q[0] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
     q[1] = make_uint4(w0[4], w0[5], w0[6], w0[7]);
     q[64] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
@@ -588,8 +595,8 @@ __global__ void __launch_bounds__(kThreads, 2) df11_linear_unpack_kernel(const _
     pdl_launch_dependents();
   };
   decode_units(ua.w[ti], blockIdx.x - ua.cta_begin[ti], ua.cta_begin[ti + 1] - ua.cta_begin[ti],
-               ua.err, ua.spin_limit, smem, start, StoreTile{ua.out[ti], ua.w[ti].ncg},
-               [](uint32_t) {});
+               ua.err, ua.spin_limit, smem, start, StoreTile{ua.out[ti], ua.w[ti].ncg, threadIdx.x & 31u},
+               []() {});
 }
 
 // ---- building the compressed form --------------------------------------------------------
@@ -600,7 +607,7 @@ struct PackWeight {
   uint32_t *unit_rows;
   uint32_t *streams;
   uint8_t *sign_mantissa;
-  uint32_t rows, cols, rbs, ncg, unit_tiles, upr;
+  uint32_t rows, cols, rbs, ncg, upr;
   uint32_t vec;            // rows of the weight on 16-byte boundaries
 };
 
@@ -637,7 +644,7 @@ __global__ void __launch_bounds__(256) linear_encode_kernel(const __grid_constan
   const uint64_t units = (uint64_t)a.rbs * a.upr;
   for (uint64_t u = (blockIdx.x * 256ull + threadIdx.x) >> 5; u < units; u += gridDim.x * 8ull) {
     const uint32_t rb = (uint32_t)(u / a.upr), ku = (uint32_t)(u - (uint64_t)rb * a.upr);
-    const uint32_t cg0 = ku * a.unit_tiles, cg1 = min(cg0 + a.unit_tiles, a.ncg);
+    const uint32_t cg0 = ku * kUnitTiles, cg1 = min(cg0 + kUnitTiles, a.ncg);
     uint32_t bits = 0;
     uint32_t row = WRITE ? a.unit_rows[u] : 0u;
     const uint32_t end = WRITE ? a.unit_rows[u + 1] : 0u;
@@ -1027,8 +1034,7 @@ LWeight device_weight(const df11_linear_weight &w) {
   l.table = static_cast<const LinearTable *>(w.table);
   l.rbs = (p.rows + kTileRows - 1) / kTileRows;
   l.ncg = (p.cols + kTileCols - 1) / kTileCols;
-  l.unit_tiles = p.unit_tiles;
-  l.upr = (l.ncg + p.unit_tiles - 1) / p.unit_tiles;
+  l.upr = (l.ncg + kUnitTiles - 1) / kUnitTiles;
   l.max_words = p.max_words;
   l.stream_rows = p.stream_rows;
   return l;
@@ -1146,8 +1152,7 @@ df11_status check_weight(const df11_linear_weight &w) {
   if (!aligned(w.streams, 16) || !aligned(w.sign_mantissa, 16) || !aligned(w.table, 16) ||
       !aligned(w.unit_rows, 4))
     return DF11_ERR_ALIGN;
-  if (p.unit_tiles < 1 || p.unit_tiles > kMaxUnitTiles || p.max_words < 1 || p.max_words > kMaxWords)
-    return DF11_ERR_FORMAT;
+  if (p.max_words < 1 || p.max_words > kMaxWords) return DF11_ERR_FORMAT;
   const LWeight l = device_weight(w);
   if (p.stream_rows > (uint64_t)l.rbs * l.upr * p.max_words) return DF11_ERR_FORMAT;
   return DF11_OK;
@@ -1376,46 +1381,30 @@ df11_status check_linear_devices(const df11_linear_weight *ws, const df11_linear
   return DF11_OK;
 }
 
-// The decode table of a code: its lengths and (right-aligned, canonical) codewords.
+// The decode table of a code: its lengths (at most kMaxLength) and right-aligned codewords.
 void make_table(const uint8_t len[256], const uint32_t code[256], LinearTable &t) {
-  std::memset(&t, 0, sizeof(t));
-  auto rot = [](uint32_t e) { return (e >> 1 | e << 7) & 0xFFu; };
-  uint32_t next = 0;
-  for (uint32_t l = 1; l <= 32; ++l) {
-    uint32_t count = 0, low = 0xFFFFFFFFu;
-    for (int e = 0; e < 256; ++e)
-      if (len[e] == l) {
-        ++count;
-        low = code[e] < low ? code[e] : low;
-      }
-    t.first[l] = count ? low : 0u;
-    t.range[l] = count << 16 | next;
-    for (int e = 0; e < 256; ++e)
-      if (len[e] == l) t.sym[next + (code[e] - low)] = (uint8_t)rot((uint32_t)e);
-    next += count;
-  }
-  for (int e = 0; e < 256; ++e) {
+  // by the next kMaxLength bits: the first codeword's exponent (rotated) and length
+  uint32_t sym[1 << kMaxLength] = {}, length[1 << kMaxLength] = {};
+  for (uint32_t e = 0; e < 256; ++e) {
     t.length[e] = len[e];
     t.code[e] = len[e] ? code[e] << (32 - len[e]) : 0u;
-  }
-  // the codeword at the start of `bits` (kPairBits wide, left-aligned in 32), if it is
-  // at most `room` long
-  auto one = [&](uint32_t bits, uint32_t room, uint32_t &sym, uint32_t &l) {
-    for (l = 1; l <= room; ++l) {
-      const uint32_t k = (bits >> (32 - l)) - t.first[l];
-      if (k < t.range[l] >> 16) {
-        sym = t.sym[(t.range[l] & 0xFFFFu) + k];
-        return true;
-      }
+    if (!len[e]) continue;
+    const uint32_t free = kMaxLength - len[e];
+    for (uint32_t i = code[e] << free; i < (code[e] + 1u) << free; ++i) {
+      sym[i] = (e >> 1 | e << 7) & 0xFFu;
+      length[i] = len[e];
     }
-    return false;
-  };
+  }
+  // bits that no codeword begins with (a code of one symbol has such): a length of one
+  for (uint32_t i = 0; i < 1u << kMaxLength; ++i)
+    if (!length[i]) length[i] = 1;
   for (uint32_t i = 0; i < kPairs; ++i) {
-    const uint32_t bits = i << (32 - kPairBits);
-    uint32_t s0 = 0, s1 = 0, l0 = 0, l1 = 0;
-    if (!one(bits, kPairBits, s0, l0)) t.pair[i] = kBothFlag | kDeepFlag;
-    else if (!one(bits << l0, kPairBits - l0, s1, l1)) t.pair[i] = kBothFlag | l0 << 24 | s0 << 8 | l0;
-    else t.pair[i] = l0 << 24 | s1 << 16 | s0 << 8 | (l0 + l1);
+    const uint32_t a = i >> (kPairBits - kMaxLength);
+    const uint32_t b = ((i << length[a]) & (kPairs - 1)) >> (kPairBits - kMaxLength);
+    const uint32_t first = length[a] << 24 | sym[a] << 8;
+    t.pair[i] = length[a] + length[b] <= (uint32_t)kPairBits
+                    ? first | sym[b] << 16 | (length[a] + length[b])
+                    : kFirstOnly | first | length[a];
   }
 }
 
@@ -1429,8 +1418,7 @@ PackWeight pack_weight(const uint16_t *d_w, const df11_linear_params &p, uint32_
   a.cols = p.cols;
   a.rbs = (p.rows + kTileRows - 1) / kTileRows;
   a.ncg = (p.cols + kTileCols - 1) / kTileCols;
-  a.unit_tiles = p.unit_tiles;
-  a.upr = (a.ncg + a.unit_tiles - 1) / a.unit_tiles;
+  a.upr = (a.ncg + kUnitTiles - 1) / kUnitTiles;
   a.vec = p.cols % 8 == 0 && aligned(d_w, 16);
   return a;
 }
@@ -1449,9 +1437,10 @@ df11_status df11_linear_sizes(uint32_t rows, uint32_t cols, uint64_t *unit_rows_
   if (!unit_rows_count || !sign_mantissa_bytes) return DF11_ERR_NULL;
   const df11_status st = check_shape(rows, cols);
   if (st != DF11_OK) return st;
-  const uint64_t n = round_up(rows, kTileRows) * round_up(cols, kTileCols);
-  *unit_rows_count = n / kTileElems + 4;  // a unit per tile at most, the total, two results
-  *sign_mantissa_bytes = n;
+  *unit_rows_count = round_up(rows, kTileRows) / kTileRows *
+                         (round_up(cols, kUnitTiles * kTileCols) / (kUnitTiles * kTileCols)) +
+                     3;  // the units', the total, two results of the builder
+  *sign_mantissa_bytes = round_up(rows, kTileRows) * round_up(cols, kTileCols);
   return DF11_OK;
 }
 
@@ -1477,8 +1466,7 @@ df11_status df11_linear_weight_begin(const uint16_t *d_w, uint32_t rows, uint32_
   try {
     uint8_t len[256];
     uint32_t code[256];
-    std::vector<uint32_t> luts;
-    codebook(hist, len, code, luts);
+    limited_code(hist, kMaxLength, len, code);
     std::vector<LinearTable> t(1);
     make_table(len, code, t[0]);
     if (cudaMemcpyAsync(table, t.data(), sizeof(LinearTable), cudaMemcpyHostToDevice, s) !=
@@ -1488,22 +1476,18 @@ df11_status df11_linear_weight_begin(const uint16_t *d_w, uint32_t rows, uint32_
   } catch (...) {
     return DF11_ERR_NOMEM;
   }
-  // the longest units whose streams stay within kMaxWords
-  for (p.unit_tiles = kMaxUnitTiles;; p.unit_tiles /= 2) {
-    PackWeight a = pack_weight(d_w, p, unit_rows, table);
-    const uint64_t units = (uint64_t)a.rbs * a.upr;
-    uint32_t *result = unit_rows + padded(p) / kTileElems + 1;
-    linear_encode_kernel<false><<<encode_grid(a), 256, 0, s>>>(a);
-    linear_rows_kernel<<<1, 1024, 0, s>>>(unit_rows, units, result);
-    uint32_t got[2] = {0, 0};
-    if (cudaGetLastError() != cudaSuccess ||
-        cudaMemcpyAsync(got, result, sizeof(got), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-      return DF11_ERR_CUDA;
-    p.stream_rows = got[0];
-    p.max_words = got[1];
-    if (p.max_words <= kMaxWords || p.unit_tiles == 1) break;
-  }
+  const PackWeight a = pack_weight(d_w, p, unit_rows, table);
+  const uint64_t units = (uint64_t)a.rbs * a.upr;
+  uint32_t *result = unit_rows + units + 1;
+  linear_encode_kernel<false><<<encode_grid(a), 256, 0, s>>>(a);
+  linear_rows_kernel<<<1, 1024, 0, s>>>(unit_rows, units, result);
+  uint32_t got[2] = {0, 0};
+  if (cudaGetLastError() != cudaSuccess ||
+      cudaMemcpyAsync(got, result, sizeof(got), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return DF11_ERR_CUDA;
+  p.stream_rows = got[0];
+  p.max_words = got[1];
   *params = p;
   return DF11_OK;
 }

@@ -17,8 +17,8 @@ import torch
 
 from . import Df11Device, Df11Host, _check, _one_device, _stream_handle, decode, lib, to_device
 
-TILE_ROWS, TILE_COLS = 16, 64
-LINEAR_TABLE_BYTES = 4 * 8192 + 4 * (33 + 33 + 2) + 256 + 2048
+TILE_ROWS, TILE_COLS, UNIT_TILES = 16, 64, 4
+LINEAR_TABLE_BYTES = 4 * 4096 + 2048
 LINEAR_MAX_BATCH = 1 << 20
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -27,8 +27,7 @@ _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 class LinearParams(ctypes.Structure):
     """df11_linear_params: shape and layout of a weight for the linear product."""
-    _fields_ = [(f, ctypes.c_uint32) for f in ("rows", "cols", "unit_tiles", "max_words",
-                                               "stream_rows")]
+    _fields_ = [(f, ctypes.c_uint32) for f in ("rows", "cols", "max_words", "stream_rows")]
 
 
 class LinearWeightDesc(ctypes.Structure):
@@ -122,7 +121,7 @@ def _compress_linear(w: torch.Tensor, stream) -> LinearWeight:
     _check(L.df11_linear_weight_begin(w.data_ptr(), rows, cols, unit_rows.data_ptr(),
                                       table.data_ptr(), ctypes.byref(p), sh),
            "df11_linear_weight_begin")
-    per_row = -(-(-(-cols // TILE_COLS)) // p.unit_tiles)
+    per_row = -(-cols // (TILE_COLS * UNIT_TILES))
     out = LinearWeight(
         params=p, streams=torch.empty(p.stream_rows * 32, dtype=torch.int32, device=dev),
         unit_rows=unit_rows[: -(-rows // TILE_ROWS) * per_row + 1].clone(),

@@ -264,19 +264,18 @@ df11_status df11_decode_gemm(const df11_tensor *tensors, const df11_gemv *ops, i
 #define DF11_LINEAR_MAX_BATCH (1u << 20)
 
 /* Bytes of a weight's decode table. */
-#define DF11_LINEAR_TABLE_BYTES (4 * 8192 + 4 * (33 + 33 + 2) + 256 + 2048)
+#define DF11_LINEAR_TABLE_BYTES (4 * 4096 + 2048)
 
 /* A weight (rows x cols) in the compressed form of the linear product, written
- * by df11_linear_weight_begin and _finish: the same coding as the other tensors' (a canonical
- * Huffman code of the exponents, sign and mantissa kept as a byte), but cut by
- * elements, so that 32 streams of a fixed number of elements lie side by
- * side.  The matrix, padded with zeros, is cut into tiles of 16 rows and 64
- * columns, and each block of 16 rows into units of unit_tiles tiles (the last may be
+ * by df11_linear_weight_begin and _finish: as in the other tensors a canonical Huffman
+ * code of the exponents, sign and mantissa kept as a byte, but with codewords of at
+ * most 8 bits and cut by elements, so that 32 streams of a fixed number of elements
+ * lie side by side.  The matrix, padded with zeros, is cut into tiles of 16 rows and
+ * 64 columns, and each block of 16 rows into units of four tiles (the last may be
  * shorter).  Stream l (0 .. 31) of a unit codes, tile after tile, the 16 columns from
  * 16 (l mod 4) on of row l/4 and then of row l/4 + 8. */
 typedef struct df11_linear_params {
   uint32_t rows, cols;
-  uint32_t unit_tiles;  /* tiles per unit: 4, 2 or 1 */
   uint32_t max_words;   /* 32-bit words of the longest stream */
   uint32_t stream_rows; /* rows of 32 words (one per stream) in `streams` */
 } df11_linear_params;
@@ -284,10 +283,12 @@ typedef struct df11_linear_params {
 typedef struct df11_linear_weight {
   const uint32_t *streams;      /* 16-byte aligned, stream_rows * 32 words: a unit's streams word
                                    by word, first bit = bit 31 */
-  const uint32_t *unit_rows;    /* first row of each unit, and the total at the end */
+  const uint32_t *unit_rows;    /* first row of each unit, and the total after them */
   const uint8_t *sign_mantissa; /* 16-byte aligned: per tile 16 bytes of each stream for rows
                                    0 .. 7, then for rows 8 .. 15 */
-  const void *table;            /* 16-byte aligned, DF11_LINEAR_TABLE_BYTES */
+  const void *table;            /* 16-byte aligned, DF11_LINEAR_TABLE_BYTES: the decode table
+                                   of 4096 words, then by exponent 256 codewords (first bit
+                                   = bit 31) and 256 lengths */
   df11_linear_params params;
 } df11_linear_weight;
 

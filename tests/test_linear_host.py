@@ -12,12 +12,12 @@ FAKE = 1 << 20  # an aligned non-null address; never dereferenced
 
 def test_struct_layout_matches_the_header():
     assert ctypes.sizeof(df11.LinearOp) == 5 * 8 + 5 * 4 + 5 * 4
-    assert ctypes.sizeof(df11.LinearParams) == 20
-    assert ctypes.sizeof(df11.LinearWeightDesc) == 4 * 8 + 24
+    assert ctypes.sizeof(df11.LinearParams) == 16
+    assert ctypes.sizeof(df11.LinearWeightDesc) == 4 * 8 + 16
 
 
 def _host_weight(rows=32, cols=128):
-    p = df11.LinearParams(rows, cols, 4, 12, 20)
+    p = df11.LinearParams(rows, cols, 12, 20)
     return df11.LinearWeight(p, torch.zeros(640, dtype=torch.int32),
                              torch.zeros(3, dtype=torch.int32),
                              torch.zeros(rows * cols, dtype=torch.uint8),
@@ -64,7 +64,7 @@ def test_refusals_of_the_binding():
 
 
 def _weight(**kw):
-    w = df11.LinearWeightDesc(FAKE, FAKE, FAKE, FAKE, df11.LinearParams(32, 128, 4, 12, 20))
+    w = df11.LinearWeightDesc(FAKE, FAKE, FAKE, FAKE, df11.LinearParams(32, 128, 12, 20))
     for k, v in kw.items():
         setattr(w.params if hasattr(w.params, k) else w, k, v)
     return w
@@ -99,8 +99,7 @@ NULL, ALIGN, FORMAT, UNSUPPORTED, TOO_LARGE, INVALID = 1, 2, 3, 4, 6, 7
     (INVALID, {}, dict(residual=FAKE, residual_stride=0)),
     (TOO_LARGE, {}, dict(batch=(1 << 20) + 1)),
     (TOO_LARGE, dict(rows=1 << 16, cols=1 << 16), dict(x_stride=1 << 16, y_stride=1 << 16)),
-    (FORMAT, dict(unit_tiles=0), {}), (FORMAT, dict(unit_tiles=5), {}),
-    (FORMAT, dict(max_words=0), {}), (FORMAT, dict(max_words=41), {}),
+    (FORMAT, dict(max_words=0), {}), (FORMAT, dict(max_words=33), {}),
     (FORMAT, dict(stream_rows=25), {}),
 ])
 def test_refusals_of_the_library(status, weight, op):
@@ -126,7 +125,7 @@ def test_refusals_of_the_builder():
     L, u = df11.lib(), ctypes.c_uint64
     a, b = u(0), u(0)
     assert L.df11_linear_sizes(33, 65, ctypes.byref(a), ctypes.byref(b)) == 0
-    assert b.value == 48 * 128 and a.value == 6 + 4
+    assert b.value == 48 * 128 and a.value == 3 + 3
     assert L.df11_linear_sizes(0, 65, ctypes.byref(a), ctypes.byref(b)) == INVALID
     assert L.df11_linear_sizes(1 << 20, 1 << 12, ctypes.byref(a), ctypes.byref(b)) == TOO_LARGE
     assert L.df11_linear_sizes(1, 1, None, ctypes.byref(b)) == NULL
@@ -140,7 +139,7 @@ def test_refusals_of_the_builder():
     w = _weight()
     assert L.df11_linear_weight_finish(None, ctypes.byref(w), None) == NULL
     assert L.df11_linear_weight_finish(FAKE, None, None) == NULL
-    bad = _weight(unit_tiles=9)
+    bad = _weight(max_words=99)
     assert L.df11_linear_weight_finish(FAKE, ctypes.byref(bad), None) == FORMAT
     assert L.df11_linear_unpack(ctypes.byref(bad), FAKE, None, None) == FORMAT
     assert L.df11_linear_unpack(ctypes.byref(w), FAKE + 2, None, None) == ALIGN
