@@ -46,21 +46,25 @@ constexpr int kThreads = 32 * kWarps;
 // ---- the code and its decode table ------------------------------------------------
 //
 // Codewords of at most 8 bits: 0.08 bits longer on average than the unlimited code of
-// Gaussian weights, but two codewords nearly always lie inside kPairBits bits.  Pair table,
-// indexed by the next kPairBits bits: both when they do (bits 0-4 their length
-// together, bits 8-15 and 16-23 the exponents, rotated right by one bit, bits 24-27 the
-// first one's length); otherwise bit 31 is set and only the first one is there (bits 0-4
-// its length).  0.03% of the pairs of Gaussian weights exceed 13 bits, 0.08% 12 bits;
-// with unlimited codewords 0.2% and 0.4%, and a warp waits for any of its 32 lanes.
+// Gaussian weights, but two codewords nearly always lie inside kPairBits bits: 0.08% of the
+// pairs exceed 12 bits, 0.4% with unlimited codewords, and a warp waits for any of its 32
+// lanes.  The streams are filled from bit 0 of a word up, a codeword's first bit lowest.
+//
+// Pair table, indexed by the next kPairBits bits: bits 7-14 and 23-30 the exponents of two
+// codewords, where a pair of BF16 words has them, bits 0-3 the length of both together,
+// bits 16-19 the first one's; when the second one does not lie inside, kFirstOnly, and bits
+// 0-3 have the first one's length.  Bits 4-6 are zero, so that two entries' sum has the
+// length of both in its low six bits.
 constexpr int kMaxLength = 8;
 constexpr int kPairBits = 12;
 constexpr uint32_t kPairs = 1u << kPairBits;
-constexpr uint32_t kFirstOnly = 0x80000000u;
+constexpr uint32_t kFirstOnly = 1u << 20;
+constexpr uint32_t kExponents = 0x7F807F80u;
 // Words of a lane's stream in a unit, at most.
 constexpr uint32_t kMaxWords = kUnitTiles * 32u * kMaxLength / 32u;
 struct LinearTable {
   uint32_t pair[kPairs];
-  uint32_t code[256];    // by exponent: the codeword, left-aligned, and its length
+  uint32_t code[256];    // by exponent: the codeword, first bit lowest, and its length
   uint32_t length[256];  // (for the builder)
 };
 static_assert(sizeof(LinearTable) == DF11_LINEAR_TABLE_BYTES, "table layout");
@@ -161,9 +165,10 @@ struct LWeight {
   uint32_t max_words, stream_rows;
 };
 
-// Two words of the lane's stream with the next bit at bit 31 - (p & 31) of `a`, and
-// where the word after them is.  Bit 5 of p is zero between steps; bits 8 and up are
-// not kept clean (the table's entries are added whole).
+// Two words of the lane's stream, b after a, and where the word after them is.  The next bit
+// is bit (p & 31) + 2 of a, or bit (p & 31) - 30 of b: two bits on from p, so that a window
+// has the table's index where an address needs it.  Bit 5 of p is zero between steps; bits 7
+// and up are not kept clean (the table's entries are added whole).
 struct LaneBits {
   uint32_t a, b, p, addr;
   // past a word: without a branch, since in most steps some lane has reached its end
@@ -175,7 +180,8 @@ struct LaneBits {
         " @q add.s32 %3, %3, 128;\n @q xor.b32 %2, %2, 32;\n}\n"
         : "+r"(a), "+r"(b), "+r"(p), "+r"(addr));
   }
-  __device__ __forceinline__ uint32_t window() const { return __funnelshift_l(b, a, p); }
+  // the next 30 bits, from bit 2 on
+  __device__ __forceinline__ uint32_t window() const { return __funnelshift_r(a, b, p); }
 };
 
 // A value that the compiler keeps in a register instead of computing it again: it would
@@ -186,32 +192,44 @@ __device__ __forceinline__ uint32_t keep(uint32_t v) {
 }
 
 // The pair table's entry of a window; the table starts at a multiple of its size, so that
-// its address takes no addition.
+// its address takes one instruction.
 __device__ __forceinline__ uint32_t look_up(uint32_t pairs, uint32_t window) {
-  return lds32(((window >> (30 - kPairBits)) & (4u * kPairs - 4u)) | pairs);
+  return lds32((window & (4u * kPairs - 4u)) | pairs);
 }
 
-// The next four exponents (rotated), first in bits 0-7.  One 32-bit window serves both
-// lookups: two pairs take at most 2 kPairBits bits.
-__device__ __forceinline__ uint32_t next4(LaneBits &s, uint32_t pairs) {
+// Two exponents from the stream's state, however long their codewords.
+__device__ __forceinline__ uint32_t slow_pair(LaneBits &s, uint32_t pairs) {
+  uint32_t e = look_up(pairs, s.window());
+  s.p += e & 15u;
+  s.refill();
+  if (e & kFirstOnly) {
+    const uint32_t f = look_up(pairs, s.window());
+    s.p += (f >> 16) & 15u;
+    s.refill();
+    e = (e & 0x7F80u) | (f & 0x7F80u) << 16;
+  }
+  return e;
+}
+
+// The next four weights, two BF16 per word, from their four sign/mantissa bytes.  One
+// window serves both lookups: two pairs take at most 24 of its 30 bits.
+__device__ __forceinline__ void next4(LaneBits &s, uint32_t pairs, uint32_t sm, uint32_t &w0,
+                                      uint32_t &w1) {
   const uint32_t w = s.window();
-  const uint32_t e1 = look_up(pairs, w);
+  uint32_t e1 = look_up(pairs, w);
   // shifts by the low five bits: the length
-  const uint32_t e2 = look_up(pairs, __funnelshift_l(0u, w, e1));
-  if ((int32_t)(e1 | e2) >= 0) {
+  uint32_t e2 = look_up(pairs, __funnelshift_r(w, 0u, e1));
+  if ((e1 | e2) & kFirstOnly) {
+    e1 = slow_pair(s, pairs);
+    e2 = slow_pair(s, pairs);
+  } else {
     s.p += e1 + e2;
     s.refill();
-    return __byte_perm(e1, e2, 0x6521);
   }
-  uint32_t r = 0;  // one by one
-#pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t e = look_up(pairs, s.window());
-    r = __funnelshift_r(r, e >> 8, 8);
-    s.p += (e >> 24) & 15u;
-    s.refill();
-  }
-  return r;
+  // a byte twice in a half word: sign in bit 15, mantissa in bits 0-6
+  const uint32_t lo = __byte_perm(sm, 0, 0x1100), hi = __byte_perm(sm, 0, 0x3322);
+  w0 = (e1 & kExponents) | (lo & ~kExponents);
+  w1 = (e2 & kExponents) | (hi & ~kExponents);
 }
 
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
@@ -222,16 +240,12 @@ __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
   return v;
 }
 
-// 16 weights of a lane, two BF16 per word
+// 16 weights of a lane
 __device__ __forceinline__ void next16(LaneBits &s, uint32_t pairs, const uint4 &sm,
                                        uint32_t (&w)[8]) {
   const uint32_t v[4] = {sm.x, sm.y, sm.z, sm.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint2 f = fuse4(v[j], next4(s, pairs));
-    w[2 * j] = f.x;
-    w[2 * j + 1] = f.y;
-  }
+  for (int j = 0; j < 4; ++j) next4(s, pairs, v[j], w[2 * j], w[2 * j + 1]);
 }
 
 // A warp's walk over its units: thread block `cta` of `ctas` has an equal, contiguous
@@ -249,7 +263,7 @@ __device__ __host__ __forceinline__ uint64_t ordered_units(uint32_t rbs, uint32_
 // Shared memory: barriers (two per warp and the table's), the warps' buffers (two units
 // each) on both sides of the table, which starts at a multiple of its size, and room for
 // what a lane of an inconsistent stream can read past its buffer before a tile's check
-// stops it (32 symbols of up to 31 bits, two words ahead).
+// stops it (at most 32 refills, two words ahead).
 constexpr uint32_t kBarBytes = 384;
 constexpr uint32_t kOverrun = 128u * (32u + 2u);
 static_assert(kBarBytes >= 8 * (2 * kWarps + 1) && kBarBytes % 128 == 0, "barriers");
@@ -263,11 +277,11 @@ __device__ __host__ constexpr uint32_t decode_smem(uint32_t max_words) {
 
 // The decoding side of both kernels: `use.load(cg)` and `use(rb, cg, w0, w1)` get every
 // tile of the warp's units in order, before and after it is decoded (w0: rows 0-7, w1: rows
-// 8-15), `moved()` is called for every group of row blocks of the thread block's range once
+// 8-15), `moved(j)` is called for every group j of row blocks of the thread block's range once
 // the warp's units there are done, and `start()` once before anything is used.
 // A unit's streams are copied into one of the warp's two buffers while it decodes the
-// other; the rows of the unit after that, and the next tile's sign/mantissa bytes, are
-// loaded ahead.
+// other; the rows of the unit after that and the next tile's sign/mantissa bytes are
+// loaded ahead along a row block.
 template <typename Start, typename Use, typename Moved>
 __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, uint32_t ctas,
                                              int32_t *err, uint32_t spin_limit, uint8_t *smem,
@@ -298,16 +312,9 @@ __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, ui
   const uint32_t q0 = (uint32_t)((o0 + kWarps - 1 - warp) / kWarps);
   const uint32_t mine = warp < lw.rbs ? ((lw.rbs - 1 - warp) / kWarps + 1) * lw.upr : 0u;
   const uint32_t q1 = min((uint32_t)((o1 + kWarps - 1 - warp) / kWarps), mine);
-  uint32_t group = q0 / lw.upr, ku = q0 - group * lw.upr;
-  // rows [r0, r1) of the unit to fetch next
-  uint32_t r0 = 0, r1 = 0;
-  auto rows_of = [&](uint32_t grp, uint32_t k) {
-    const uint32_t *p = lw.unit_rows + (grp * kWarps + warp) * lw.upr + k;
-    r0 = __ldg(p);
-    r1 = __ldg(p + 1);
-  };
-  // into buffer i; returns the words, 0 when the table of rows is inconsistent
-  auto fetch = [&](uint32_t i) -> uint32_t {
+  // rows [r0, r1) of a unit into buffer i, and its sign/mantissa bytes (from byte `sm` on)
+  // into L2; returns the words, 0 when the table of rows is inconsistent
+  auto fetch = [&](uint32_t r0, uint32_t r1, uint32_t i, uint32_t sm, uint32_t tiles) -> uint32_t {
     const uint32_t n = r1 - r0;
     if (r1 < r0 || n > lw.max_words || n == 0 || r1 > lw.stream_rows) {
       if (lane == 0) report(err, DF11_DEV_ERR_CAPACITY);
@@ -316,98 +323,89 @@ __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, ui
     if (lane == 0) {
       mbar_arrive_expect_tx(wbar + 8u * i, n * 128u);
       bulk_g2s(buf + i * bytes, lw.streams + (size_t)r0 * 32u, n * 128u, wbar + 8u * i);
+      bulk_prefetch_l2(lw.sign_mantissa + sm, tiles * kTileElems);
     }
     return n;
   };
-  uint32_t words = 0, phase = 0;  // phase bit i: parity of buffer i's next wait
-  const uint8_t *smp = lw.sign_mantissa + 16u * lane;
-  uint4 sm0 = make_uint4(0, 0, 0, 0), sm1 = sm0;
-  auto tile_at = [&](uint32_t grp, uint32_t k) {
-    smp = lw.sign_mantissa + 16u * lane +
-          ((size_t)(grp * kWarps + warp) * lw.ncg + k * kUnitTiles) * kTileElems;
+  // the bytes of the warp's unit q, and the words of a unit's streams once they are asked for
+  auto bytes_of = [&](uint32_t rb, uint32_t cg) {  // below 2^32: the weight's elements
+    return (rb * lw.ncg + cg) * kTileElems;
   };
-  uint32_t ng = group, nk = ku;  // the unit after the current one
-  auto advance = [&]() {
-    if (++nk == lw.upr) {
-      nk = 0;
-      ++ng;
-    }
-  };
+  uint32_t words = 0;
   if (q0 < q1) {
-    rows_of(group, ku);
-    tile_at(group, ku);
-    sm0 = ldg_stream(smp);
-    sm1 = ldg_stream(smp + 512);
-    words = fetch(0);
-    advance();
-    if (q0 + 1 < q1) rows_of(ng, nk);
+    const uint32_t rb = q0 / lw.upr * kWarps + warp, ku = q0 % lw.upr;
+    const uint32_t *rows = lw.unit_rows + (rb * lw.upr + ku);
+    words = fetch(__ldg(rows), __ldg(rows + 1), 0, bytes_of(rb, ku * kUnitTiles),
+                  min(kUnitTiles, lw.ncg - ku * kUnitTiles));
   }
-  bool table = mbar_wait(tbar, 0, spin_limit);
-  if (!__all_sync(0xFFFFFFFFu, table)) {
+  bool running = true;
+  if (!__all_sync(0xFFFFFFFFu, mbar_wait(tbar, 0, spin_limit))) {
     if (lane == 0) report(err, DF11_DEV_ERR_TIMEOUT);
-    table = false;
+    running = false;
   }
   start();
-  uint32_t done = g0, bad = 0, i = 0;
-  for (uint32_t q = q0; q < q1; ++q, i ^= 1u) {
-    while (done < group) {
-      moved();
-      ++done;
-    }
-    const uint32_t cg0 = ku * kUnitTiles, nt = min(kUnitTiles, lw.ncg - cg0);
+  uint32_t done = g0, bad = 0;
+  uint32_t i = 0, phase = 0;  // buffer of the current unit; bit j: parity of buffer j's next wait
+  for (uint32_t q = q0; q < q1 && running;) {
+    // the units of one row block
+    const uint32_t group = q / lw.upr, ku = q - group * lw.upr, count = min(lw.upr - ku, q1 - q);
     const uint32_t rb = group * kWarps + warp;
-    group = ng;
-    ku = nk;
-    const bool more = q + 1 < q1;
-    uint32_t next_words = 0;
-    __syncwarp();  // every lane is done with the other buffer
-    if (more) {
-      next_words = fetch(i ^ 1u);
-      advance();
-      if (q + 2 < q1) rows_of(ng, nk);
-    }
-    bool ok = words != 0;
-    if (ok) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(wbar + 8u * i, (phase >> i) & 1u, spin_limit));
-      phase ^= 1u << i;
-      if (!ok) {
-        // the copy may still come: leave, once the other one has landed or not
-        if (lane == 0) {
-          report(err, DF11_DEV_ERR_TIMEOUT);
-          if (next_words) mbar_wait(wbar + 8u * (i ^ 1u), (phase >> (i ^ 1u)) & 1u, spin_limit);
+    q += count;
+    for (; done < group; ++done) moved(done - g0);
+    const uint32_t rows = rb * lw.upr + ku;
+    uint32_t cg = ku * kUnitTiles;
+    uint32_t smo = bytes_of(rb, cg) + 16u * lane;
+    uint32_t r1 = __ldg(lw.unit_rows + rows + 1), r2 = count > 1 ? __ldg(lw.unit_rows + rows + 2) : 0u;
+    uint4 sm0 = ldg_stream(lw.sign_mantissa + smo), sm1 = ldg_stream(lw.sign_mantissa + smo + 512u);
+    if (q > q0 + count)  // the first one is on its way
+      words = fetch(__ldg(lw.unit_rows + rows), r1, i, bytes_of(rb, cg), min(kUnitTiles, lw.ncg - cg));
+    for (uint32_t u = 1; u <= count; ++u, i ^= 1u) {
+      uint32_t next_words = 0;
+      __syncwarp();  // every lane is done with the other buffer
+      if (u < count) {
+        next_words = fetch(r1, r2, i ^ 1u, bytes_of(rb, cg + kUnitTiles),
+                           min(kUnitTiles, lw.ncg - cg - kUnitTiles));
+        r1 = r2;
+        if (u + 1 < count) r2 = __ldg(lw.unit_rows + rows + u + 2);
+      }
+      if (words) {
+        running = __all_sync(0xFFFFFFFFu, mbar_wait(wbar + 8u * i, (phase >> i) & 1u, spin_limit));
+        phase ^= 1u << i;
+        if (!running) {
+          // the copy may still come: leave, once the other one has landed or not
+          if (lane == 0) {
+            report(err, DF11_DEV_ERR_TIMEOUT);
+            if (next_words) mbar_wait(wbar + 8u * (i ^ 1u), (phase >> (i ^ 1u)) & 1u, spin_limit);
+          }
+          break;
         }
-        break;
       }
-    }
-    const uint32_t row0 = buf + i * bytes + 4u * lane;
-    LaneBits s{lds32(row0), lds32(row0 + 128u), 0u, row0 + 256u};
-    for (uint32_t c = 0; c < nt; ++c) {
-      const uint4 v0 = sm0, v1 = sm1;
-      if (c + 1 < nt) smp += kTileElems;
-      else if (more) tile_at(group, ku);
-      sm0 = ldg_stream(smp);
-      sm1 = ldg_stream(smp + 512);
-      if (s.addr - row0 > bytes + 256u) {  // read past the unit's words
-        bad = 1u;
-        s.addr = row0;
-      }
-      if (ok && table) {
-        use.load(cg0 + c);
+      const uint32_t row0 = buf + i * bytes + 4u * lane;
+      LaneBits s{0u, lds32(row0), 30u, row0 + 128u};  // the first bit is bit 0 of b
+      const uint32_t cg1 = min(cg + kUnitTiles, lw.ncg);
+      for (; cg < cg1; ++cg) {
+        if (s.addr - row0 > bytes + 128u) {  // read past the unit's words
+          bad = 1u;
+          s.addr = row0;
+        }
+        // the next tile's bytes, or a tile's that is there for the last one of the row block
+        if (cg + 1 < lw.ncg) smo += kTileElems;
         uint32_t w0[8], w1[8];
-        next16(s, pairs, v0, w0);
-        next16(s, pairs, v1, w1);
-        use(rb, cg0 + c, w0, w1);
+        next16(s, pairs, sm0, w0);
+        sm0 = ldg_stream(lw.sign_mantissa + smo);
+        use.load(cg);
+        next16(s, pairs, sm1, w1);
+        sm1 = ldg_stream(lw.sign_mantissa + smo + 512u);
+        if (words) use(rb, cg, w0, w1);
       }
+      // the longest stream ends in the unit's last word: its bits are those of the words
+      // before b, two more than p says
+      const uint32_t used = (((s.addr - row0) >> 2) - 64u + (s.p & 31u) + 2u + 31u) >> 5;
+      if (words && __reduce_max_sync(0xFFFFFFFFu, used) != words) bad = 1u;
+      words = next_words;
     }
-    // the longest stream ends in the unit's last word
-    const uint32_t used = ((s.addr - row0 - 256u) >> 7) + ((s.p & 31u) ? 1u : 0u);
-    if (__reduce_max_sync(0xFFFFFFFFu, used) != words) bad |= words;
-    words = next_words;
   }
-  while (done < g1) {
-    moved();
-    ++done;
-  }
+  for (; done < g1; ++done) moved(done - g0);
   if (bad) report(err, DF11_DEV_ERR_COUNT);
 }
 
@@ -443,23 +441,24 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 template <int NB>
 struct Multiply {
   float (&acc)[NB][4];
-  const uint16_t *x;  // the lane's token and columns
-  uint64_t step;      // bytes from token n to token n + 8
-  uint32_t tiles;     // tiles in which x has the lane's columns
-  uint32_t tokens;    // of the lane: n = lane / 4 + 8 j, j below this
+  const uint8_t *x;
+  uint32_t offset;  // of the lane's token and columns; 32 rows of x end below 2^32 bytes
+  uint32_t step;    // from token n to token n + 8
+  uint32_t tiles;   // tiles in which x has the lane's columns
+  uint32_t tokens;  // of the lane: n = lane / 4 + 8 j, j below this
   uint4 x0, x1;
   __device__ __forceinline__ Multiply(const LTensor &lt, uint32_t lane, float (&a)[NB][4]) : acc(a) {
     const uint32_t n = lane >> 2, c = 16u * (lane & 3u);
-    x = lt.x + (size_t)n * lt.x_stride + c;
-    step = 16ull * lt.x_stride;
-    tiles = lt.x_cols > c ? (lt.x_cols - c + kTileCols - 1) / kTileCols : 0u;
+    x = reinterpret_cast<const uint8_t *>(lt.x);
+    offset = 2u * (n * lt.x_stride + c);
+    step = 16u * lt.x_stride;
     tokens = lt.batch > n ? (lt.batch - n + 7u) / 8u : 0u;
+    tiles = lt.x_cols > c && tokens ? (lt.x_cols - c + kTileCols - 1) / kTileCols : 0u;
   }
   __device__ __forceinline__ void load_x(uint32_t j, uint32_t cg) {
     x0 = x1 = make_uint4(0, 0, 0, 0);
-    if (j < tokens && cg < tiles) {
-      const uint4 *p = reinterpret_cast<const uint4 *>(
-          reinterpret_cast<const uint8_t *>(x) + j * step + cg * (2u * kTileCols));
+    if ((j == 0 || j < tokens) && cg < tiles) {
+      const uint4 *p = reinterpret_cast<const uint4 *>(x + (offset + j * step + cg * (2u * kTileCols)));
       x0 = __ldg(p);
       x1 = __ldg(p + 1);
     }
@@ -492,10 +491,10 @@ __global__ void __launch_bounds__(kThreads, NB > 2 ? 1 : 2)
   float acc[NB][4];
 #pragma unroll
   for (int j = 0; j < NB; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  float *part = lt.part + ((size_t)cta * lt.slots * kWarps + warp) * (16 * 8 * NB);
   // the warp's sums of a group's row block to the workspace, [token][row]
-  auto moved = [&]() {
-    float *q = part + (2u * (lane & 3u)) * 16u + (lane >> 2);
+  auto moved = [&](uint32_t slot) {
+    float *q = lt.part + (((size_t)cta * lt.slots + slot) * kWarps + warp) * (16 * 8 * NB) +
+               2u * (lane & 3u) * 16u + (lane >> 2);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       q[128 * j] = acc[j][0];
@@ -504,7 +503,6 @@ __global__ void __launch_bounds__(kThreads, NB > 2 ? 1 : 2)
       q[128 * j + 24] = acc[j][3];
       acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
     }
-    part += kWarps * 16 * 8 * NB;
   };
   // x may come from the previous kernel, which may still read the workspace
   auto start = [&]() {
@@ -596,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 2) df11_linear_unpack_kernel(const _
   };
   decode_units(ua.w[ti], blockIdx.x - ua.cta_begin[ti], ua.cta_begin[ti + 1] - ua.cta_begin[ti],
                ua.err, ua.spin_limit, smem, start, StoreTile{ua.out[ti], ua.w[ti].ncg, threadIdx.x & 31u},
-               []() {});
+               [](uint32_t) {});
 }
 
 // ---- building the compressed form --------------------------------------------------------
@@ -648,7 +646,7 @@ __global__ void __launch_bounds__(256) linear_encode_kernel(const __grid_constan
     uint32_t bits = 0;
     uint32_t row = WRITE ? a.unit_rows[u] : 0u;
     const uint32_t end = WRITE ? a.unit_rows[u + 1] : 0u;
-    uint64_t buf = 0;  // the next bits, left-aligned; `bits` of them
+    uint64_t buf = 0;  // the next bits, `bits` of them
     for (uint32_t cg = cg0; cg < cg1; ++cg) {
 #pragma unroll 1
       for (uint32_t h = 0; h < 2; ++h) {
@@ -663,12 +661,12 @@ __global__ void __launch_bounds__(256) linear_encode_kernel(const __grid_constan
           } else {
             const uint32_t byte = (e16 >> 8 & 0x80u) | (e16 & 0x7Fu);
             sm[j >> 2] = (j & 3) ? sm[j >> 2] | byte << (8 * (j & 3)) : byte;
-            buf |= (uint64_t)code_s[exp] << 32 >> bits;
+            buf |= (uint64_t)code_s[exp] << bits;
             bits += len_s[exp];
             if (bits >= 32) {
-              a.streams[(size_t)row * 32u + lane] = (uint32_t)(buf >> 32);
+              a.streams[(size_t)row * 32u + lane] = (uint32_t)buf;
               ++row;
-              buf <<= 32;
+              buf >>= 32;
               bits -= 32;
             }
           }
@@ -680,7 +678,7 @@ __global__ void __launch_bounds__(256) linear_encode_kernel(const __grid_constan
     }
     if constexpr (WRITE) {
       for (; row < end; ++row) {
-        a.streams[(size_t)row * 32u + lane] = (uint32_t)(buf >> 32);
+        a.streams[(size_t)row * 32u + lane] = (uint32_t)buf;
         buf = 0;
       }
     } else {
@@ -1020,9 +1018,10 @@ constexpr uint32_t kFusedMax = 32;
 
 uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
-// x as the kernels read it: 16-byte loads of whole 16-column groups
+// x as the kernels read it: 16-byte loads of whole 16-column groups, by 32-bit offsets
+// when few tokens have rows very far apart
 bool needs_pack(const df11_linear &op, uint32_t cols) {
-  return cols % 16 || op.x_stride % 8 || !aligned(op.x, 16);
+  return cols % 16 || op.x_stride % 8 || !aligned(op.x, 16) || op.x_stride > (1u << 25);
 }
 
 LWeight device_weight(const df11_linear_weight &w) {
@@ -1383,28 +1382,27 @@ df11_status check_linear_devices(const df11_linear_weight *ws, const df11_linear
 
 // The decode table of a code: its lengths (at most kMaxLength) and right-aligned codewords.
 void make_table(const uint8_t len[256], const uint32_t code[256], LinearTable &t) {
-  // by the next kMaxLength bits: the first codeword's exponent (rotated) and length
-  uint32_t sym[1 << kMaxLength] = {}, length[1 << kMaxLength] = {};
+  // by the next kMaxLength bits: the first codeword's exponent and length (bits that no
+  // codeword begins with, as a code of one symbol has them: exponent 0, one bit)
+  uint32_t sym[1 << kMaxLength] = {}, length[1 << kMaxLength];
+  for (uint32_t &l : length) l = 1;
   for (uint32_t e = 0; e < 256; ++e) {
     t.length[e] = len[e];
-    t.code[e] = len[e] ? code[e] << (32 - len[e]) : 0u;
+    t.code[e] = 0;
+    for (uint32_t i = 0; i < len[e]; ++i) t.code[e] |= (code[e] >> i & 1u) << (len[e] - 1 - i);
     if (!len[e]) continue;
-    const uint32_t free = kMaxLength - len[e];
-    for (uint32_t i = code[e] << free; i < (code[e] + 1u) << free; ++i) {
-      sym[i] = (e >> 1 | e << 7) & 0xFFu;
+    for (uint32_t i = t.code[e]; i < 1u << kMaxLength; i += 1u << len[e]) {
+      sym[i] = e;
       length[i] = len[e];
     }
   }
-  // bits that no codeword begins with (a code of one symbol has such): a length of one
-  for (uint32_t i = 0; i < 1u << kMaxLength; ++i)
-    if (!length[i]) length[i] = 1;
+  constexpr uint32_t kMask = (1u << kMaxLength) - 1u;
   for (uint32_t i = 0; i < kPairs; ++i) {
-    const uint32_t a = i >> (kPairBits - kMaxLength);
-    const uint32_t b = ((i << length[a]) & (kPairs - 1)) >> (kPairBits - kMaxLength);
-    const uint32_t first = length[a] << 24 | sym[a] << 8;
+    const uint32_t a = i & kMask, b = (i >> length[a]) & kMask;
+    const uint32_t first = length[a] << 16 | sym[a] << 7;
     t.pair[i] = length[a] + length[b] <= (uint32_t)kPairBits
-                    ? first | sym[b] << 16 | (length[a] + length[b])
-                    : kFirstOnly | first | length[a];
+                    ? first | sym[b] << 23 | (length[a] + length[b])
+                    : first | kFirstOnly | length[a];
   }
 }
 

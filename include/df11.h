@@ -282,13 +282,13 @@ typedef struct df11_linear_params {
 
 typedef struct df11_linear_weight {
   const uint32_t *streams;      /* 16-byte aligned, stream_rows * 32 words: a unit's streams word
-                                   by word, first bit = bit 31 */
+                                   by word, first bit = bit 0 */
   const uint32_t *unit_rows;    /* first row of each unit, and the total after them */
   const uint8_t *sign_mantissa; /* 16-byte aligned: per tile 16 bytes of each stream for rows
                                    0 .. 7, then for rows 8 .. 15 */
   const void *table;            /* 16-byte aligned, DF11_LINEAR_TABLE_BYTES: the decode table
                                    of 4096 words, then by exponent 256 codewords (first bit
-                                   = bit 31) and 256 lengths */
+                                   = bit 0) and 256 lengths */
   df11_linear_params params;
 } df11_linear_weight;
 

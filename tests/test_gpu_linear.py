@@ -299,7 +299,7 @@ def _lane_streams(w):
     sm = w.sign_mantissa.cpu().numpy().reshape(rows // 16, cols // 64, 2, 32, 16)
     # the code, from its stored codewords and lengths
     tail = w.table.cpu().numpy()[-2048:].view(np.uint32)
-    book = {(int(tail[256 + e]), int(tail[e]) >> (32 - int(tail[256 + e]))): e
+    book = {f"{int(tail[e]):b}".zfill(int(tail[256 + e]))[::-1]: e
             for e in range(256) if tail[256 + e]}
     out = np.zeros((rows, cols), np.uint16)
     per_row = -(-cols // 256)
@@ -308,15 +308,15 @@ def _lane_streams(w):
     for u in range(len(first) - 1):
         rb, k = divmod(u, per_row)
         for lane in range(32):
-            bits = "".join(f"{x:032b}" for x in words[first[u]:first[u + 1], lane])
+            bits = "".join(f"{x:032b}"[::-1] for x in words[first[u]:first[u + 1], lane])
             at = 0
             for cg in range(4 * k, min(4 * k + 4, cols // 64)):
                 for h in range(2):
                     for j in range(16):
                         n = 1
-                        while (n, int(bits[at:at + n], 2)) not in book:
+                        while bits[at:at + n] not in book:
                             n += 1
-                        e = book[n, int(bits[at:at + n], 2)]
+                        e = book[bits[at:at + n]]
                         at += n
                         b = int(sm[rb, cg, h, lane, j])
                         out[16 * rb + 8 * h + lane // 4, 64 * cg + 16 * (lane % 4) + j] = \
