@@ -154,18 +154,21 @@ df11_status launch_cluster(void (*kern)(Args...), uint32_t ctas, uint32_t thread
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DF11_OK : DF11_ERR_CUDA;
 }
 
+// The kernel's shared-memory limit raised to `smem` where needed, and the thread blocks of
+// it that the device holds.  `carveout`: percentage of the SM's memory asked for as shared
+// memory; the default is all of it, since most kernels here keep their working set there,
+// and the occupancy query assumes this split.
 template <typename K>
-df11_status prepare(K kern, int threads, size_t smem, int instance, uint64_t &budget) {
+df11_status prepare(K kern, int threads, size_t smem, int instance, uint64_t &budget,
+                    int carveout = 100) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DF11_ERR_CUDA;
   DeviceInfo &di = device_info(dev);
   if (instance < 0 || instance >= kInstances) return DF11_ERR_INVALID;
   if (smem > 48 * 1024 && di.configured[instance].load() < smem) {
-    // all of the unified L1 as shared memory: these kernels keep their
-    // working set there, and the occupancy query assumes this split
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
             cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, carveout) !=
             cudaSuccess)
       return DF11_ERR_CUDA;
     di.configured[instance].store(smem);

@@ -40,32 +40,38 @@ namespace {
 
 constexpr uint32_t kTileRows = 16, kTileCols = 64, kTileElems = kTileRows * kTileCols;
 constexpr uint32_t kUnitTiles = 4;
-constexpr int kWarps = 16;  // warps of a thread block: a group of 16 row blocks, one each
-constexpr int kThreads = 32 * kWarps;
+// Warps of a thread block (W below), of which an SM holds one: one per row block of a group.
+// Decoding is a chain of dependent lookups, so its rate follows the warps: 260 us with 32
+// warps, 284 with 24, 335 with 16 for 151936 x 4096 and 8 tokens.  16 where the streams are
+// too long for more, and above 8 tokens, where the activations of a tile need the registers
+// (12288 x 4096, 16 tokens: 43.1 us with 16 warps, 46.5 with 32).
+constexpr int kManyWarps = 32, kFewWarps = 16;
 
 // ---- the code and its decode table ------------------------------------------------
 //
-// Codewords of at most 8 bits: 0.08 bits longer on average than the unlimited code of
-// Gaussian weights, but two codewords nearly always lie inside kPairBits bits: 0.08% of the
-// pairs exceed 12 bits, 0.4% with unlimited codewords, and a warp waits for any of its 32
-// lanes.  The streams are filled from bit 0 of a word up, a codeword's first bit lowest.
-//
-// Pair table, indexed by the next kPairBits bits: bits 7-14 and 23-30 the exponents of two
-// codewords, where a pair of BF16 words has them, bits 0-3 the length of both together,
-// bits 16-19 the first one's; when the second one does not lie inside, kFirstOnly, and bits
-// 0-3 have the first one's length.  Bits 4-6 are zero, so that two entries' sum has the
-// length of both in its low six bits.
+// Codewords of at most 8 bits (0.08 bits longer on average than the unlimited code of
+// Gaussian weights), so that a table of 256 entries has every one of them, and small enough
+// that each lane of a warp has a copy in its own bank of shared memory: entry i of lane l at
+// byte 256 i + 4 l.  A lookup then costs one wavefront (a table shared by the lanes: 3.4
+// for 32 lanes at independent places), and four codewords need at most the 32 bits
+// of one window.  The streams are filled from bit 0 of a word up, a codeword's first
+// bit lowest.
+// An entry: bits 0-3 the codeword's length, bits 7-14 the exponent, where a BF16 word has
+// it; the others zero, so that a sum of four entries has the lengths' sum in its low six
+// bits.  The sign and mantissa bits of four weights are one word: those of the first two
+// where a pair of BF16 words has them, those of the other two where the pair has exponents,
+// so that a rotation by a byte puts them in place.
+//   The steps are bound by the ALU pipe (half rate), so what can be a multiply-add is one.
 constexpr int kMaxLength = 8;
-constexpr int kPairBits = 12;
-constexpr uint32_t kPairs = 1u << kPairBits;
-constexpr uint32_t kFirstOnly = 1u << 20;
+constexpr uint32_t kEntries = 1u << kMaxLength;
+constexpr uint32_t kTableBytes = 256u * kEntries;  // in shared memory; 128 of each 256 used
 constexpr uint32_t kExponents = 0x7F807F80u;
 // Words of a lane's stream in a unit, at most.
 constexpr uint32_t kMaxWords = kUnitTiles * 32u * kMaxLength / 32u;
 struct LinearTable {
-  uint32_t pair[kPairs];
-  uint32_t code[256];    // by exponent: the codeword, first bit lowest, and its length
-  uint32_t length[256];  // (for the builder)
+  uint32_t entry[kEntries];
+  uint8_t code[256];    // by exponent: the codeword, first bit lowest, and its length
+  uint8_t length[256];  // (for the builder)
 };
 static_assert(sizeof(LinearTable) == DF11_LINEAR_TABLE_BYTES, "table layout");
 
@@ -163,25 +169,25 @@ struct LWeight {
   const LinearTable *table;
   uint32_t rbs, ncg, upr;         // row blocks, tiles and units per row block
   uint32_t max_words, stream_rows;
+  uint32_t one, k64;              // 1 and 65536 (see next4)
 };
 
-// Two words of the lane's stream, b after a, and where the word after them is.  The next bit
-// is bit (p & 31) + 2 of a, or bit (p & 31) - 30 of b: two bits on from p, so that a window
-// has the table's index where an address needs it.  Bit 5 of p is zero between steps; bits 7
-// and up are not kept clean (the table's entries are added whole).
+// Two words of the lane's stream, b after a, with the next bit at bit (p & 31) of a, and
+// where the word after them is.  Bits 6 and up of p are not kept clean (the table's entries
+// are added whole).
 struct LaneBits {
   uint32_t a, b, p, addr;
-  // past a word: without a branch, since in most steps some lane has reached its end
-  __device__ __forceinline__ void refill() {
+  // to position `t`, at most 32 bits on, which is past a word when bit 5 changes: without a
+  // branch, since in most steps some lane has reached its word's end
+  __device__ __forceinline__ void move(uint32_t t, uint32_t one) {
     asm volatile(
-        "{\n .reg .pred q;\n .reg .b32 t;\n"
-        " and.b32 t, %2, 32;\n setp.ne.b32 q, t, 0;\n"
-        " @q mov.b32 %0, %1;\n @q ld.shared.b32 %1, [%3];\n"
-        " @q add.s32 %3, %3, 128;\n @q xor.b32 %2, %2, 32;\n}\n"
-        : "+r"(a), "+r"(b), "+r"(p), "+r"(addr));
+        "{\n .reg .pred q;\n .reg .b32 x;\n"
+        " xor.b32 x, %2, %4;\n and.b32 x, x, 32;\n setp.ne.b32 q, x, 0;\n"
+        " @q mul.lo.u32 %0, %1, %5;\n @q ld.shared.b32 %1, [%3];\n"
+        " @q mad.lo.u32 %3, %5, 128, %3;\n mov.b32 %2, %4;\n}\n"
+        : "+r"(a), "+r"(b), "+r"(p), "+r"(addr)
+        : "r"(t), "r"(one));
   }
-  // the next 30 bits, from bit 2 on
-  __device__ __forceinline__ uint32_t window() const { return __funnelshift_r(a, b, p); }
 };
 
 // A value that the compiler keeps in a register instead of computing it again: it would
@@ -191,47 +197,39 @@ __device__ __forceinline__ uint32_t keep(uint32_t v) {
   return v;
 }
 
-// The pair table's entry of a window; the table starts at a multiple of its size, so that
-// its address takes one instruction.
-__device__ __forceinline__ uint32_t look_up(uint32_t pairs, uint32_t window) {
-  return lds32((window & (4u * kPairs - 4u)) | pairs);
+// The entry of the codeword at the start of a window: `table` is the lane's copy, which
+// starts at a multiple of 64 KB plus 4 times the lane, so one byte permute has the address.
+__device__ __forceinline__ uint32_t look_up(uint32_t table, uint32_t window) {
+  return lds32(__byte_perm(window, table, 0x7604));
 }
 
-// Two exponents from the stream's state, however long their codewords.
-__device__ __forceinline__ uint32_t slow_pair(LaneBits &s, uint32_t pairs) {
-  uint32_t e = look_up(pairs, s.window());
-  s.p += e & 15u;
-  s.refill();
-  if (e & kFirstOnly) {
-    const uint32_t f = look_up(pairs, s.window());
-    s.p += (f >> 16) & 15u;
-    s.refill();
-    e = (e & 0x7F80u) | (f & 0x7F80u) << 16;
-  }
-  return e;
+// The next four weights, two BF16 per word, from their sign and mantissa bits.  The shifts
+// use an entry's low five bits: the length.  `one` and `k64` are 1 and 65536, arguments of
+// the launch because the compiler would not multiply by constants like these.
+__device__ __forceinline__ void next4(LaneBits &s, uint32_t table, uint32_t one, uint32_t k64,
+                                      uint32_t sm, uint32_t &w0, uint32_t &w1) {
+  uint32_t w = __funnelshift_r(s.a, s.b, s.p);
+  const uint32_t e0 = look_up(table, w);
+  w = __funnelshift_r(w, 0u, e0);
+  const uint32_t e1 = look_up(table, w);
+  w = __funnelshift_r(w, 0u, e1);
+  const uint32_t e2 = look_up(table, w);
+  w = __funnelshift_r(w, 0u, e2);
+  const uint32_t e3 = look_up(table, w);
+  s.move(e3 * one + (e2 * one + (e1 * one + (e0 * one + s.p))), one);
+  w0 = ((e1 * k64 + e0) & kExponents) | (sm & ~kExponents);
+  w1 = ((e3 * k64 + e2) & kExponents) | (__byte_perm(sm, 0, 0x0321) & ~kExponents);
 }
 
-// The next four weights, two BF16 per word, from their four sign/mantissa bytes.  One
-// window serves both lookups: two pairs take at most 24 of its 30 bits.
-__device__ __forceinline__ void next4(LaneBits &s, uint32_t pairs, uint32_t sm, uint32_t &w0,
-                                      uint32_t &w1) {
-  const uint32_t w = s.window();
-  uint32_t e1 = look_up(pairs, w);
-  // shifts by the low five bits: the length
-  uint32_t e2 = look_up(pairs, __funnelshift_r(w, 0u, e1));
-  if ((e1 | e2) & kFirstOnly) {
-    e1 = slow_pair(s, pairs);
-    e2 = slow_pair(s, pairs);
-  } else {
-    s.p += e1 + e2;
-    s.refill();
-  }
-  // a byte twice in a half word: sign in bit 15, mantissa in bits 0-6
-  const uint32_t lo = __byte_perm(sm, 0, 0x1100), hi = __byte_perm(sm, 0, 0x3322);
-  w0 = (e1 & kExponents) | (lo & ~kExponents);
-  w1 = (e2 & kExponents) | (hi & ~kExponents);
+// 16 weights of a lane
+__device__ __forceinline__ void next16(LaneBits &s, uint32_t table, uint32_t one, uint32_t k64,
+                                       const uint4 &sm, uint32_t (&w)[8]) {
+  const uint32_t v[4] = {sm.x, sm.y, sm.z, sm.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) next4(s, table, one, k64, v[j], w[2 * j], w[2 * j + 1]);
 }
 
+// 16 bytes that are read once
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -240,39 +238,31 @@ __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
   return v;
 }
 
-// 16 weights of a lane
-__device__ __forceinline__ void next16(LaneBits &s, uint32_t pairs, const uint4 &sm,
-                                       uint32_t (&w)[8]) {
-  const uint32_t v[4] = {sm.x, sm.y, sm.z, sm.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) next4(s, pairs, v[j], w[2 * j], w[2 * j + 1]);
-}
-
 // A warp's walk over its units: thread block `cta` of `ctas` has an equal, contiguous
-// share of the units in the order (group of 16 row blocks, unit along the rows, row block
-// of the group), and warp w of it those of the group's row block w.  So the warps of a
+// share of the units in the order (group of W row blocks, unit along the rows, row block of
+// the group), and warp w of it those of the group's row block w.  So the warps of a
 // thread block are at the same columns of x at about the same time.
 __device__ __host__ __forceinline__ uint64_t first_unit(uint64_t cta, uint64_t units, uint64_t ctas) {
   return cta * units / ctas;
 }
 // units in that order, row blocks past the last included
-__device__ __host__ __forceinline__ uint64_t ordered_units(uint32_t rbs, uint32_t upr) {
-  return (uint64_t)((rbs + kWarps - 1) / kWarps) * upr * kWarps;
+__device__ __host__ __forceinline__ uint64_t ordered_units(uint32_t rbs, uint32_t upr, uint32_t w) {
+  return (uint64_t)((rbs + w - 1) / w) * upr * w;
 }
 
-// Shared memory: barriers (two per warp and the table's), the warps' buffers (two units
-// each) on both sides of the table, which starts at a multiple of its size, and room for
-// what a lane of an inconsistent stream can read past its buffer before a tile's check
-// stops it (at most 32 refills, two words ahead).
-constexpr uint32_t kBarBytes = 384;
-constexpr uint32_t kOverrun = 128u * (32u + 2u);
-static_assert(kBarBytes >= 8 * (2 * kWarps + 1) && kBarBytes % 128 == 0, "barriers");
+// Shared memory: barriers (two per warp), the warps' buffers (two units each) on both sides
+// of the table, which starts at a multiple of its size, and room for what a lane of an
+// inconsistent stream can read past its buffer before a tile's check stops it (at most 8
+// refills, two words ahead).
+constexpr uint32_t kBarBytes = 512;
+constexpr uint32_t kOverrun = 128u * (8u + 2u);
+static_assert(kBarBytes >= 16 * kManyWarps && kBarBytes % 128 == 0, "barriers");
 
-__device__ __host__ constexpr uint32_t decode_smem(uint32_t max_words) {
+__device__ __host__ constexpr uint32_t decode_smem(uint32_t max_words, uint32_t warps) {
   // the space before the table is below the table's size, and holds all buffers or leaves
   // less than one warp's free
-  const uint32_t buffers = (kWarps + 1) * 2u * max_words * 128u;
-  return kBarBytes + (buffers > 4u * kPairs ? buffers : 4u * kPairs) + 4u * kPairs + kOverrun;
+  const uint32_t buffers = (warps + 1) * 2u * max_words * 128u;
+  return kBarBytes + (buffers > kTableBytes ? buffers : kTableBytes) + kTableBytes + kOverrun;
 }
 
 // The decoding side of both kernels: `use.load(cg)` and `use(rb, cg, w0, w1)` get every
@@ -282,36 +272,32 @@ __device__ __host__ constexpr uint32_t decode_smem(uint32_t max_words) {
 // A unit's streams are copied into one of the warp's two buffers while it decodes the
 // other; the rows of the unit after that and the next tile's sign/mantissa bytes are
 // loaded ahead along a row block.
-template <typename Start, typename Use, typename Moved>
+template <int W, typename Start, typename Use, typename Moved>
 __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, uint32_t ctas,
                                              int32_t *err, uint32_t spin_limit, uint8_t *smem,
                                              Start start, Use use, Moved moved) {
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t bars = keep(smem_addr(smem));
-  const uint32_t tbar = bars + 8u * (2 * kWarps), wbar = bars + 16u * warp;
+  const uint32_t bars = keep(smem_addr(smem)), wbar = bars + 16u * warp;
   const uint32_t bytes = lw.max_words * 128u;
-  const uint32_t pairs = keep((bars + kBarBytes + 4u * kPairs - 1u) & ~(4u * kPairs - 1u));
-  const uint32_t before = min((pairs - bars - kBarBytes) / (2u * bytes), (uint32_t)kWarps);
+  const uint32_t at = (bars + kBarBytes + kTableBytes - 1u) & ~(kTableBytes - 1u);
+  const uint32_t before = min((at - bars - kBarBytes) / (2u * bytes), (uint32_t)W);
   const uint32_t buf = keep(warp < before ? bars + kBarBytes + warp * 2u * bytes
-                                          : pairs + 4u * kPairs + (warp - before) * 2u * bytes);
-  if (tid < 2 * kWarps + 1) {
-    mbar_init(bars + 8u * tid, 1);
+                                          : at + kTableBytes + (warp - before) * 2u * bytes);
+  const uint32_t table = keep(at + 4u * lane), one = lw.one, k64 = lw.k64;
+  if (lane < 2) {  // the warp's own barriers
+    mbar_init(wbar + 8u * lane, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  __syncthreads();
-  if (tid == 0) {
-    mbar_arrive_expect_tx(tbar, 4u * kPairs);
-    bulk_g2s(pairs, lw.table->pair, 4u * kPairs, tbar);
-  }
-  const uint64_t units = ordered_units(lw.rbs, lw.upr);
+  __syncwarp();
+  const uint64_t units = ordered_units(lw.rbs, lw.upr, W);
   const uint64_t o0 = first_unit(cta, units, ctas), o1 = first_unit(cta + 1, units, ctas);
-  const uint32_t per_group = lw.upr * kWarps;
+  const uint32_t per_group = lw.upr * W;
   const uint32_t g0 = (uint32_t)(o0 / per_group), g1 = (uint32_t)((o1 + per_group - 1) / per_group);
   // this warp's units: q = group * upr + (unit along the rows), [q0, q1), without those of
   // row blocks past the last
-  const uint32_t q0 = (uint32_t)((o0 + kWarps - 1 - warp) / kWarps);
-  const uint32_t mine = warp < lw.rbs ? ((lw.rbs - 1 - warp) / kWarps + 1) * lw.upr : 0u;
-  const uint32_t q1 = min((uint32_t)((o1 + kWarps - 1 - warp) / kWarps), mine);
+  const uint32_t q0 = (uint32_t)((o0 + W - 1 - warp) / W);
+  const uint32_t mine = warp < lw.rbs ? ((lw.rbs - 1 - warp) / W + 1) * lw.upr : 0u;
+  const uint32_t q1 = min((uint32_t)((o1 + W - 1 - warp) / W), mine);
   // rows [r0, r1) of a unit into buffer i, and its sign/mantissa bytes (from byte `sm` on)
   // into L2; returns the words, 0 when the table of rows is inconsistent
   auto fetch = [&](uint32_t r0, uint32_t r1, uint32_t i, uint32_t sm, uint32_t tiles) -> uint32_t {
@@ -333,23 +319,22 @@ __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, ui
   };
   uint32_t words = 0;
   if (q0 < q1) {
-    const uint32_t rb = q0 / lw.upr * kWarps + warp, ku = q0 % lw.upr;
+    const uint32_t rb = q0 / lw.upr * W + warp, ku = q0 % lw.upr;
     const uint32_t *rows = lw.unit_rows + (rb * lw.upr + ku);
     words = fetch(__ldg(rows), __ldg(rows + 1), 0, bytes_of(rb, ku * kUnitTiles),
                   min(kUnitTiles, lw.ncg - ku * kUnitTiles));
   }
+  for (uint32_t e = warp; e < kEntries; e += W)  // every lane's copy of the table
+    sts32(table + 256u * e, __ldg(lw.table->entry + e));
+  __syncthreads();
   bool running = true;
-  if (!__all_sync(0xFFFFFFFFu, mbar_wait(tbar, 0, spin_limit))) {
-    if (lane == 0) report(err, DF11_DEV_ERR_TIMEOUT);
-    running = false;
-  }
   start();
   uint32_t done = g0, bad = 0;
   uint32_t i = 0, phase = 0;  // buffer of the current unit; bit j: parity of buffer j's next wait
   for (uint32_t q = q0; q < q1 && running;) {
     // the units of one row block
     const uint32_t group = q / lw.upr, ku = q - group * lw.upr, count = min(lw.upr - ku, q1 - q);
-    const uint32_t rb = group * kWarps + warp;
+    const uint32_t rb = group * W + warp;
     q += count;
     for (; done < group; ++done) moved(done - g0);
     const uint32_t rows = rb * lw.upr + ku;
@@ -381,26 +366,25 @@ __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, ui
         }
       }
       const uint32_t row0 = buf + i * bytes + 4u * lane;
-      LaneBits s{0u, lds32(row0), 30u, row0 + 128u};  // the first bit is bit 0 of b
+      LaneBits s{lds32(row0), lds32(row0 + 128u), 0u, row0 + 256u};
       const uint32_t cg1 = min(cg + kUnitTiles, lw.ncg);
       for (; cg < cg1; ++cg) {
-        if (s.addr - row0 > bytes + 128u) {  // read past the unit's words
+        if (s.addr - row0 > bytes + 256u) {  // read past the unit's words
           bad = 1u;
           s.addr = row0;
         }
         // the next tile's bytes, or a tile's that is there for the last one of the row block
         if (cg + 1 < lw.ncg) smo += kTileElems;
         uint32_t w0[8], w1[8];
-        next16(s, pairs, sm0, w0);
-        sm0 = ldg_stream(lw.sign_mantissa + smo);
         use.load(cg);
-        next16(s, pairs, sm1, w1);
+        next16(s, table, one, k64, sm0, w0);
+        sm0 = ldg_stream(lw.sign_mantissa + smo);
+        next16(s, table, one, k64, sm1, w1);
         sm1 = ldg_stream(lw.sign_mantissa + smo + 512u);
         if (words) use(rb, cg, w0, w1);
       }
-      // the longest stream ends in the unit's last word: its bits are those of the words
-      // before b, two more than p says
-      const uint32_t used = (((s.addr - row0) >> 2) - 64u + (s.p & 31u) + 2u + 31u) >> 5;
+      // the longest stream ends in the unit's last word
+      const uint32_t used = ((s.addr - row0 - 256u) >> 7) + (s.p & 31u ? 1u : 0u);
       if (words && __reduce_max_sync(0xFFFFFFFFu, used) != words) bad = 1u;
       words = next_words;
     }
@@ -446,7 +430,7 @@ struct Multiply {
   uint32_t step;    // from token n to token n + 8
   uint32_t tiles;   // tiles in which x has the lane's columns
   uint32_t tokens;  // of the lane: n = lane / 4 + 8 j, j below this
-  uint4 x0, x1;
+  uint4 xv[NB][2];
   __device__ __forceinline__ Multiply(const LTensor &lt, uint32_t lane, float (&a)[NB][4]) : acc(a) {
     const uint32_t n = lane >> 2, c = 16u * (lane & 3u);
     x = reinterpret_cast<const uint8_t *>(lt.x);
@@ -455,30 +439,38 @@ struct Multiply {
     tokens = lt.batch > n ? (lt.batch - n + 7u) / 8u : 0u;
     tiles = lt.x_cols > c && tokens ? (lt.x_cols - c + kTileCols - 1) / kTileCols : 0u;
   }
-  __device__ __forceinline__ void load_x(uint32_t j, uint32_t cg) {
-    x0 = x1 = make_uint4(0, 0, 0, 0);
-    if ((j == 0 || j < tokens) && cg < tiles) {
-      const uint4 *p = reinterpret_cast<const uint4 *>(x + (offset + j * step + cg * (2u * kTileCols)));
-      x0 = __ldg(p);
-      x1 = __ldg(p + 1);
+  // issued where it stands, before the tile is decoded: the compiler would move plain loads
+  // down to the products
+  __device__ __forceinline__ void load(uint32_t cg) {
+#pragma unroll
+    for (uint32_t j = 0; j < NB; ++j) {
+      const uint8_t *p = x + (offset + j * step + cg * (2u * kTileCols));
+      const uint32_t there = (j == 0 || j < tokens) && cg < tiles;
+      asm volatile(
+          "{\n .reg .pred q;\n setp.ne.u32 q, %9, 0;\n"
+          " mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+          " mov.b32 %4, 0;\n mov.b32 %5, 0;\n mov.b32 %6, 0;\n mov.b32 %7, 0;\n"
+          " @q ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%8];\n"
+          " @q ld.global.nc.v4.b32 {%4, %5, %6, %7}, [%8 + 16];\n}\n"
+          : "=&r"(xv[j][0].x), "=&r"(xv[j][0].y), "=&r"(xv[j][0].z), "=&r"(xv[j][0].w),
+            "=&r"(xv[j][1].x), "=&r"(xv[j][1].y), "=&r"(xv[j][1].z), "=&r"(xv[j][1].w)
+          : "l"(p), "r"(there));
     }
   }
-  __device__ __forceinline__ void load(uint32_t cg) { load_x(0, cg); }
-  __device__ __forceinline__ void operator()(uint32_t, uint32_t cg, const uint32_t (&w0)[8],
+  __device__ __forceinline__ void operator()(uint32_t, uint32_t, const uint32_t (&w0)[8],
                                              const uint32_t (&w1)[8]) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      mma_bf16(acc[j], w0[0], w1[0], w0[1], w1[1], x0.x, x0.y);
-      mma_bf16(acc[j], w0[2], w1[2], w0[3], w1[3], x0.z, x0.w);
-      mma_bf16(acc[j], w0[4], w1[4], w0[5], w1[5], x1.x, x1.y);
-      mma_bf16(acc[j], w0[6], w1[6], w0[7], w1[7], x1.z, x1.w);
-      if (j + 1 < NB) load_x(j + 1, cg);
+      mma_bf16(acc[j], w0[0], w1[0], w0[1], w1[1], xv[j][0].x, xv[j][0].y);
+      mma_bf16(acc[j], w0[2], w1[2], w0[3], w1[3], xv[j][0].z, xv[j][0].w);
+      mma_bf16(acc[j], w0[4], w1[4], w0[5], w1[5], xv[j][1].x, xv[j][1].y);
+      mma_bf16(acc[j], w0[6], w1[6], w0[7], w1[7], xv[j][1].z, xv[j][1].w);
     }
   }
 };
 
-template <int NB>
-__global__ void __launch_bounds__(kThreads, NB > 2 ? 1 : 2)
+template <int NB, int W>
+__global__ void __launch_bounds__(32 * W, 1)
     df11_linear_kernel(const __grid_constant__ LBatch lb) {
   extern __shared__ __align__(128) uint8_t smem[];
   int ti = 0;
@@ -493,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, NB > 2 ? 1 : 2)
   for (int j = 0; j < NB; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
   // the warp's sums of a group's row block to the workspace, [token][row]
   auto moved = [&](uint32_t slot) {
-    float *q = lt.part + (((size_t)cta * lt.slots + slot) * kWarps + warp) * (16 * 8 * NB) +
+    float *q = lt.part + (((size_t)cta * lt.slots + slot) * W + warp) * (16 * 8 * NB) +
                2u * (lane & 3u) * 16u + (lane >> 2);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -509,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, NB > 2 ? 1 : 2)
     pdl_wait();
     pdl_launch_dependents();
   };
-  decode_units(lt.w, cta, ctas, lb.err, lb.spin_limit, smem, start, Multiply<NB>(lt, lane, acc), moved);
+  decode_units<W>(lt.w, cta, ctas, lb.err, lb.spin_limit, smem, start, Multiply<NB>(lt, lane, acc), moved);
 }
 
 // The warps' sums of every row block added in a fixed order, and the epilogue.
@@ -523,7 +515,7 @@ struct FTensor {
 struct FBatch {
   FTensor t[DF11_MAX_BATCH];
   int count;
-  uint32_t nb;  // groups of 8 tokens in the workspace's layout
+  uint32_t nb, warps;  // groups of 8 tokens, warps per thread block in the workspace's layout
 };
 constexpr int kFinishThreads = 128;
 
@@ -542,18 +534,19 @@ __global__ void __launch_bounds__(kFinishThreads)
   pdl_launch_dependents();
   if (rb >= ft.rbs || row >= ft.rows) return;
   // the thread blocks that hold units of the row block's group
-  const uint64_t units = ordered_units(ft.rbs, ft.upr), per_group = (uint64_t)ft.upr * kWarps;
-  const uint64_t group = rb / kWarps;
+  const uint64_t units = ordered_units(ft.rbs, ft.upr, fb.warps), per_group = (uint64_t)ft.upr * fb.warps;
+  const uint64_t group = rb / fb.warps;
   auto holder = [&](uint64_t o) { return (uint32_t)(((o + 1) * ft.ctas - 1) / units); };
   const uint32_t c0 = holder(group * per_group), c1 = holder((group + 1) * per_group - 1);
   const uint32_t per_warp = 16u * 8u * fb.nb;
-  const float *p = ft.part + (size_t)(rb % kWarps) * per_warp + token * 16u + r;
+  const float *p = ft.part + (size_t)(rb % fb.warps) * per_warp + token * 16u + r;
   float sum = 0.f;
   // slot of the group in a thread block's part: 0 but for those that begin before it
   sum = __ldcg(p + ((size_t)c0 * ft.slots + (group - first_unit(c0, units, ft.ctas) / per_group)) *
-                       kWarps * per_warp);
+                       fb.warps * per_warp);
 #pragma unroll 4
-  for (uint32_t c = c0 + 1; c <= c1; ++c) sum += __ldcg(p + (size_t)c * ft.slots * kWarps * per_warp);
+  for (uint32_t c = c0 + 1; c <= c1; ++c)
+    sum += __ldcg(p + (size_t)c * ft.slots * fb.warps * per_warp);
   store_any(ft.e, finish(ft.e, sum, token, row), token, row);
 }
 
@@ -583,7 +576,9 @@ struct StoreTile {
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 2) df11_linear_unpack_kernel(const __grid_constant__ UArgs ua) {
+template <int W>
+__global__ void __launch_bounds__(32 * W, 1)
+    df11_linear_unpack_kernel(const __grid_constant__ UArgs ua) {
   extern __shared__ __align__(128) uint8_t smem[];
   int ti = 0;
   for (int i = 1; i < ua.count; ++i)
@@ -592,8 +587,8 @@ __global__ void __launch_bounds__(kThreads, 2) df11_linear_unpack_kernel(const _
     pdl_wait();
     pdl_launch_dependents();
   };
-  decode_units(ua.w[ti], blockIdx.x - ua.cta_begin[ti], ua.cta_begin[ti + 1] - ua.cta_begin[ti],
-               ua.err, ua.spin_limit, smem, start, StoreTile{ua.out[ti], ua.w[ti].ncg, threadIdx.x & 31u},
+  decode_units<W>(ua.w[ti], blockIdx.x - ua.cta_begin[ti], ua.cta_begin[ti + 1] - ua.cta_begin[ti],
+                  ua.err, ua.spin_limit, smem, start, StoreTile{ua.out[ti], ua.w[ti].ncg, threadIdx.x & 31u},
                [](uint32_t) {});
 }
 
@@ -659,8 +654,12 @@ __global__ void __launch_bounds__(256) linear_encode_kernel(const __grid_constan
           if (!WRITE) {
             bits += len_s[exp];
           } else {
-            const uint32_t byte = (e16 >> 8 & 0x80u) | (e16 & 0x7Fu);
-            sm[j >> 2] = (j & 3) ? sm[j >> 2] | byte << (8 * (j & 3)) : byte;
+            const uint32_t sign = e16 >> 15, man = e16 & 0x7Fu;
+            const uint32_t bits4 = (j & 3) == 0   ? man | sign << 15
+                                   : (j & 3) == 1 ? man << 16 | sign << 31
+                                   : (j & 3) == 2 ? man << 8 | sign << 23
+                                                  : man << 24 | sign << 7;
+            sm[j >> 2] = (j & 3) ? sm[j >> 2] | bits4 : bits4;
             buf |= (uint64_t)code_s[exp] << bits;
             bits += len_s[exp];
             if (bits >= 32) {
@@ -1036,6 +1035,8 @@ LWeight device_weight(const df11_linear_weight &w) {
   l.upr = (l.ncg + kUnitTiles - 1) / kUnitTiles;
   l.max_words = p.max_words;
   l.stream_rows = p.stream_rows;
+  l.one = 1;
+  l.k64 = 65536;
   return l;
 }
 
@@ -1044,14 +1045,14 @@ uint64_t padded(const df11_linear_params &p) {
 }
 
 // the thread blocks of a launch over its weights, by units
-df11_status split_units(const df11_linear_weight *ws, int count, uint64_t budget, uint64_t *ctas) {
+void split_units(const df11_linear_weight *ws, int count, uint32_t warps, uint64_t budget,
+                 uint64_t *ctas) {
   uint32_t units[DF11_MAX_BATCH];
   for (int i = 0; i < count; ++i) {
     const LWeight l = device_weight(ws[i]);
-    units[i] = (uint32_t)ordered_units(l.rbs, l.upr);
+    units[i] = (uint32_t)ordered_units(l.rbs, l.upr, warps);
   }
   split_blocks(units, count, budget, ctas);
-  return DF11_OK;
 }
 
 uint32_t longest_stream(const df11_linear_weight *ws, int count) {
@@ -1062,7 +1063,7 @@ uint32_t longest_stream(const df11_linear_weight *ws, int count) {
 
 struct Plan {
   bool fused = false;
-  uint32_t nb = 1;                       // groups of 8 tokens (fused)
+  uint32_t nb = 1, warps = 0;            // groups of 8 tokens, warps per thread block (fused)
   uint64_t ctas[DF11_MAX_BATCH] = {};    // thread blocks per weight (fused)
   uint32_t slots[DF11_MAX_BATCH] = {};
   uint64_t part[DF11_MAX_BATCH] = {};    // workspace offsets: partial sums or decoded weight
@@ -1071,10 +1072,20 @@ struct Plan {
   size_t smem = 0;
 };
 
+// warps per thread block whose buffers fit in shared memory beside the table
+uint32_t warps_for(uint32_t max_words) {
+  return decode_smem(max_words, kManyWarps) <= 227 * 1024 ? kManyWarps : kFewWarps;
+}
+
+// Percentage of the SM's memory asked for as shared memory: no more than the kernels need,
+// since the activations are read through the rest (5% on 151936 x 4096 and 8 tokens).
+int carveout(uint32_t warps) { return warps == kManyWarps ? 80 : 60; }
+
 using LinearKernel = void (*)(LBatch);
-LinearKernel pick_kernel(uint32_t nb, int &instance) {
-  instance = nb == 1 ? 66 : (nb == 2 ? 67 : 68);
-  return nb == 1 ? df11_linear_kernel<1> : (nb == 2 ? df11_linear_kernel<2> : df11_linear_kernel<4>);
+LinearKernel pick_kernel(uint32_t nb, uint32_t warps, int &instance) {
+  instance = nb == 1 ? (warps == kManyWarps ? 66 : 67) : (nb == 2 ? 68 : 69);
+  if (nb == 1) return warps == kManyWarps ? df11_linear_kernel<1, kManyWarps> : df11_linear_kernel<1, kFewWarps>;
+  return nb == 2 ? df11_linear_kernel<2, kFewWarps> : df11_linear_kernel<4, kFewWarps>;
 }
 
 // What a group of at most DF11_MAX_BATCH weights needs from the workspace.
@@ -1097,22 +1108,25 @@ df11_status make_plan(const df11_linear_weight *ws, const df11_linear *ops, int 
     return DF11_OK;
   }
   pl.nb = max_batch <= 8 ? 1 : (max_batch <= 16 ? 2 : 4);
-  pl.smem = decode_smem(longest_stream(ws, count));
+  const uint32_t words = longest_stream(ws, count);
+  pl.warps = pl.nb > 1 ? kFewWarps : warps_for(words);
+  pl.smem = decode_smem(words, pl.warps);
   int instance = 0;
   uint64_t budget = 0;
-  const LinearKernel kern = pick_kernel(pl.nb, instance);
-  const df11_status st = prepare(kern, kThreads, pl.smem, instance, budget);
+  const LinearKernel kern = pick_kernel(pl.nb, pl.warps, instance);
+  const df11_status st = prepare(kern, 32 * pl.warps, pl.smem, instance, budget, carveout(pl.warps));
   if (st != DF11_OK) return st;
-  split_units(ws, count, budget, pl.ctas);
+  split_units(ws, count, pl.warps, budget, pl.ctas);
   for (int i = 0; i < count; ++i) {
     const LWeight l = device_weight(ws[i]);
-    const uint64_t units = ordered_units(l.rbs, l.upr), per_group = (uint64_t)l.upr * kWarps;
+    const uint64_t units = ordered_units(l.rbs, l.upr, pl.warps);
+    const uint64_t per_group = (uint64_t)l.upr * pl.warps;
     const uint64_t per = (units + pl.ctas[i] - 1) / pl.ctas[i];
     uint64_t slots = (per + per_group - 2) / per_group + 1;
     if (slots > units / per_group) slots = units / per_group;
     pl.slots[i] = (uint32_t)slots;
     pl.part[i] = off;
-    off += round_up(pl.ctas[i] * slots * kWarps * 16 * 8 * pl.nb * sizeof(float), 256);
+    off += round_up(pl.ctas[i] * slots * pl.warps * 16 * 8 * pl.nb * sizeof(float), 256);
   }
   pl.bytes = off;
   return DF11_OK;
@@ -1228,6 +1242,7 @@ df11_status launch_fused(const df11_linear_weight *ws, const df11_linear *ops, i
   lb.count = fb.count = count;
   lb.spin_limit = kSpinLimit;
   fb.nb = pl.nb;
+  fb.warps = pl.warps;
   uint32_t cta = 0, blocks = 0;
   for (int i = 0; i < count; ++i) {
     LTensor &l = lb.t[i];
@@ -1254,8 +1269,8 @@ df11_status launch_fused(const df11_linear_weight *ws, const df11_linear *ops, i
   }
   lb.cta_end = cta;
   int instance = 0;
-  const LinearKernel kern = pick_kernel(pl.nb, instance);
-  const df11_status st = launch_pdl(kern, dim3(cta), kThreads, pl.smem, s, lb);
+  const LinearKernel kern = pick_kernel(pl.nb, pl.warps, instance);
+  const df11_status st = launch_pdl(kern, dim3(cta), 32 * pl.warps, pl.smem, s, lb);
   if (st != DF11_OK) return st;
   return launch_pdl(df11_linear_finish_kernel, dim3(blocks), kFinishThreads, 0, s, fb);
 }
@@ -1264,11 +1279,15 @@ df11_status launch_fused(const df11_linear_weight *ws, const df11_linear *ops, i
 df11_status launch_unpack(const df11_linear_weight *ws, int count, uint16_t *const *out,
                           int32_t *d_err, cudaStream_t s) {
   UArgs ua{};
-  const size_t smem = decode_smem(longest_stream(ws, count));
+  const uint32_t words = longest_stream(ws, count), warps = warps_for(words);
+  const size_t smem = decode_smem(words, warps);
   uint64_t budget = 0, ctas[DF11_MAX_BATCH];
-  const df11_status st = prepare(df11_linear_unpack_kernel, kThreads, smem, 69, budget);
+  void (*kern)(UArgs) = warps == kManyWarps ? df11_linear_unpack_kernel<kManyWarps>
+                                            : df11_linear_unpack_kernel<kFewWarps>;
+  const df11_status st = prepare(kern, 32 * warps, smem, warps == kManyWarps ? 71 : 72, budget,
+                                 carveout(warps));
   if (st != DF11_OK) return st;
-  split_units(ws, count, budget, ctas);
+  split_units(ws, count, warps, budget, ctas);
   ua.err = d_err;
   ua.count = count;
   ua.spin_limit = kSpinLimit;
@@ -1277,7 +1296,7 @@ df11_status launch_unpack(const df11_linear_weight *ws, int count, uint16_t *con
     ua.out[i] = out[i];
     ua.cta_begin[i + 1] = ua.cta_begin[i] + (uint32_t)ctas[i];
   }
-  return launch_pdl(df11_linear_unpack_kernel, dim3(ua.cta_begin[count]), kThreads, smem, s, ua);
+  return launch_pdl(kern, dim3(ua.cta_begin[count]), 32 * warps, smem, s, ua);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -1382,27 +1401,15 @@ df11_status check_linear_devices(const df11_linear_weight *ws, const df11_linear
 
 // The decode table of a code: its lengths (at most kMaxLength) and right-aligned codewords.
 void make_table(const uint8_t len[256], const uint32_t code[256], LinearTable &t) {
-  // by the next kMaxLength bits: the first codeword's exponent and length (bits that no
-  // codeword begins with, as a code of one symbol has them: exponent 0, one bit)
-  uint32_t sym[1 << kMaxLength] = {}, length[1 << kMaxLength];
-  for (uint32_t &l : length) l = 1;
+  // bits that no codeword begins with (a code of one symbol has such): a length of one
+  for (uint32_t &e : t.entry) e = 1;
   for (uint32_t e = 0; e < 256; ++e) {
+    uint32_t c = 0;
+    for (uint32_t i = 0; i < len[e]; ++i) c |= (code[e] >> i & 1u) << (len[e] - 1 - i);
+    t.code[e] = (uint8_t)c;
     t.length[e] = len[e];
-    t.code[e] = 0;
-    for (uint32_t i = 0; i < len[e]; ++i) t.code[e] |= (code[e] >> i & 1u) << (len[e] - 1 - i);
-    if (!len[e]) continue;
-    for (uint32_t i = t.code[e]; i < 1u << kMaxLength; i += 1u << len[e]) {
-      sym[i] = e;
-      length[i] = len[e];
-    }
-  }
-  constexpr uint32_t kMask = (1u << kMaxLength) - 1u;
-  for (uint32_t i = 0; i < kPairs; ++i) {
-    const uint32_t a = i & kMask, b = (i >> length[a]) & kMask;
-    const uint32_t first = length[a] << 16 | sym[a] << 7;
-    t.pair[i] = length[a] + length[b] <= (uint32_t)kPairBits
-                    ? first | sym[b] << 23 | (length[a] + length[b])
-                    : first | kFirstOnly | length[a];
+    if (len[e])
+      for (uint32_t i = c; i < kEntries; i += 1u << len[e]) t.entry[i] = e << 7 | len[e];
   }
 }
 

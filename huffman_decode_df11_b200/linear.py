@@ -18,7 +18,7 @@ import torch
 from . import Df11Device, Df11Host, _check, _one_device, _stream_handle, decode, lib, to_device
 
 TILE_ROWS, TILE_COLS, UNIT_TILES = 16, 64, 4
-LINEAR_TABLE_BYTES = 4 * 4096 + 2048
+LINEAR_TABLE_BYTES = 4 * 256 + 256 + 256
 LINEAR_MAX_BATCH = 1 << 20
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}

@@ -264,7 +264,7 @@ df11_status df11_decode_gemm(const df11_tensor *tensors, const df11_gemv *ops, i
 #define DF11_LINEAR_MAX_BATCH (1u << 20)
 
 /* Bytes of a weight's decode table. */
-#define DF11_LINEAR_TABLE_BYTES (4 * 4096 + 2048)
+#define DF11_LINEAR_TABLE_BYTES (4 * 256 + 256 + 256)
 
 /* A weight (rows x cols) in the compressed form of the linear product, written
  * by df11_linear_weight_begin and _finish: as in the other tensors a canonical Huffman
@@ -285,10 +285,14 @@ typedef struct df11_linear_weight {
                                    by word, first bit = bit 0 */
   const uint32_t *unit_rows;    /* first row of each unit, and the total after them */
   const uint8_t *sign_mantissa; /* 16-byte aligned: per tile 16 bytes of each stream for rows
-                                   0 .. 7, then for rows 8 .. 15 */
+                                   0 .. 7, then for rows 8 .. 15; a word of four elements:
+                                   mantissas in bits 0-6, 16-22, 8-14 and 24-30, signs in
+                                   bits 15, 31, 23 and 7 */
   const void *table;            /* 16-byte aligned, DF11_LINEAR_TABLE_BYTES: the decode table
-                                   of 4096 words, then by exponent 256 codewords (first bit
-                                   = bit 0) and 256 lengths */
+                                   of 256 words, by the next 8 bits of a stream (exponent in
+                                   bits 7-14, codeword length in bits 0-3), then by
+                                   exponent 256 codewords (bytes, first bit = bit 0) and
+                                   256 lengths (bytes) */
   df11_linear_params params;
 } df11_linear_weight;
 

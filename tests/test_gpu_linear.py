@@ -296,9 +296,10 @@ def _lane_streams(w):
     rows, cols = -(-p.rows // 16) * 16, -(-p.cols // 64) * 64
     words = w.streams.cpu().numpy().view(np.uint32).reshape(-1, 32)
     first = w.unit_rows.cpu().numpy()
-    sm = w.sign_mantissa.cpu().numpy().reshape(rows // 16, cols // 64, 2, 32, 16)
+    sm = w.sign_mantissa.cpu().numpy().view(np.uint32).reshape(rows // 16, cols // 64, 2, 32, 4)
+    mantissa, sign = (0, 16, 8, 24), (15, 31, 23, 7)
     # the code, from its stored codewords and lengths
-    tail = w.table.cpu().numpy()[-2048:].view(np.uint32)
+    tail = w.table.cpu().numpy()[-512:]
     book = {f"{int(tail[e]):b}".zfill(int(tail[256 + e]))[::-1]: e
             for e in range(256) if tail[256 + e]}
     out = np.zeros((rows, cols), np.uint16)
@@ -318,9 +319,9 @@ def _lane_streams(w):
                             n += 1
                         e = book[bits[at:at + n]]
                         at += n
-                        b = int(sm[rb, cg, h, lane, j])
+                        four = int(sm[rb, cg, h, lane, j // 4])
                         out[16 * rb + 8 * h + lane // 4, 64 * cg + 16 * (lane % 4) + j] = \
-                            (b & 0x80) << 8 | e << 7 | b & 0x7F
+                            (four >> sign[j % 4] & 1) << 15 | e << 7 | four >> mantissa[j % 4] & 0x7F
             assert "1" not in bits[at:] and len(bits) - at >= 0
     return out
 
