@@ -729,8 +729,8 @@ __global__ void __launch_bounds__(1024) linear_rows_kernel(uint32_t *unit_rows, 
 // ---- more tokens: tcgen05 product of the decoded tiles ------------------------
 //
 // D[token][row] = sum_c x[token][c] W[row][c]: A is x (128 tokens, TMA from the
-// caller's rows), B the decoded tiles (BN rows; a 16 x 64 tile is 16 rows of 128
-// bytes, so a TMA box of BN/16 row blocks is BN rows of 64 columns), both in the
+// caller's rows), B the decoded tiles (bn rows; a 16 x 64 tile is 16 rows of 128
+// bytes, so a TMA box of bn/16 row blocks is bn rows of 64 columns), both in the
 // 128-byte swizzle, K in steps of 64.  One warp issues the copies, one the
 // products, four move finished accumulators (two, in turn) out through the
 // epilogue: a lane is a token, its columns consecutive rows of W.
@@ -740,19 +740,21 @@ constexpr int kGemmThreads = 6 * 32;  // warps 0-3: epilogue, 4: copies, 5: prod
 struct GemmArgs {
   Epilogue e;
   uint32_t tokens, rows, ncg;         // ncg: 64-column steps
+  uint32_t bn, stages, tmem_cols;     // rows of W per tile, stages of shared memory
   uint32_t tiles_m, tiles;            // token tiles, all tiles
   uint32_t vec;                       // rows of y, multiplier and residual take 16-byte accesses
   int32_t *err;
   uint32_t spin_limit;
 };
 
-template <int BN>
-struct GemmLayout {
-  static constexpr uint32_t a_bytes = kGemmTokens * 128, b_bytes = BN * 128;
-  static constexpr uint32_t stage_bytes = a_bytes + b_bytes;
-  static constexpr int stages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
-  static constexpr uint32_t smem = 1024 + stages * stage_bytes + 256;
-};
+constexpr uint32_t kXBytes = kGemmTokens * 128;
+constexpr uint32_t kMaxStages = 8;
+// barriers: full and empty per stage, two accumulators' full and empty; the tensor-memory
+// address
+constexpr uint32_t kGemmTail = 8 * (2 * kMaxStages + 4) + 16;
+constexpr uint32_t gemm_smem(uint32_t bn, uint32_t stages) {
+  return 1024 + stages * (kXBytes + bn * 128) + kGemmTail;
+}
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
                                             uint32_t bar) {
@@ -777,9 +779,20 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
          (2ull << 61);
 }
 
-// 16 consecutive rows of one token: loads of 16 bytes where aligned
-__device__ __forceinline__ void load16(const void *p, size_t i, bool f32, float (&v)[16]) {
-  if (f32) {
+// `n` (at most 16) consecutive rows of one token, all loads before their first use: 16 bytes
+// at a time where whole and aligned
+template <bool VEC>
+__device__ __forceinline__ void load16(const void *p, size_t i, bool f32, uint32_t n,
+                                       float (&v)[16]) {
+  if (!VEC) {
+#pragma unroll
+    for (uint32_t j = 0; j < 16; ++j) {
+      v[j] = 0.f;
+      if (j < n)
+        v[j] = f32 ? static_cast<const float *>(p)[i + j]
+                   : __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i + j] << 16);
+    }
+  } else if (f32) {
     const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -801,29 +814,35 @@ __device__ __forceinline__ void load16(const void *p, size_t i, bool f32, float 
   }
 }
 
+template <bool VEC>
 __device__ __forceinline__ void finish16(const Epilogue &e, float (&v)[16], uint32_t token,
-                                         uint32_t row) {
-  float t[16];
+                                         uint32_t row, uint32_t n) {
+  float m[16], r[16];
+  if (e.mul) load16<VEC>(e.mul, (size_t)token * e.mul_stride + row, e.flags & kMulF32, n, m);
+  if (e.res) load16<VEC>(e.res, (size_t)token * e.res_stride + row, e.flags & kResF32, n, r);
   if (e.bias) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] += load_any(e.bias, row + j, e.flags & kBiasF32);
+    for (uint32_t j = 0; j < 16; ++j)
+      if (VEC || j < n) v[j] += load_any(e.bias, row + j, e.flags & kBiasF32);
   }
   if (e.act != DF11_ACT_NONE) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = activate(v[j], e.act);
   }
   if (e.mul) {
-    load16(e.mul, (size_t)token * e.mul_stride + row, e.flags & kMulF32, t);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] *= t[j];
+    for (int j = 0; j < 16; ++j) v[j] *= m[j];
   }
   if (e.res) {
-    load16(e.res, (size_t)token * e.res_stride + row, e.flags & kResF32, t);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] += t[j];
+    for (int j = 0; j < 16; ++j) v[j] += r[j];
   }
   const size_t i = (size_t)token * e.y_stride + row;
-  if (e.flags & kOutF32) {
+  if (!VEC) {
+#pragma unroll
+    for (uint32_t j = 0; j < 16; ++j)
+      if (j < n) store_any(e, v[j], token, row + j);
+  } else if (e.flags & kOutF32) {
     float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(e.y) + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -837,29 +856,27 @@ __device__ __forceinline__ void finish16(const Epilogue &e, float (&v)[16], uint
   }
 }
 
-template <int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     df11_linear_gemm_kernel(const __grid_constant__ CUtensorMap map_x,
                             const __grid_constant__ CUtensorMap map_w,
                             const __grid_constant__ GemmArgs ga) {
-  using L = GemmLayout<BN>;
-  constexpr int S = L::stages;
+  const uint32_t S = ga.stages, bn = ga.bn, stage_bytes = kXBytes + bn * 128u;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-  const uint32_t bars = base + S * L::stage_bytes;
+  const uint32_t bars = base + S * stage_bytes;
   // full[S], empty[S], acc_full[2], acc_empty[2], the tensor-memory address
-  auto full = [&](int i) { return bars + 8u * i; };
-  auto empty = [&](int i) { return bars + 8u * (S + i); };
-  auto acc_full = [&](int i) { return bars + 8u * (2 * S + i); };
-  auto acc_empty = [&](int i) { return bars + 8u * (2 * S + 2 + i); };
-  const uint32_t taddr_s = bars + 8u * (2 * S + 4);
+  auto full = [&](uint32_t i) { return bars + 8u * i; };
+  auto empty = [&](uint32_t i) { return bars + 8u * (kMaxStages + i); };
+  auto acc_full = [&](uint32_t i) { return bars + 8u * (2 * kMaxStages + i); };
+  auto acc_empty = [&](uint32_t i) { return bars + 8u * (2 * kMaxStages + 2 + i); };
+  const uint32_t taddr_s = bars + 8u * (2 * kMaxStages + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
+    for (uint32_t i = 0; i < S; ++i) {
       mbar_init(full(i), 1);
       mbar_init(empty(i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (uint32_t i = 0; i < 2; ++i) {
       mbar_init(acc_full(i), 1);
       mbar_init(acc_empty(i), 4);
     }
@@ -867,7 +884,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   if (warp == 5) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(taddr_s),
-                 "r"(2u * BN)
+                 "r"(ga.tmem_cols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -880,20 +897,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   if (warp == 4) {
     if (lane == 0) {
-      uint32_t k = 0;
+      uint32_t k = 0, s = 0, par = 0;  // copies so far; the stage, and its uses' parity
       for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
         const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m;
         for (uint32_t c = 0; c < ga.ncg; ++c, ++k) {
-          const uint32_t s = k % S, par = (k / S) & 1u;
           if (!mbar_wait(empty(s), par ^ 1u, ga.spin_limit)) {
             failed = true;
             break;
           }
-          mbar_arrive_expect_tx(full(s), L::stage_bytes);
-          tma_load_2d(base + s * L::stage_bytes, &map_x, (int)(64u * c), (int)(tm * kGemmTokens),
+          mbar_arrive_expect_tx(full(s), stage_bytes);
+          tma_load_2d(base + s * stage_bytes, &map_x, (int)(64u * c), (int)(tm * kGemmTokens),
                       full(s));
-          tma_load_4d(base + s * L::stage_bytes + L::a_bytes, &map_w, 0, 0, (int)c,
-                      (int)(tn * (BN / 16)), full(s));
+          tma_load_4d(base + s * stage_bytes + kXBytes, &map_w, 0, 0, (int)c,
+                      (int)(tn * (bn / 16)), full(s));
+          if (++s == S) {
+            s = 0;
+            par ^= 1u;
+          }
         }
       }
       pdl_launch_dependents();
@@ -904,9 +924,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   } else if (warp == 5) {
     // fp32 accumulators, BF16 operands, both K-major
-    constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((BN / 8) << 17) |
-                               ((kGemmTokens / 16) << 24);
-    uint32_t k = 0, n = 0;
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((bn / 8) << 17) |
+                           ((kGemmTokens / 16) << 24);
+    uint32_t k = 0, n = 0, s = 0, par = 0;
     for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x, ++n) {
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_empty(n & 1), ((n >> 1) & 1u) ^ 1u,
                                               ga.spin_limit))) {
@@ -914,17 +934,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t d = tmem + (n & 1u) * BN;
+      const uint32_t d = tmem + (n & 1u) * bn;
       for (uint32_t c = 0; c < ga.ncg; ++c, ++k) {
-        const uint32_t s = k % S;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(full(s), (k / S) & 1u, ga.spin_limit))) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(full(s), par, ga.spin_limit))) {
           failed = true;
           break;
         }
         tc_fence_after();
         if (lane == 0) {
-          const uint64_t ad = sw128_desc(base + s * L::stage_bytes);
-          const uint64_t bd = sw128_desc(base + s * L::stage_bytes + L::a_bytes);
+          const uint64_t ad = sw128_desc(base + s * stage_bytes);
+          const uint64_t bd = sw128_desc(base + s * stage_bytes + kXBytes);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {  // K = 16: 32 bytes on
             const uint32_t add = c || j ? 1u : 0u;
@@ -945,6 +964,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 : "memory");
         }
         __syncwarp();
+        if (++s == S) {
+          s = 0;
+          par ^= 1u;
+        }
       }
     }
     // no product in flight when the tensor memory goes
@@ -961,9 +984,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       tc_fence_after();
       const uint32_t token = tm * kGemmTokens + 32u * warp + lane;
-      const uint32_t src = tmem + ((32u * warp) << 16) + (n & 1u) * BN;
-      for (uint32_t c = 0; c < BN; c += 16) {
-        const uint32_t row = tn * BN + c;
+      const uint32_t src = tmem + ((32u * warp) << 16) + (n & 1u) * bn;
+      for (uint32_t c = 0; c < bn; c += 16) {
+        const uint32_t row = tn * bn + c;
         if (row >= ga.rows) break;
         uint32_t u[16];
         asm volatile(
@@ -981,16 +1004,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (token >= ga.tokens) {
           // a row of the tile past the last token
         } else if (ga.vec && row + 16 <= ga.rows) {
-          finish16(ga.e, v, token, row);
+          finish16<true>(ga.e, v, token, row, 16u);
         } else {
-#pragma unroll 1
-          for (int j = 0; j < 16; ++j)
-            if (row + j < ga.rows) {
-              float o = v[0];
-#pragma unroll
-              for (int l = 1; l < 16; ++l) o = l == j ? v[l] : o;
-              store_any(ga.e, finish(ga.e, o, token, row + j), token, row + j);
-            }
+          finish16<false>(ga.e, v, token, row, min(ga.rows - row, 16u));
         }
         __syncwarp();
       }
@@ -1005,7 +1021,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __syncthreads();
   if (warp == 5) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2u * BN)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(ga.tmem_cols)
                  : "memory");
   }
 }
@@ -1317,18 +1333,6 @@ EncodeTiled encode_tiled() {
   return f;
 }
 
-template <int BN>
-df11_status launch_gemm_bn(const CUtensorMap &mx, CUtensorMap mw, GemmArgs ga, int sms,
-                           int instance, cudaStream_t s) {
-  auto kern = df11_linear_gemm_kernel<BN>;
-  uint64_t budget = 0;
-  const df11_status st = prepare(kern, kGemmThreads, GemmLayout<BN>::smem, instance, budget);
-  if (st != DF11_OK) return st;
-  ga.tiles = ga.tiles_m * ((ga.rows + BN - 1) / BN);
-  const uint32_t grid = ga.tiles < (uint32_t)sms ? ga.tiles : (uint32_t)sms;
-  return launch_pdl(kern, dim3(grid), kGemmThreads, GemmLayout<BN>::smem, s, mx, mw, ga);
-}
-
 df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, const uint16_t *w,
                         const Activations &x, int32_t *d_err, cudaStream_t s) {
   const EncodeTiled encode = encode_tiled();
@@ -1350,18 +1354,23 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
   ga.vec = vec_ok(op.y, op.y_stride, op.y_type) &&
            vec_ok(op.multiplier, op.multiplier_stride, op.multiplier_type) &&
            vec_ok(op.residual, op.residual_stride, op.residual_type);
-  // the widest tile whose rounds over the SMs cost least (a round costs about
-  // its tile's rows; narrow tiles read x more often)
-  uint32_t best = 64;
+  // the tile width whose rounds over the SMs cost least: a round costs about its tile's rows,
+  // and what 32 more would for reading x and emptying the accumulator; the wider one of two
+  // (4096 rows and 2048 tokens on 148 SMs: 240 rows, 288 tiles in two rounds)
   uint64_t cost = ~0ull;
-  for (uint32_t bn : {256u, 128u, 64u}) {
+  for (uint32_t bn = 256; bn >= 16; bn -= 16) {
     const uint64_t tiles = (uint64_t)ga.tiles_m * ((rows + bn - 1) / bn);
     const uint64_t c = (tiles + sms - 1) / sms * (bn + 32);
     if (c < cost) {
       cost = c;
-      best = bn;
+      ga.bn = bn;
+      ga.tiles = (uint32_t)tiles;
     }
   }
+  ga.stages = kMaxStages;
+  while (gemm_smem(ga.bn, ga.stages) > 200 * 1024) --ga.stages;
+  ga.tmem_cols = 32;
+  while (ga.tmem_cols < 2 * ga.bn) ga.tmem_cols *= 2;
   CUtensorMap mx, mw;
   {
     const cuuint64_t dims[2] = {x.cols, op.batch}, strides[1] = {2ull * x.stride};
@@ -1375,16 +1384,19 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
   {
     const cuuint64_t dims[4] = {64, 16, ga.ncg, (rows + 15u) / 16u};
     const cuuint64_t strides[3] = {128, 2048, 2048ull * ga.ncg};
-    const cuuint32_t box[4] = {64, 16, 1, best / 16}, one[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, 16, 1, ga.bn / 16}, one[4] = {1, 1, 1, 1};
     if (encode(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(w), dims, strides,
                box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
         CUDA_SUCCESS)
       return DF11_ERR_CUDA;
   }
-  if (best == 256) return launch_gemm_bn<256>(mx, mw, ga, sms, 75, s);
-  if (best == 128) return launch_gemm_bn<128>(mx, mw, ga, sms, 76, s);
-  return launch_gemm_bn<64>(mx, mw, ga, sms, 77, s);
+  const size_t smem = gemm_smem(ga.bn, ga.stages);
+  uint64_t budget = 0;
+  const df11_status st = prepare(df11_linear_gemm_kernel, kGemmThreads, smem, 75, budget);
+  if (st != DF11_OK) return st;
+  const uint32_t grid = ga.tiles < (uint32_t)sms ? ga.tiles : (uint32_t)sms;
+  return launch_pdl(df11_linear_gemm_kernel, dim3(grid), kGemmThreads, smem, s, mx, mw, ga);
 }
 
 df11_status check_linear_devices(const df11_linear_weight *ws, const df11_linear *ops, int count,
