@@ -324,8 +324,9 @@ __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, ui
     words = fetch(__ldg(rows), __ldg(rows + 1), 0, bytes_of(rb, ku * kUnitTiles),
                   min(kUnitTiles, lw.ncg - ku * kUnitTiles));
   }
-  for (uint32_t e = warp; e < kEntries; e += W)  // every lane's copy of the table
-    sts32(table + 256u * e, __ldg(lw.table->entry + e));
+#pragma unroll
+  for (uint32_t e = 0; e < kEntries; e += W)  // every lane's copy of the table
+    sts32(table + 256u * (e + warp), __ldg(lw.table->entry + e + warp));
   __syncthreads();
   bool running = true;
   start();
@@ -530,23 +531,30 @@ __global__ void __launch_bounds__(kFinishThreads)
   const uint32_t i = (blockIdx.x - ft.block_begin) * kFinishThreads + threadIdx.x;
   const uint32_t r = i & 15u, rb = (i >> 4) / ft.batch;
   const uint32_t token = (i >> 4) - rb * ft.batch, row = 16u * rb + r;
-  pdl_wait();
-  pdl_launch_dependents();
-  if (rb >= ft.rbs || row >= ft.rows) return;
+  const bool here = rb < ft.rbs && row < ft.rows;
   // the thread blocks that hold units of the row block's group
   const uint64_t units = ordered_units(ft.rbs, ft.upr, fb.warps), per_group = (uint64_t)ft.upr * fb.warps;
   const uint64_t group = rb / fb.warps;
   auto holder = [&](uint64_t o) { return (uint32_t)(((o + 1) * ft.ctas - 1) / units); };
   const uint32_t c0 = holder(group * per_group), c1 = holder((group + 1) * per_group - 1);
   const uint32_t per_warp = 16u * 8u * fb.nb;
-  const float *p = ft.part + (size_t)(rb % fb.warps) * per_warp + token * 16u + r;
-  float sum = 0.f;
   // slot of the group in a thread block's part: 0 but for those that begin before it
-  sum = __ldcg(p + ((size_t)c0 * ft.slots + (group - first_unit(c0, units, ft.ctas) / per_group)) *
-                       fb.warps * per_warp);
-#pragma unroll 4
-  for (uint32_t c = c0 + 1; c <= c1; ++c)
-    sum += __ldcg(p + (size_t)c * ft.slots * fb.warps * per_warp);
+  const uint64_t slot = group - first_unit(c0, units, ft.ctas) / per_group;
+  const float *p = ft.part + (size_t)(rb % fb.warps) * per_warp + token * 16u + r;
+  const size_t stride = (size_t)ft.slots * fb.warps * per_warp;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!here) return;
+  float sum = __ldcg(p + c0 * stride + slot * fb.warps * per_warp);
+  constexpr uint32_t kAhead = 8;  // loads before the first addition
+  for (uint32_t c = c0 + 1; c <= c1; c += kAhead) {
+    float v[kAhead];
+#pragma unroll
+    for (uint32_t j = 0; j < kAhead; ++j) v[j] = c + j <= c1 ? __ldcg(p + (c + j) * stride) : 0.f;
+#pragma unroll
+    for (uint32_t j = 0; j < kAhead; ++j)
+      if (c + j <= c1) sum += v[j];
+  }
   store_any(ft.e, finish(ft.e, sum, token, row), token, row);
 }
 
