@@ -74,23 +74,53 @@ __device__ __forceinline__ void embed_store(const EmbedArgs &a, size_t i, uint32
       (uint16_t)(a.scaled ? bf16_bits(scaled_value(a, bits)) : bits);
 }
 
-// the last format block whose first element is at or before element e
-__device__ uint32_t find_block(const KTensor &k, uint32_t e, int lane) {
+// the last format block whose first element is at or before element e, and that element
+__device__ __forceinline__ uint32_t find_block(const KTensor &k, uint32_t e, int lane, uint32_t &at) {
   const uint32_t guess = (uint32_t)((uint64_t)e * k.num_blocks / k.n);
   const uint32_t lo = guess > 15u ? guess - 15u : 0u;
   const uint32_t i = lo + (uint32_t)lane;
-  const bool at = i < k.num_blocks && __ldg(k.block_out_pos + i) <= e;
-  const uint32_t m = __ballot_sync(0xFFFFFFFFu, at);
+  const uint32_t v = i < k.num_blocks ? __ldg(k.block_out_pos + i) : 0xFFFFFFFFu;
+  const uint32_t m = __ballot_sync(0xFFFFFFFFu, i < k.num_blocks && v <= e);
   const bool below = m == 0, above = m == 0xFFFFFFFFu && lo + 32u < k.num_blocks;
-  if (!below && !above) return lo + 31u - (uint32_t)__clz(m);
+  if (!below && !above) {
+    const int last = 31 - __clz(m);
+    at = __shfl_sync(0xFFFFFFFFu, v, last);
+    return lo + (uint32_t)last;
+  }
   uint32_t first = below ? 0u : lo + 31u, last = below ? lo + 1u : k.num_blocks;
   while (last - first > 1u) {
     const uint32_t mid = first + ((last - first) >> 1);
     if (__ldg(k.block_out_pos + mid) <= e) first = mid;
     else last = mid;
   }
+  at = __ldg(k.block_out_pos + first);
   return first;
 }
+
+// What a lane needs of its chunk: the codewords that start in it, its words and the next one
+// (as they are in memory), and the gap fields of it and the next one from bit 31 down.
+template <int C>
+struct Chunk {
+  uint32_t cnt, gaps, w[C / 4 + 1];
+  __device__ __forceinline__ void load(const KTensor &k, uint64_t chunk) {
+    constexpr int NW = C / 4 + 1;
+    cnt = gaps = 0;
+    if (chunk >= (uint64_t)k.num_blocks * kT) return;
+    cnt = __ldg(k.chunk_counts + chunk);
+    const uint2 *q = reinterpret_cast<const uint2 *>(k.bitstream + chunk * C);
+#pragma unroll
+    for (int j = 0; j < NW / 2; ++j) {
+      const uint2 v = __ldg(q + j);
+      w[2 * j] = v.x;
+      w[2 * j + 1] = v.y;
+    }
+    w[NW - 1] = __ldg(reinterpret_cast<const uint32_t *>(q + NW / 2));
+    const uint64_t bit = 5ull * chunk;
+    const uint32_t *g = reinterpret_cast<const uint32_t *>(k.gaps) + (bit >> 5);
+    gaps = __funnelshift_l(__byte_perm(__ldg(g + 1), 0, 0x0123), __byte_perm(__ldg(g), 0, 0x0123),
+                           (uint32_t)bit);
+  }
+};
 
 template <int C>
 __global__ void __launch_bounds__(kWarps * 32)
@@ -118,7 +148,6 @@ __global__ void __launch_bounds__(kWarps * 32)
   pdl_launch_dependents();
   bool table = false;
   const uint64_t items = (uint64_t)a.tokens * a.segs;
-  const uint64_t chunks = (uint64_t)tk.num_blocks * kT;
   for (uint64_t item = blockIdx.x + (uint64_t)gridDim.x * warp; item < items;
        item += (uint64_t)gridDim.x * kWarps) {
     const uint32_t token = (uint32_t)(item / a.segs), seg = (uint32_t)(item - (uint64_t)token * a.segs);
@@ -136,8 +165,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     const uint32_t row0 = (uint32_t)id * a.dim;  // elements of a tensor: below 2^32
     const uint32_t e0 = row0 + c_first, e1 = row0 + c_last;
-    const uint32_t b = find_block(tk, e0, lane);
-    uint32_t P = __ldg(tk.block_out_pos + b), chunk0;
+    uint32_t P, chunk0;
+    const uint32_t b = find_block(tk, e0, lane, P);
     if (P > e0) {  // inconsistent positions
       if (lane == 0) report(a.err, DF11_DEV_ERR_COUNT);
       continue;
@@ -168,10 +197,12 @@ __global__ void __launch_bounds__(kWarps * 32)
       P += __shfl_sync(0xFFFFFFFFu, before, src);
       chunk0 = b * kT + 8u * src + __shfl_sync(0xFFFFFFFFu, j, src);
     }
+    Chunk<C> next;
+    next.load(tk, (uint64_t)chunk0 + lane);
     for (uint64_t c0 = chunk0; P < e1; c0 += 32) {
       const uint64_t chunk = c0 + lane;
-      const bool here = chunk < chunks;
-      const uint32_t cnt = here ? __ldg(tk.chunk_counts + chunk) : 0u;
+      Chunk<C> ck = next;
+      const uint32_t cnt = ck.cnt;
       uint32_t incl = cnt;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -183,25 +214,23 @@ __global__ void __launch_bounds__(kWarps * 32)
         if (lane == 0) report(a.err, DF11_DEV_ERR_COUNT);
         break;
       }
+      // the next 32 chunks, and the first sign/mantissa bytes, arrive during the walk
+      if (P + total < e1) next.load(tk, chunk + 32);
       const uint32_t E = P + incl - cnt, base = P & ~15u;
       const bool need = cnt && E < e1 && E + cnt > e0;
+      // elements [lo, hi) past `base` are the row's, element i at byte i of the region
+      const uint32_t lo = max(e0, P) - base, hi = min(e1 - base, P - base + total);
+      const uint8_t *sm = tk.sign_mantissa + base;
+      uint4 sv = make_uint4(0, 0, 0, 0);
+      if (a.vec && (lo & ~15u) + 16u * lane < hi)
+        sv = __ldg(reinterpret_cast<const uint4 *>(sm + (lo & ~15u)) + lane);
       int start = 0, end = 0, bad = 0;
       uint32_t w[NW];
       if (need) {
-        const uint2 *q = reinterpret_cast<const uint2 *>(tk.bitstream + chunk * C);
 #pragma unroll
-        for (int j = 0; j < NW / 2; ++j) {
-          const uint2 v = __ldg(q + j);
-          w[2 * j] = __byte_perm(v.x, 0, 0x0123);
-          w[2 * j + 1] = __byte_perm(v.y, 0, 0x0123);
-        }
-        w[NW - 1] = __byte_perm(__ldg(reinterpret_cast<const uint32_t *>(q + NW / 2)), 0, 0x0123);
-        const uint64_t gbit = 5ull * chunk;
-        const uint32_t *gp = reinterpret_cast<const uint32_t *>(tk.gaps) + (gbit >> 5);
-        const uint32_t v = __funnelshift_l(__byte_perm(__ldg(gp + 1), 0, 0x0123),
-                                           __byte_perm(__ldg(gp), 0, 0x0123), (uint32_t)gbit);
-        start = (int)(v >> 27);
-        end = C * 8 + (int)((v >> 22) & 31u);
+        for (int j = 0; j < NW; ++j) w[j] = __byte_perm(ck.w[j], 0, 0x0123);
+        start = (int)(ck.gaps >> 27);
+        end = C * 8 + (int)((ck.gaps >> 22) & 31u);
         const uint64_t bit0 = chunk * (C * 8);
         if (bit0 >= tk.total_bits) start = end = 0;
         else if ((uint64_t)end > tk.total_bits - bit0) end = (int)(tk.total_bits - bit0);
@@ -233,16 +262,14 @@ __global__ void __launch_bounds__(kWarps * 32)
         if (bad) report(a.err, bad);
       }
       __syncwarp();
-      // elements [lo, hi) past `base` are the row's, element i at byte i of the region
-      const uint32_t lo = max(e0, P) - base, hi = min(e1 - base, P - base + total);
-      const uint8_t *sm = tk.sign_mantissa + base;
       const size_t out_base = out0 + base - row0;  // may wrap below the row: base is before it
       if (a.vec) {
         for (uint32_t i = (lo & ~15u) + 16u * lane; i < hi; i += 512u) {
           const uint4 rv = lds128(region + i);
-          const uint4 sv = __ldg(reinterpret_cast<const uint4 *>(sm + i));
-          const uint2 p0 = fuse4(sv.x, rv.x), p1 = fuse4(sv.y, rv.y);
-          const uint2 p2 = fuse4(sv.z, rv.z), p3 = fuse4(sv.w, rv.w);
+          const uint4 cur = sv;  // the next group's bytes ahead
+          if (i + 512u < hi) sv = __ldg(reinterpret_cast<const uint4 *>(sm + i + 512u));
+          const uint2 p0 = fuse4(cur.x, rv.x), p1 = fuse4(cur.y, rv.y);
+          const uint2 p2 = fuse4(cur.z, rv.z), p3 = fuse4(cur.w, rv.w);
           const uint32_t u[8] = {p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
           const size_t o = out_base + i;
           if (i >= lo && i + 16u <= hi) {
@@ -271,8 +298,16 @@ __global__ void __launch_bounds__(kWarps * 32)
           }
         }
       } else {
-        for (uint32_t i = lo + lane; i < hi; i += 32)
-          embed_store(a, out_base + i, fuse1(__ldg(sm + i), lds8(region + i)));
+        constexpr uint32_t kAhead = 8;  // loads before the first store
+        for (uint32_t i = lo + lane; i < hi; i += 32 * kAhead) {
+          uint32_t v[kAhead];
+#pragma unroll
+          for (uint32_t j = 0; j < kAhead; ++j) v[j] = i + 32 * j < hi ? __ldg(sm + i + 32 * j) : 0u;
+#pragma unroll
+          for (uint32_t j = 0; j < kAhead; ++j)
+            if (i + 32 * j < hi)
+              embed_store(a, out_base + i + 32 * j, fuse1(v[j], lds8(region + i + 32 * j)));
+        }
       }
       __syncwarp();
       // the region zero again (a walk over corrupt data may write 7 bytes more)
@@ -327,7 +362,7 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
 // warp keeps a contiguous part of the list, so equal ids stay in token order.
 // An id outside the table sorts behind every row.
 __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs a) {
-  __shared__ uint32_t whist[kSortWarps][kMaxDigits];
+  __shared__ uint32_t whist[kSortWarps][kMaxDigits + 1];  // a column in 32 banks
   __shared__ uint32_t own[kMaxDigits], base[kMaxDigits], warp_total[kMaxDigits / 32];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
@@ -361,14 +396,18 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
       __syncwarp();
     }
     __syncthreads();
-    if (tid < digits) {  // counts of the warps before, and this thread block's
-      uint32_t sum = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t v = whist[w][tid];
-        whist[w][tid] = sum;
-        sum += v;
+    // per digit, the counts of the warps before and this thread block's: a warp per digit, a
+    // lane per warp
+    for (uint32_t d = warp; d < digits; d += kSortWarps) {
+      const uint32_t v = whist[lane][d];
+      uint32_t incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= (uint32_t)o) incl += u;
       }
-      own[tid] = sum;
+      whist[lane][d] = incl - v;
+      if (lane == 31) own[d] = incl;
     }
     cluster_sync();
     if (tid < kMaxDigits) {  // where each digit's tokens of this thread block begin
@@ -428,7 +467,7 @@ struct RunArgs {
   const uint32_t *touched;    // NULL: rows without tokens keep their values
   float *head, *tail;         // per piece: sums of the run that began before it / that goes on
   uint64_t grad_stride, out_stride;
-  uint32_t tokens, rows, dim, piece, pieces, col_tiles, part_stride;
+  uint32_t tokens, rows, dim, piece, pieces, col_tiles, join_tiles, part_stride;
   uint32_t accumulate;
   float scale;
 };
@@ -583,22 +622,35 @@ __global__ void __launch_bounds__(kRunThreads) embedding_runs_kernel(const __gri
 // the heads of the pieces after it, in order.
 template <typename O, int V>
 __global__ void __launch_bounds__(kRunThreads) embedding_join_kernel(const __grid_constant__ RunArgs a) {
+  __shared__ uint32_t stop_s[kRunThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
-  const uint32_t piece = blockIdx.x / a.col_tiles, ct = blockIdx.x - piece * a.col_tiles;
+  const uint32_t piece = blockIdx.x / a.join_tiles, ct = blockIdx.x - piece * a.join_tiles;
   const uint32_t i0 = piece * a.piece, i1 = i0 + a.piece;
   if (i1 >= a.tokens) return;
   const uint32_t key = __ldcg(a.key + i1 - 1);
   if (key >= a.rows || __ldcg(a.key + i1) != key) return;
   // begun before this piece: another thread block's
   if (i0 && __ldcg(a.key + i0 - 1) == key) return;
-  uint32_t lo = i1, hi = a.tokens;  // the run's end: the first larger key
-  while (lo < hi) {
-    const uint32_t mid = lo + ((hi - lo) >> 1);
-    if (__ldcg(a.key + mid) == key) lo = mid + 1;
-    else hi = mid;
+  // the run's last piece: the first one after this that does not end in the run's key, or
+  // whose next token has another; a piece per thread, until some thread has it
+  uint32_t last = piece + 1;
+  for (;; last += kRunThreads) {
+    const uint32_t p = last + threadIdx.x;
+    const uint64_t e = ((uint64_t)p + 1) * a.piece;  // the token after the piece
+    const bool goes_on = e < a.tokens && __ldcg(a.key + e) == key;
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, !goes_on);
+    if ((threadIdx.x & 31u) == 0) stop_s[threadIdx.x >> 5] = m ? (threadIdx.x & ~31u) + __ffs(m) - 1 : kRunThreads;
+    __syncthreads();
+    uint32_t first = kRunThreads;
+#pragma unroll
+    for (int w = 0; w < kRunThreads / 32; ++w) first = min(first, stop_s[w]);
+    __syncthreads();
+    if (first < kRunThreads) {
+      last += first;
+      break;
+    }
   }
-  const uint32_t last = (lo - 1) / a.piece;
   const uint32_t col = (ct * kRunThreads + threadIdx.x) * V;
   if (col >= a.dim) return;
   float s[V];
@@ -614,7 +666,7 @@ __global__ void __launch_bounds__(kRunThreads) embedding_join_kernel(const __gri
     }
   };
   load(a.tail + (size_t)piece * a.part_stride + col, s);
-  constexpr uint32_t kAhead = 4;
+  constexpr uint32_t kAhead = 8;
   for (uint32_t p = piece + 1; p <= last; p += kAhead) {
     float v[kAhead][V];
 #pragma unroll
@@ -642,8 +694,24 @@ df11_status launch_embedding(EmbedArgs &a, size_t smem, int instance, cudaStream
   uint64_t budget = 0;
   const df11_status st = prepare(kern, kWarps * 32, smem, instance, budget);
   if (st != DF11_OK) return st;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DF11_ERR_CUDA;
+  const uint64_t sms = device_info(dev).sms;
+  // A row in segments that 32 chunks hold on average (30, since a row begins and ends inside
+  // a chunk), while there are fewer rows than warps; more of a row per warp otherwise, which
+  // then finds its place in the stream once.
+  const uint64_t per_pass = 30ull * a.k.n / ((uint64_t)a.k.num_blocks * kT) + 1;
+  const uint64_t most = (a.dim + per_pass - 1) / per_pass;
+  uint64_t segs = budget * kWarps / a.tokens;
+  segs = segs < 1 ? 1 : (segs > most ? most : segs);
+  a.seg_len = (uint32_t)round_up((a.dim + segs - 1) / segs, 16);
+  a.segs = (a.dim + a.seg_len - 1) / a.seg_len;
+  // every SM, then every warp of a thread block, then more thread blocks per SM
   const uint64_t items = (uint64_t)a.tokens * a.segs;
-  return launch_pdl(kern, dim3((uint32_t)(items < budget ? items : budget)), kWarps * 32, smem, s, a);
+  uint64_t grid = (items + kWarps - 1) / kWarps;
+  if (grid < sms) grid = items < sms ? items : sms;
+  if (grid > budget) grid = budget;
+  return launch_pdl(kern, dim3((uint32_t)grid), kWarps * 32, smem, s, a);
 }
 
 struct GradPlan {
@@ -715,7 +783,9 @@ df11_status launch_runs(const RunArgs &a, uint32_t zero_blocks, cudaStream_t s) 
   df11_status st = launch_pdl(embedding_runs_kernel<G, O, V>, dim3(runs + zero_blocks), kRunThreads,
                               0, s, a);
   if (st != DF11_OK || a.pieces < 2) return st;
-  return launch_pdl(embedding_join_kernel<O, V>, dim3(runs), kRunThreads, 0, s, a);
+  // four columns per thread at most: more threads on the few rows that many tokens share
+  return launch_pdl(embedding_join_kernel<O, V == 1 ? 1 : 4>, dim3(a.pieces * a.join_tiles),
+                    kRunThreads, 0, s, a);
 }
 
 template <typename O>
@@ -773,12 +843,6 @@ df11_status df11_decode_embedding(const df11_tensor *table, const df11_embedding
   a.vec = op->dim % 16 == 0 && aligned(op->out, 16) &&
           op->out_stride * type_bytes(op->out_type) % 16 == 0;
   a.spin_limit = kSpinLimit;
-  // segments of a row that 32 chunks hold on average (30, since a row begins
-  // and ends inside a chunk), in whole 16-element groups
-  const uint64_t per_pass = 30 * p.n / ((uint64_t)p.num_blocks * kT) + 1;
-  const uint64_t segs = (op->dim + per_pass - 1) / per_pass;
-  a.seg_len = (uint32_t)round_up((op->dim + segs - 1) / segs, 16);
-  a.segs = (op->dim + a.seg_len - 1) / a.seg_len;
   // 32 chunks from any chunk on: first element's offset, elements, the walk's slack
   a.region_bytes = (uint32_t)round_up(15 + 32ull * p.max_chunk_elems + 8, 16);
   const size_t smem = kOffStages + (size_t)kWarps * a.region_bytes;
@@ -824,9 +888,9 @@ df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspa
   so.digit_bits = p.digit_bits;
   so.touched_words = p.words;
   so.ids64 = op->ids_type == DF11_IDS_I64;
-  // one thread block per 4096 tokens, up to a cluster of eight
+  // one thread block per 1024 tokens (32 per warp), up to a cluster of eight
   uint32_t ctas = 1;
-  while (ctas < 8 && (uint64_t)ctas * 4096 < op->tokens) ctas *= 2;
+  while (ctas < 8 && (uint64_t)ctas * kSortThreads < op->tokens) ctas *= 2;
   st = launch_cluster(embedding_sort_kernel, ctas, kSortThreads, s, so);
   if (st != DF11_OK) return st;
   RunArgs r{};
@@ -845,6 +909,7 @@ df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspa
   r.piece = p.piece;
   r.pieces = p.pieces;
   r.col_tiles = p.col_tiles;
+  r.join_tiles = (op->dim + kRunThreads * (p.v > 1 ? 4 : 1) - 1) / (kRunThreads * (p.v > 1 ? 4 : 1));
   r.part_stride = p.part_stride;
   r.accumulate = op->accumulate ? 1 : 0;
   r.scale = op->scale;

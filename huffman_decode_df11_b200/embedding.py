@@ -168,27 +168,34 @@ def embedding_gradient(ids: torch.Tensor, grad: torch.Tensor, rows: int,
         raise ValueError("rows must be positive and below 2^31")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    with torch.cuda.device(grad.device), torch.cuda.stream(_on_stream(stream)):
-        if out is None:
-            if out_dtype not in _TYPES:
-                raise TypeError(f"out_dtype: expected float32 or bfloat16, got {out_dtype}")
-            out = torch.empty(rows, dim, dtype=out_dtype, device=grad.device)
-        if out.dtype not in _TYPES:
-            raise TypeError(f"out: expected float32 or bfloat16, got {out.dtype}")
-        if tuple(out.shape) != (rows, dim) or out.device != grad.device:
-            raise ValueError(f"out: expected {rows} x {dim} on {grad.device}, got "
-                             f"{tuple(out.shape)} on {out.device}")
-        op = EmbeddingGradOp(ids.data_ptr(), grad.data_ptr(), out.data_ptr(),
-                             _row_stride("grad", grad, tokens, dim),
-                             _row_stride("out", out, rows, dim), rows, dim, tokens,
-                             _IDS[ids.dtype], _TYPES[grad.dtype], _TYPES[out.dtype],
-                             1 if accumulate else 0, _check_scale(scale))
-        L, size = lib(), ctypes.c_size_t(0)
-        _check(L.df11_embedding_gradient_workspace(ctypes.byref(op), ctypes.byref(size)),
-               "df11_embedding_gradient_workspace")
-        # the workspace is allocated and freed in the order of the call's stream
-        work = _aligned_empty(size.value, grad.device)
-        _check(L.df11_embedding_gradient(ctypes.byref(op), work.data_ptr(), size.value,
-                                         err.data_ptr() if err is not None else None,
-                                         _stream_handle(stream)), "df11_embedding_gradient")
+    if stream is not None or torch.cuda.current_device() != grad.device.index:
+        # the output and the workspace are allocated (and freed) in the order of the call's stream
+        with torch.cuda.device(grad.device), torch.cuda.stream(_on_stream(stream)):
+            return _embedding_gradient(ids, grad, rows, out, scale, accumulate, out_dtype, err)
+    return _embedding_gradient(ids, grad, rows, out, scale, accumulate, out_dtype, err)
+
+
+def _embedding_gradient(ids, grad, rows, out, scale, accumulate, out_dtype, err):
+    tokens, dim, dev = ids.numel(), grad.shape[-1], grad.device
+    if out is None:
+        if out_dtype not in _TYPES:
+            raise TypeError(f"out_dtype: expected float32 or bfloat16, got {out_dtype}")
+        out = torch.empty((rows, dim), dtype=out_dtype, device=dev)
+    elif out.dtype not in _TYPES:
+        raise TypeError(f"out: expected float32 or bfloat16, got {out.dtype}")
+    elif out.shape != (rows, dim) or out.device != dev:
+        raise ValueError(f"out: expected {rows} x {dim} on {dev}, got {tuple(out.shape)} on "
+                         f"{out.device}")
+    op = EmbeddingGradOp(ids.data_ptr(), grad.data_ptr(), out.data_ptr(),
+                         _row_stride("grad", grad, tokens, dim), _row_stride("out", out, rows, dim),
+                         rows, dim, tokens, _IDS[ids.dtype], _TYPES[grad.dtype], _TYPES[out.dtype],
+                         1 if accumulate else 0, _check_scale(scale))
+    L, size, ref = lib(), ctypes.c_size_t(0), ctypes.byref(op)
+    _check(L.df11_embedding_gradient_workspace(ref, ctypes.byref(size)),
+           "df11_embedding_gradient_workspace")
+    work = _aligned_empty(size.value, dev)
+    _check(L.df11_embedding_gradient(ref, work.data_ptr(), size.value,
+                                     err.data_ptr() if err is not None else None,
+                                     torch.cuda.current_stream().cuda_stream),
+           "df11_embedding_gradient")
     return out

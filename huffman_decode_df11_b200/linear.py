@@ -203,7 +203,7 @@ def _each(name, values, n, default=None):
 def _aligned_empty(nbytes: int, device) -> torch.Tensor:
     t = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
     off = -t.data_ptr() % 256
-    return t[off:off + nbytes]
+    return t[off:] if off else t  # allocations start on 256 bytes as a rule
 
 
 class LinearPlan:
