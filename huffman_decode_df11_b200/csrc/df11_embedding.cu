@@ -323,14 +323,21 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 // ---- gradient: sort by token ----------------------------------------------------
 
-constexpr int kSortThreads = 1024, kSortWarps = 32, kMaxDigits = 256;
+constexpr int kSortThreads = 1024, kSortWarps = 32, kMaxDigitBits = 9, kMaxDigits = 512;
+constexpr uint32_t kBatch = 4;  // tokens of a lane loaded together
 
 struct SortArgs {
   const void *ids;
   uint32_t *key[2], *tok[2];  // the sorted list ends in [passes & 1]
+  uint32_t *crossing;         // [0]: runs that cross pieces, counted by the next kernel
   uint32_t *touched;          // a bit per row that has tokens; NULL: not wanted
+  // the clusters after the first set rows zero_from .. rows - 1 of the gradient to zero
+  // meanwhile, tokens or not: the last ones of the table, which the fewest tokens have
+  void *out;
+  uint64_t out_stride;        // in bytes
+  uint32_t row_bytes, zero_from, touched_words;
   int32_t *err;
-  uint32_t tokens, rows, passes, digit_bits, touched_words, ids64;
+  uint32_t tokens, rows, passes, digit_bits, ids64;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -358,12 +365,53 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// One cluster sorts (id, token) by id, least significant digit first; every
+// the lanes of `active` whose digit is this lane's (a vote per bit: a match instruction takes
+// several times as long for 32 different digits)
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit, uint32_t bits, uint32_t active) {
+  uint32_t peers = active;
+  for (uint32_t b = 0; b < bits; ++b) {
+    const bool one = (digit >> b) & 1u;
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, one);
+    peers &= one ? m : ~m;
+  }
+  return peers;
+}
+
+struct SortShared {
+  uint32_t whist[kSortWarps][kMaxDigits + 1];  // a column in 32 banks
+  uint32_t own[kMaxDigits], base[kMaxDigits], warp_total[kMaxDigits / 32];
+};
+
+// Rows zero_from .. rows - 1 set to zero by thread block `block` of `blocks`, 16 bytes at a
+// time where the rows follow one another or start on 16-byte boundaries.
+__device__ void zero_rows(const SortArgs &a, uint32_t block, uint32_t blocks) {
+  uint8_t *out = static_cast<uint8_t *>(a.out) + (uint64_t)a.zero_from * a.out_stride;
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  const bool whole = a.out_stride == a.row_bytes;
+  const uint64_t n = a.rows - a.zero_from, rows = whole ? 1 : n;
+  const uint64_t bytes = whole ? n * a.row_bytes : a.row_bytes;
+  const bool vec = (uintptr_t)out % 16 == 0 && (whole || a.out_stride % 16 == 0);
+  // a row per thread block, or all of them over one
+  const uint64_t first = whole ? (uint64_t)block * kSortThreads + threadIdx.x : threadIdx.x;
+  const uint64_t step = whole ? (uint64_t)blocks * kSortThreads : kSortThreads;
+  for (uint64_t r = whole ? 0 : block; r < rows; r += whole ? 1 : blocks) {
+    uint8_t *p = out + r * a.out_stride;
+    const uint64_t quads = vec ? bytes / 16 : 0;
+    for (uint64_t i = first; i < quads; i += step) reinterpret_cast<uint4 *>(p)[i] = z;
+    for (uint64_t i = quads * 8 + first; i < bytes / 2; i += step)
+      reinterpret_cast<uint16_t *>(p)[i] = 0;
+  }
+}
+
+// The first cluster sorts (id, token) by id, least significant digit first; every
 // warp keeps a contiguous part of the list, so equal ids stay in token order.
 // An id outside the table sorts behind every row.
 __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs a) {
-  __shared__ uint32_t whist[kSortWarps][kMaxDigits + 1];  // a column in 32 banks
-  __shared__ uint32_t own[kMaxDigits], base[kMaxDigits], warp_total[kMaxDigits / 32];
+  extern __shared__ SortShared sort_shared[];
+  auto &whist = sort_shared->whist;
+  auto &own = sort_shared->own;
+  auto &base = sort_shared->base;
+  auto &warp_total = sort_shared->warp_total;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
   const uint32_t parts = ctas * kSortWarps;
@@ -372,6 +420,12 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
   const uint64_t end = begin + per < a.tokens ? begin + per : a.tokens;
   const uint32_t digits = 1u << a.digit_bits;
   pdl_wait();  // the ids may come from the previous kernel; the workspace may still be read
+  if (blockIdx.x >= ctas) {
+    zero_rows(a, blockIdx.x - ctas, gridDim.x - ctas);
+    pdl_launch_dependents();
+    return;  // a whole cluster
+  }
+  if (rank == 0 && tid == 0) a.crossing[0] = 0;
   if (a.touched)
     for (uint32_t i = rank * kSortThreads + tid; i < a.touched_words; i += ctas * kSortThreads)
       a.touched[i] = 0;
@@ -387,13 +441,21 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
     };
     for (uint32_t d = lane; d < digits; d += 32) whist[warp][d] = 0;
     __syncwarp();
-    for (uint64_t i = begin + lane; i - lane < end; i += 32) {
-      const bool act = i < end;
-      const uint32_t digit = act ? (load(i) >> shift) & (digits - 1u) : 0xFFFFFFFFu;
-      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, digit);
-      if (act && (peers >> lane) == 1u)  // the last of the peers
-        whist[warp][digit] += __popc(peers);
-      __syncwarp();
+    uint32_t held[kBatch];  // the keys of the batch at hand; of the whole part if it has but one
+    for (uint64_t i0 = begin; i0 < end; i0 += 32 * kBatch) {
+#pragma unroll
+      for (uint32_t j = 0; j < kBatch; ++j)
+        if (i0 + 32 * j + lane < end) held[j] = load(i0 + 32 * j + lane);
+#pragma unroll
+      for (uint32_t j = 0; j < kBatch; ++j) {
+        if (i0 + 32 * j >= end) break;
+        const bool act = i0 + 32 * j + lane < end;
+        const uint32_t digit = act ? (held[j] >> shift) & (digits - 1u) : 0u;
+        const uint32_t peers = same_digit(digit, a.digit_bits, __ballot_sync(0xFFFFFFFFu, act));
+        if (act && (peers >> lane) == 1u)  // the last of the peers
+          whist[warp][digit] += __popc(peers);
+        __syncwarp();
+      }
     }
     __syncthreads();
     // per digit, the counts of the warps before and this thread block's: a warp per digit, a
@@ -431,26 +493,43 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
     if (tid < kMaxDigits)
       for (uint32_t w = 0; w < warp; ++w) base[tid] += warp_total[w];
     __syncthreads();
-    for (uint64_t i = begin + lane; i - lane < end; i += 32) {
-      const bool act = i < end;
-      const uint32_t key = act ? load(i) : 0u;
-      const uint32_t digit = act ? (key >> shift) & (digits - 1u) : 0xFFFFFFFFu;
-      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, digit);
-      uint32_t at = 0;
-      if (act) at = base[digit] + whist[warp][digit] + __popc(peers & ((1u << lane) - 1u));
-      __syncwarp();
-      if (act && (peers >> lane) == 1u) whist[warp][digit] += __popc(peers);
-      __syncwarp();
-      if (act) {
-        dk[at] = key;
-        dt[at] = p ? __ldcg(st + i) : (uint32_t)i;
-        if (p == 0) {
-          if (key == a.rows) report(a.err, DF11_DEV_ERR_INDEX);
-          else if (a.touched) atomicOr(a.touched + (key >> 5), 1u << (key & 31u));
+    for (uint64_t i0 = begin; i0 < end; i0 += 32 * kBatch) {
+      uint32_t tok[kBatch];
+#pragma unroll
+      for (uint32_t j = 0; j < kBatch; ++j) {
+        const uint64_t i = i0 + 32 * j + lane;
+        if (i >= end) continue;
+        if (per > 32 * kBatch) held[j] = load(i);
+        tok[j] = p ? __ldcg(st + i) : (uint32_t)i;
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < kBatch; ++j) {
+        if (i0 + 32 * j >= end) break;
+        const bool act = i0 + 32 * j + lane < end;
+        const uint32_t key = held[j];
+        const uint32_t digit = act ? (key >> shift) & (digits - 1u) : 0u;
+        const uint32_t peers = same_digit(digit, a.digit_bits, __ballot_sync(0xFFFFFFFFu, act));
+        uint32_t at = 0;
+        if (act) at = base[digit] + whist[warp][digit] + __popc(peers & ((1u << lane) - 1u));
+        __syncwarp();
+        if (act && (peers >> lane) == 1u) whist[warp][digit] += __popc(peers);
+        __syncwarp();
+        if (act) {
+          dk[at] = key;
+          dt[at] = tok[j];
         }
       }
     }
     cluster_sync();  // the list is whole, and own[] read by everyone
+  }
+  // the rows that have tokens, by the first token of each (all tokens' marks would meet at
+  // the few words of the commonest rows)
+  const uint32_t *sk = a.key[a.passes & 1];
+  for (uint64_t i = rank * kSortThreads + tid; i < a.tokens; i += ctas * kSortThreads) {
+    const uint32_t key = __ldcg(sk + i);
+    if (i && __ldcg(sk + i - 1) == key) continue;
+    if (key == a.rows) report(a.err, DF11_DEV_ERR_INDEX);
+    else if (a.touched) atomicOr(a.touched + (key >> 5), 1u << (key & 31u));
   }
   pdl_launch_dependents();
 }
@@ -464,10 +543,12 @@ struct RunArgs {
   const void *grad;
   void *out;
   const uint32_t *key, *tok;  // sorted
-  const uint32_t *touched;    // NULL: rows without tokens keep their values
+  const uint32_t *touched;    // a bit per row that has tokens
+  uint32_t zero_rows;         // rows below this without one are set to zero here
+  uint32_t *crossing;         // their number, then the pieces where runs begin that cross pieces
   float *head, *tail;         // per piece: sums of the run that began before it / that goes on
   uint64_t grad_stride, out_stride;
-  uint32_t tokens, rows, dim, piece, pieces, col_tiles, join_tiles, part_stride;
+  uint32_t tokens, rows, dim, piece, pieces, col_tiles, part_stride;
   uint32_t accumulate;
   float scale;
 };
@@ -546,9 +627,8 @@ __device__ __forceinline__ void write_part(float *p, const float (&s)[V]) {
   }
 }
 
-// Thread blocks below pieces * col_tiles: the runs of one piece of the sorted
-// list, kRunThreads * V columns.  The others: 32 rows each, those without a token
-// set to zero.
+// Thread blocks below pieces * col_tiles: the runs of one piece of the sorted list,
+// kRunThreads * V columns.  The others: 32 rows each, those without a token set to zero.
 template <typename G, typename O, int V>
 __global__ void __launch_bounds__(kRunThreads) embedding_runs_kernel(const __grid_constant__ RunArgs a) {
   __shared__ uint32_t key_s[kMaxPiece + 2], tok_s[kMaxPiece];
@@ -560,7 +640,7 @@ __global__ void __launch_bounds__(kRunThreads) embedding_runs_kernel(const __gri
     const uint32_t bits = __ldg(a.touched + word);
     for (uint32_t r = 0; r < 32; ++r) {
       const uint32_t row = 32u * word + r;
-      if (row >= a.rows) break;
+      if (row >= a.zero_rows) break;
       if ((bits >> r) & 1u) continue;
       O *p = static_cast<O *>(a.out) + (size_t)row * a.out_stride;
       if constexpr (V == 1) {
@@ -584,6 +664,10 @@ __global__ void __launch_bounds__(kRunThreads) embedding_runs_kernel(const __gri
   if (tid == 32) key_s[0] = i0 ? __ldcg(a.key + i0 - 1) : 0xFFFFFFFFu;
   if (tid == 33) key_s[n + 1] = i1 < a.tokens ? __ldcg(a.key + i1) : 0xFFFFFFFFu;
   __syncthreads();
+  // the piece's last run goes on and began here: the next kernel puts it together (in any
+  // order, since every run is by itself)
+  if (ct == 0 && tid == 0 && key_s[n] < a.rows && key_s[n + 1] == key_s[n] && key_s[0] != key_s[n])
+    a.crossing[1 + atomicAdd(a.crossing, 1u)] = piece;
   const uint32_t col = (ct * kRunThreads + tid) * V;
   if (col >= a.dim) return;
   const G *g = static_cast<const G *>(a.grad) + col;
@@ -618,68 +702,84 @@ __global__ void __launch_bounds__(kRunThreads) embedding_runs_kernel(const __gri
   }
 }
 
-// A run that crosses pieces, by the piece where it begins: its tail there and
-// the heads of the pieces after it, in order.
+// A run that crosses pieces: its tail in the piece where it begins and the heads of the
+// pieces after it, 32 V columns per thread block.  Each of the four warps adds every fourth
+// head, and their sums follow the tail in order.
+constexpr uint32_t kJoinWarps = kRunThreads / 32;
 template <typename O, int V>
-__global__ void __launch_bounds__(kRunThreads) embedding_join_kernel(const __grid_constant__ RunArgs a) {
-  __shared__ uint32_t stop_s[kRunThreads / 32];
+__global__ void __launch_bounds__(kRunThreads, 12) embedding_join_kernel(const __grid_constant__ RunArgs a) {
+  __shared__ uint32_t stop_s[kJoinWarps];
+  __shared__ float sums[kJoinWarps][32 * V];
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_launch_dependents();
-  const uint32_t piece = blockIdx.x / a.join_tiles, ct = blockIdx.x - piece * a.join_tiles;
-  const uint32_t i0 = piece * a.piece, i1 = i0 + a.piece;
-  if (i1 >= a.tokens) return;
-  const uint32_t key = __ldcg(a.key + i1 - 1);
-  if (key >= a.rows || __ldcg(a.key + i1) != key) return;
-  // begun before this piece: another thread block's
-  if (i0 && __ldcg(a.key + i0 - 1) == key) return;
-  // the run's last piece: the first one after this that does not end in the run's key, or
-  // whose next token has another; a piece per thread, until some thread has it
-  uint32_t last = piece + 1;
-  for (;; last += kRunThreads) {
-    const uint32_t p = last + threadIdx.x;
-    const uint64_t e = ((uint64_t)p + 1) * a.piece;  // the token after the piece
-    const bool goes_on = e < a.tokens && __ldcg(a.key + e) == key;
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, !goes_on);
-    if ((threadIdx.x & 31u) == 0) stop_s[threadIdx.x >> 5] = m ? (threadIdx.x & ~31u) + __ffs(m) - 1 : kRunThreads;
-    __syncthreads();
-    uint32_t first = kRunThreads;
+  const uint32_t tiles = (a.dim + 32 * V - 1) / (32 * V);
+  const uint64_t work = (uint64_t)__ldcg(a.crossing) * tiles;
+  for (uint64_t u = blockIdx.x; u < work; u += gridDim.x) {
+    const uint32_t piece = __ldcg(a.crossing + 1 + u / tiles), tile = (uint32_t)(u % tiles);
+    const uint32_t key = __ldcg(a.key + (piece + 1) * a.piece);
+    // the run's last piece: the first one after this whose next token has another key; a
+    // piece per thread, until some thread has it
+    uint32_t last = piece + 1;
+    for (;; last += kRunThreads) {
+      const uint64_t e = ((uint64_t)last + tid + 1) * a.piece;  // the token after the piece
+      const bool goes_on = e < a.tokens && __ldcg(a.key + e) == key;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, !goes_on);
+      if (lane == 0) stop_s[warp] = m ? (tid & ~31u) + __ffs(m) - 1 : kRunThreads;
+      __syncthreads();
+      uint32_t first = kRunThreads;
 #pragma unroll
-    for (int w = 0; w < kRunThreads / 32; ++w) first = min(first, stop_s[w]);
-    __syncthreads();
-    if (first < kRunThreads) {
-      last += first;
-      break;
-    }
-  }
-  const uint32_t col = (ct * kRunThreads + threadIdx.x) * V;
-  if (col >= a.dim) return;
-  float s[V];
-  auto load = [&](const float *p, float (&v)[V]) {
-    if constexpr (V == 1) {
-      v[0] = __ldcg(p);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; j += 4) {
-        const float4 q = __ldcg(reinterpret_cast<const float4 *>(p + j));
-        v[j] = q.x; v[j + 1] = q.y; v[j + 2] = q.z; v[j + 3] = q.w;
+      for (uint32_t w = 0; w < kJoinWarps; ++w) first = min(first, stop_s[w]);
+      __syncthreads();
+      if (first < kRunThreads) {
+        last += first;
+        break;
       }
     }
-  };
-  load(a.tail + (size_t)piece * a.part_stride + col, s);
-  constexpr uint32_t kAhead = 8;
-  for (uint32_t p = piece + 1; p <= last; p += kAhead) {
-    float v[kAhead][V];
+    const uint32_t col = (tile * 32 + lane) * V;
+    float s[V];
+    auto load = [&](const float *p, float (&v)[V]) {
+      if constexpr (V == 1) {
+        v[0] = __ldcg(p);
+      } else {
 #pragma unroll
-    for (uint32_t u = 0; u < kAhead; ++u)
-      if (p + u <= last) load(a.head + (size_t)(p + u) * a.part_stride + col, v[u]);
-#pragma unroll
-    for (uint32_t u = 0; u < kAhead; ++u)
-      if (p + u <= last) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) s[j] += v[u][j];
+        for (int j = 0; j < V; j += 4) {
+          const float4 q = __ldcg(reinterpret_cast<const float4 *>(p + j));
+          v[j] = q.x; v[j + 1] = q.y; v[j + 2] = q.z; v[j + 3] = q.w;
+        }
       }
+    };
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = 0.f;
+    if (col < a.dim) {
+      constexpr uint32_t kAhead = 4;
+      for (uint32_t p = piece + 1 + warp; p <= last; p += kAhead * kJoinWarps) {
+        float v[kAhead][V];
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; ++k)
+          if (p + k * kJoinWarps <= last)
+            load(a.head + (size_t)(p + k * kJoinWarps) * a.part_stride + col, v[k]);
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; ++k)
+          if (p + k * kJoinWarps <= last) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] += v[k][j];
+          }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) sums[warp][lane * V + j] = s[j];
+    __syncthreads();
+    if (warp == 0 && col < a.dim) {
+      load(a.tail + (size_t)piece * a.part_stride + col, s);
+#pragma unroll
+      for (uint32_t w = 0; w < kJoinWarps; ++w)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] += sums[w][lane * V + j];
+      write_row<O, V>(a, key, col, s);
+    }
+    __syncthreads();
   }
-  write_row<O, V>(a, key, col, s);
 }
 
 // ---- host side --------------------------------------------------------------------
@@ -715,8 +815,8 @@ df11_status launch_embedding(EmbedArgs &a, size_t smem, int instance, cudaStream
 }
 
 struct GradPlan {
-  uint32_t piece, pieces, col_tiles, part_stride, passes, digit_bits, words;
-  uint64_t key[2], tok[2], touched, head, tail, bytes;
+  uint32_t piece, pieces, col_tiles, part_stride, passes, digit_bits;
+  uint64_t key[2], tok[2], touched, crossing, head, tail, bytes;
   int v;  // columns per thread
 };
 
@@ -741,9 +841,8 @@ GradPlan grad_plan(const df11_embedding_grad &op) {
   p.part_stride = (uint32_t)round_up(op.dim, 8);
   uint32_t bits = 1;
   while ((op.rows >> bits) != 0) ++bits;  // keys 0 .. rows
-  p.passes = (bits + 7) / 8;
+  p.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
   p.digit_bits = (bits + p.passes - 1) / p.passes;
-  p.words = (op.rows + 31) / 32;
   uint64_t off = 0;
   auto take = [&](uint64_t bytes) {
     const uint64_t at = off;
@@ -754,7 +853,8 @@ GradPlan grad_plan(const df11_embedding_grad &op) {
     p.key[i] = take(4ull * op.tokens);
     p.tok[i] = take(4ull * op.tokens);
   }
-  p.touched = take(4ull * p.words);
+  p.touched = take((op.rows + 31ull) / 32 * 4);
+  p.crossing = take(4ull * (p.pieces + 1));
   p.head = take(4ull * p.pieces * p.part_stride);
   p.tail = take(4ull * p.pieces * p.part_stride);
   p.bytes = off;
@@ -767,7 +867,8 @@ df11_status check_grad(const df11_embedding_grad *op) {
       (op->ids_type != DF11_IDS_I32 && op->ids_type != DF11_IDS_I64))
     return DF11_ERR_INVALID;
   if (op->rows == 0 || op->dim == 0) return DF11_ERR_INVALID;
-  if (op->rows >= (1u << 31) || op->tokens >= (1u << 31)) return DF11_ERR_TOO_LARGE;
+  if (op->rows >= (1u << 31) || op->tokens >= (1u << 31) || op->dim >= (1u << 30))
+    return DF11_ERR_TOO_LARGE;
   if (op->out_stride < op->dim || (op->tokens && op->grad_stride < op->dim)) return DF11_ERR_INVALID;
   if (!op->out || (op->tokens && (!op->ids || !op->grad))) return DF11_ERR_NULL;
   if (!aligned(op->ids, op->ids_type == DF11_IDS_I64 ? 8 : 4) ||
@@ -777,24 +878,22 @@ df11_status check_grad(const df11_embedding_grad *op) {
 }
 
 template <typename G, typename O, int V>
-df11_status launch_runs(const RunArgs &a, uint32_t zero_blocks, cudaStream_t s) {
-  const uint32_t runs = a.pieces * a.col_tiles;
-  if (runs + zero_blocks == 0) return DF11_OK;
-  df11_status st = launch_pdl(embedding_runs_kernel<G, O, V>, dim3(runs + zero_blocks), kRunThreads,
-                              0, s, a);
+df11_status launch_runs(const RunArgs &a, cudaStream_t s) {
+  const uint32_t blocks = a.pieces * a.col_tiles + (a.zero_rows + 31) / 32;
+  if (blocks == 0) return DF11_OK;
+  df11_status st = launch_pdl(embedding_runs_kernel<G, O, V>, dim3(blocks), kRunThreads, 0, s, a);
   if (st != DF11_OK || a.pieces < 2) return st;
   // four columns per thread at most: more threads on the few rows that many tokens share
-  return launch_pdl(embedding_join_kernel<O, V == 1 ? 1 : 4>, dim3(a.pieces * a.join_tiles),
+  constexpr int J = V == 1 ? 1 : 4;
+  const uint64_t most = (uint64_t)a.pieces * ((a.dim + 32 * J - 1) / (32 * J));
+  return launch_pdl(embedding_join_kernel<O, J>, dim3((uint32_t)(most < 148 * 12 ? most : 148 * 12)),
                     kRunThreads, 0, s, a);
 }
 
 template <typename O>
-df11_status launch_runs_for(const RunArgs &a, bool grad_f32, bool vec, uint32_t zero_blocks,
-                            cudaStream_t s) {
-  if (grad_f32)
-    return vec ? launch_runs<float, O, 4>(a, zero_blocks, s) : launch_runs<float, O, 1>(a, zero_blocks, s);
-  return vec ? launch_runs<uint16_t, O, 8>(a, zero_blocks, s)
-             : launch_runs<uint16_t, O, 1>(a, zero_blocks, s);
+df11_status launch_runs_for(const RunArgs &a, bool grad_f32, bool vec, cudaStream_t s) {
+  if (grad_f32) return vec ? launch_runs<float, O, 4>(a, s) : launch_runs<float, O, 1>(a, s);
+  return vec ? launch_runs<uint16_t, O, 8>(a, s) : launch_runs<uint16_t, O, 1>(a, s);
 }
 
 }  // namespace
@@ -880,25 +979,43 @@ df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspa
     so.key[i] = reinterpret_cast<uint32_t *>(ws + p.key[i]);
     so.tok[i] = reinterpret_cast<uint32_t *>(ws + p.tok[i]);
   }
-  so.touched = op->accumulate ? nullptr : reinterpret_cast<uint32_t *>(ws + p.touched);
+  so.crossing = reinterpret_cast<uint32_t *>(ws + p.crossing);
   so.err = d_err;
   so.tokens = op->tokens;
   so.rows = op->rows;
   so.passes = p.passes;
   so.digit_bits = p.digit_bits;
-  so.touched_words = p.words;
   so.ids64 = op->ids_type == DF11_IDS_I64;
   // one thread block per 1024 tokens (32 per warp), up to a cluster of eight
   uint32_t ctas = 1;
   while (ctas < 8 && (uint64_t)ctas * kSortThreads < op->tokens) ctas *= 2;
-  st = launch_cluster(embedding_sort_kernel, ctas, kSortThreads, s, so);
+  uint64_t budget = 0;
+  st = prepare(embedding_sort_kernel, kSortThreads, sizeof(SortShared), 81, budget);
+  if (st != DF11_OK) return st;
+  // Rows set to zero beside the sort, as many as it leaves time for: it takes about 10 us, and
+  // 1 us per 1300 tokens, and the other SMs write 4.5 MB per us (measured).  The rest
+  // is set to zero beside the runs, where rows with tokens are left out.
+  uint32_t grid = ctas;
+  if (!op->accumulate) {
+    so.touched = reinterpret_cast<uint32_t *>(ws + p.touched);
+    so.touched_words = (op->rows + 31) / 32;
+    so.out = op->out;
+    so.out_stride = op->out_stride * type_bytes(op->out_type);
+    so.row_bytes = (uint32_t)(op->dim * type_bytes(op->out_type));
+    uint64_t beside = (10 + op->tokens / 1300) * 4500000ull / so.row_bytes;
+    if (beside > op->rows) beside = op->rows;
+    so.zero_from = (uint32_t)(op->rows - beside);
+    uint64_t blocks = (beside * so.row_bytes + 65535) / 65536;
+    if (blocks > budget) blocks = budget;
+    grid += (uint32_t)round_up(blocks, ctas);
+  }
+  st = launch_cluster(embedding_sort_kernel, grid, ctas, kSortThreads, sizeof(SortShared), s, so);
   if (st != DF11_OK) return st;
   RunArgs r{};
   r.grad = op->grad;
   r.out = op->out;
   r.key = so.key[p.passes & 1];
   r.tok = so.tok[p.passes & 1];
-  r.touched = so.touched;
   r.head = reinterpret_cast<float *>(ws + p.head);
   r.tail = reinterpret_cast<float *>(ws + p.tail);
   r.grad_stride = op->grad_stride;
@@ -909,14 +1026,15 @@ df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspa
   r.piece = p.piece;
   r.pieces = p.pieces;
   r.col_tiles = p.col_tiles;
-  r.join_tiles = (op->dim + kRunThreads * (p.v > 1 ? 4 : 1) - 1) / (kRunThreads * (p.v > 1 ? 4 : 1));
+  r.crossing = so.crossing;
+  r.touched = so.touched;
+  r.zero_rows = so.zero_from;
   r.part_stride = p.part_stride;
   r.accumulate = op->accumulate ? 1 : 0;
   r.scale = op->scale;
-  const uint32_t zero_blocks = op->accumulate ? 0 : p.words;
   const bool gf = op->grad_type == DF11_F32, vec = p.v > 1;
-  return op->out_type == DF11_F32 ? launch_runs_for<float>(r, gf, vec, zero_blocks, s)
-                                  : launch_runs_for<uint16_t>(r, gf, vec, zero_blocks, s);
+  return op->out_type == DF11_F32 ? launch_runs_for<float>(r, gf, vec, s)
+                                  : launch_runs_for<uint16_t>(r, gf, vec, s);
 }
 
 }  // extern "C"

@@ -135,13 +135,14 @@ df11_status launch_pdl(void (*kern)(Args...), dim3 grid, uint32_t threads, size_
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DF11_OK : DF11_ERR_CUDA;
 }
 
-// The same for a grid that is one cluster of `ctas` thread blocks (at most 8).
+// The same for a grid of clusters of `ctas` thread blocks (at most 8).
 template <typename... Args>
-df11_status launch_cluster(void (*kern)(Args...), uint32_t ctas, uint32_t threads, cudaStream_t s,
-                           Args... args) {
+df11_status launch_cluster(void (*kern)(Args...), uint32_t grid, uint32_t ctas, uint32_t threads,
+                           size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
