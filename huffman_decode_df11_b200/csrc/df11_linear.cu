@@ -458,14 +458,20 @@ struct Multiply {
           : "l"(p), "r"(there));
     }
   }
+  // A tile's products are summed from zero and then added in fp32: the tensor cores cut off
+  // what an addition leaves below their accumulator, so a long chain of products drifts
+  // towards zero (relative error 3.8e-6 at 4096 columns; 2e-7 like this).
   __device__ __forceinline__ void operator()(uint32_t, uint32_t, const uint32_t (&w0)[8],
                                              const uint32_t (&w1)[8]) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      mma_bf16(acc[j], w0[0], w1[0], w0[1], w1[1], xv[j][0].x, xv[j][0].y);
-      mma_bf16(acc[j], w0[2], w1[2], w0[3], w1[3], xv[j][0].z, xv[j][0].w);
-      mma_bf16(acc[j], w0[4], w1[4], w0[5], w1[5], xv[j][1].x, xv[j][1].y);
-      mma_bf16(acc[j], w0[6], w1[6], w0[7], w1[7], xv[j][1].z, xv[j][1].w);
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_bf16(t, w0[0], w1[0], w0[1], w1[1], xv[j][0].x, xv[j][0].y);
+      mma_bf16(t, w0[2], w1[2], w0[3], w1[3], xv[j][0].z, xv[j][0].w);
+      mma_bf16(t, w0[4], w1[4], w0[5], w1[5], xv[j][1].x, xv[j][1].y);
+      mma_bf16(t, w0[6], w1[6], w0[7], w1[7], xv[j][1].z, xv[j][1].w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[j][k] += t[k];
     }
   }
 };
@@ -740,10 +746,16 @@ __global__ void __launch_bounds__(1024) linear_rows_kernel(uint32_t *unit_rows, 
 // caller's rows), B the decoded tiles (bn rows; a 16 x 64 tile is 16 rows of 128
 // bytes, so a TMA box of bn/16 row blocks is bn rows of 64 columns), both in the
 // 128-byte swizzle, K in steps of 64.  One warp issues the copies, one the
-// products, four move finished accumulators (two, in turn) out through the
-// epilogue: a lane is a token, its columns consecutive rows of W.
+// products, eight move finished accumulators (two, in turn) out through the
+// epilogue: a lane is a token, its columns consecutive rows of W, two warps
+// taking groups of 16 in turn.
+//   For fp32 outputs the accumulators are moved out every kPart steps and added in
+// registers (SUMS), because the tensor cores cut off what an addition leaves below their
+// accumulator: at 12288 columns that drifts by 1e-5, which a BF16 output does not
+// show.  Tiles are then at most 128 rows wide.
 constexpr int kGemmTokens = 128;
-constexpr int kGemmThreads = 6 * 32;  // warps 0-3: epilogue, 4: copies, 5: products
+constexpr int kEpilogueWarps = 8;  // warps 0-7: epilogue, 8: copies, 9: products
+constexpr int kGemmThreads = (kEpilogueWarps + 2) * 32;
 
 struct GemmArgs {
   Epilogue e;
@@ -756,6 +768,8 @@ struct GemmArgs {
 };
 
 constexpr uint32_t kXBytes = kGemmTokens * 128;
+constexpr uint32_t kPart = 8;      // steps of 64 columns between accumulators (SUMS)
+constexpr uint32_t kSumRows = 128; // rows of a tile whose sums are in registers (SUMS)
 constexpr uint32_t kMaxStages = 8;
 // barriers: full and empty per stage, two accumulators' full and empty; the tensor-memory
 // address
@@ -864,6 +878,7 @@ __device__ __forceinline__ void finish16(const Epilogue &e, float (&v)[16], uint
   }
 }
 
+template <bool SUMS>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     df11_linear_gemm_kernel(const __grid_constant__ CUtensorMap map_x,
                             const __grid_constant__ CUtensorMap map_w,
@@ -886,11 +901,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (uint32_t i = 0; i < 2; ++i) {
       mbar_init(acc_full(i), 1);
-      mbar_init(acc_empty(i), 4);
+      mbar_init(acc_empty(i), kEpilogueWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 5) {
+  if (warp == kEpilogueWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(taddr_s),
                  "r"(ga.tmem_cols)
                  : "memory");
@@ -903,7 +918,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   pdl_wait();  // the decoded weight, and x, come from the kernels before
   bool failed = false;
 
-  if (warp == 4) {
+  if (warp == kEpilogueWarps) {
     if (lane == 0) {
       uint32_t k = 0, s = 0, par = 0;  // copies so far; the stage, and its uses' parity
       for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
@@ -930,20 +945,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (!mbar_wait(full(j % S), (j / S) & 1u, ga.spin_limit)) failed = true;
       if (failed) report(ga.err, DF11_DEV_ERR_TIMEOUT);
     }
-  } else if (warp == 5) {
+  } else if (warp == kEpilogueWarps + 1) {
     // fp32 accumulators, BF16 operands, both K-major
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((bn / 8) << 17) |
                            ((kGemmTokens / 16) << 24);
     uint32_t k = 0, n = 0, s = 0, par = 0;
-    for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x, ++n) {
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_empty(n & 1), ((n >> 1) & 1u) ^ 1u,
-                                              ga.spin_limit))) {
-        failed = true;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t d = tmem + (n & 1u) * bn;
+    for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
+      uint32_t d = 0;
       for (uint32_t c = 0; c < ga.ncg; ++c, ++k) {
+        const bool first = SUMS ? c % kPart == 0 : c == 0;  // into the other accumulator
+        const bool last = c + 1 == ga.ncg || (SUMS && (c + 1) % kPart == 0);
+        if (first) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_empty(n & 1), ((n >> 1) & 1u) ^ 1u,
+                                                  ga.spin_limit))) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          d = tmem + (n & 1u) * bn;
+        }
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(full(s), par, ga.spin_limit))) {
           failed = true;
           break;
@@ -954,7 +974,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint64_t bd = sw128_desc(base + s * stage_bytes + kXBytes);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {  // K = 16: 32 bytes on
-            const uint32_t add = c || j ? 1u : 0u;
+            const uint32_t add = !first || j ? 1u : 0u;
             asm volatile(
                 "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
@@ -965,13 +985,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                   empty(s))
               : "memory");
-          if (c + 1 == ga.ncg)
+          if (last)
             asm volatile(
                 "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                     acc_full(n & 1))
                 : "memory");
         }
         __syncwarp();
+        if (last) ++n;
         if (++s == S) {
           s = 0;
           par ^= 1u;
@@ -984,50 +1005,78 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (failed && lane == 0) report(ga.err, DF11_DEV_ERR_TIMEOUT);
   } else {
     uint32_t n = 0;
-    for (uint32_t tile = blockIdx.x; tile < ga.tiles; tile += gridDim.x, ++n) {
-      const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full(n & 1), (n >> 1) & 1u, ga.spin_limit))) {
-        failed = true;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t token = tm * kGemmTokens + 32u * warp + lane;
-      const uint32_t src = tmem + ((32u * warp) << 16) + (n & 1u) * bn;
-      for (uint32_t c = 0; c < bn; c += 16) {
-        const uint32_t row = tn * bn + c;
-        if (row >= ga.rows) break;
-        uint32_t u[16];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-            "%11, %12, %13, %14, %15}, [%16];"
-            : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
-              "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]),
-              "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
-            : "r"(src + c)
-            : "memory");
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        float v[16];
+    const uint32_t quarter = warp & 3, half = 16u * (warp >> 2);
+    const uint32_t lanes = tmem + ((32u * quarter) << 16);
+    // 16 of the lane's columns
+    auto read16 = [&](uint32_t src, float (&v)[16]) {
+      uint32_t u[16];
+      asm volatile(
+          "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+          "%11, %12, %13, %14, %15}, [%16];"
+          : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+            "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]),
+            "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+          : "r"(src)
+          : "memory");
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(u[j]);
-        if (token >= ga.tokens) {
-          // a row of the tile past the last token
-        } else if (ga.vec && row + 16 <= ga.rows) {
-          finish16<true>(ga.e, v, token, row, 16u);
-        } else {
-          finish16<false>(ga.e, v, token, row, min(ga.rows - row, 16u));
-        }
-        __syncwarp();
-      }
+      for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(u[j]);
+    };
+    auto write16 = [&](float (&v)[16], uint32_t token, uint32_t row) {
+      if (token >= ga.tokens || row >= ga.rows) return;
+      if (ga.vec && row + 16 <= ga.rows) finish16<true>(ga.e, v, token, row, 16u);
+      else finish16<false>(ga.e, v, token, row, min(ga.rows - row, 16u));
+    };
+    auto acquire = [&]() {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full(n & 1), (n >> 1) & 1u, ga.spin_limit)))
+        failed = true;
+      tc_fence_after();
+      return !failed;
+    };
+    auto release = [&]() {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty(n & 1));
+      ++n;
+    };
+    for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
+      const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m;
+      const uint32_t token = tm * kGemmTokens + 32u * quarter + lane;
+      if constexpr (SUMS) {
+        float sum[kSumRows / 32][16];
+        for (uint32_t c0 = 0; c0 < ga.ncg; c0 += kPart) {
+          if (!acquire()) break;
+#pragma unroll
+          for (uint32_t g = 0; g < kSumRows / 32; ++g) {
+            if (32u * g + half >= bn) break;
+            float v[16];
+            read16(lanes + (n & 1u) * bn + 32u * g + half, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[g][j] = c0 ? sum[g][j] + v[j] : v[j];
+          }
+          release();
+        }
+        if (failed) break;
+#pragma unroll
+        for (uint32_t g = 0; g < kSumRows / 32; ++g)
+          if (32u * g + half < bn) write16(sum[g], token, tn * bn + 32u * g + half);
+      } else {
+        if (!acquire()) break;
+        for (uint32_t c = half; c < bn && tn * bn + c < ga.rows; c += 32) {
+          float v[16];
+          read16(lanes + (n & 1u) * bn + c, v);
+          write16(v, token, tn * bn + c);
+          __syncwarp();
+        }
+        release();
+      }
     }
     if (failed && lane == 0) report(ga.err, DF11_DEV_ERR_TIMEOUT);
   }
   // every warp is here before the tensor memory goes
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kEpilogueWarps + 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(ga.tmem_cols)
                  : "memory");
@@ -1366,7 +1415,8 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
   // and what 32 more would for reading x and emptying the accumulator; the wider one of two
   // (4096 rows and 2048 tokens on 148 SMs: 240 rows, 288 tiles in two rounds)
   uint64_t cost = ~0ull;
-  for (uint32_t bn = 256; bn >= 16; bn -= 16) {
+  const bool sums = op.y_type == DF11_F32 && ga.ncg > kPart;
+  for (uint32_t bn = sums ? kSumRows : 256; bn >= 16; bn -= 16) {
     const uint64_t tiles = (uint64_t)ga.tiles_m * ((rows + bn - 1) / bn);
     const uint64_t c = (tiles + sms - 1) / sms * (bn + 32);
     if (c < cost) {
@@ -1401,10 +1451,12 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
   }
   const size_t smem = gemm_smem(ga.bn, ga.stages);
   uint64_t budget = 0;
-  const df11_status st = prepare(df11_linear_gemm_kernel, kGemmThreads, smem, 75, budget);
+  void (*kern)(CUtensorMap, CUtensorMap, GemmArgs) =
+      sums ? df11_linear_gemm_kernel<true> : df11_linear_gemm_kernel<false>;
+  const df11_status st = prepare(kern, kGemmThreads, smem, sums ? 75 : 76, budget);
   if (st != DF11_OK) return st;
   const uint32_t grid = ga.tiles < (uint32_t)sms ? ga.tiles : (uint32_t)sms;
-  return launch_pdl(df11_linear_gemm_kernel, dim3(grid), kGemmThreads, smem, s, mx, mw, ga);
+  return launch_pdl(kern, dim3(grid), kGemmThreads, smem, s, mx, mw, ga);
 }
 
 df11_status check_linear_devices(const df11_linear_weight *ws, const df11_linear *ops, int count,

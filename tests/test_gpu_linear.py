@@ -427,3 +427,19 @@ def test_corrupt_weights_are_flagged_and_the_next_call_is_right(tokens, field):
     c.streams.copy_(good[2])
     y, = _run([c], [x], out_dtype=torch.float32)
     _check(w, x, y)
+
+
+@pytest.mark.parametrize("tokens", [1, 32, 40, 300])
+def test_long_sums_do_not_drift(tokens):
+    # the sum of 12288 positive products has a relative error of the order of fp32's own
+    # rounding, not of 12288 times it.  Exact products; a tile (64 columns, 16 products a step)
+    # or 512 columns are summed where each of at most 32 additions may cut off one unit
+    # (2^-23) of a partial sum of a part, the parts then with half a unit each: at most
+    # 32 2^-23 (the parts' own) + 200 2^-24 relative, and in the mean far less
+    cols = 12288
+    w = _bf16((64, cols), 0.02, 1).abs()
+    x = _bf16((tokens, cols), 1.0, 2).abs().cuda()
+    y, = _run([df11.compress_linear(w.cuda())], [x], out_dtype=torch.float32)
+    want = x.cpu().double() @ w.double().T
+    rel = ((y.cpu().double() - want) / want).abs()
+    assert float(rel.max()) <= 32 * 2.0 ** -23 + 200 * 2.0 ** -24
