@@ -129,6 +129,7 @@ def _compress_linear(w: torch.Tensor, stream) -> LinearWeight:
     d = out.desc()
     _check(L.df11_linear_weight_finish(w.data_ptr(), ctypes.byref(d), sh),
            "df11_linear_weight_finish")
+    torch.cuda.current_stream().synchronize()
     return out
 
 
@@ -216,10 +217,10 @@ class LinearPlan:
     outputs (tokens x rows).  `biases` (rows), `multipliers` and `residuals`
     (tokens x rows): per weight a float32 or BF16 tensor or None.
     `activations`: per weight "none", "relu", "gelu", "gelu_tanh" or "silu".
-    Rows of all of them must be contiguous; the row strides are free.  A
-    residual may be the output itself.  Runs of one plan share its workspace
-    and must not overlap on the GPU; plans on several streams at once are
-    plans of their own."""
+    Rows of all of them must be contiguous, at any distance of a row's length
+    or more.  A residual may be the output itself.  Runs of one plan share its
+    workspace and must not overlap on the GPU, graphs that captured them
+    included; for several streams at once, make a plan for each."""
 
     def __init__(self, ds: Sequence[LinearWeight], xs: Sequence[torch.Tensor],
                  ys: Sequence[torch.Tensor], biases=None, activations=None, multipliers=None,
@@ -244,6 +245,7 @@ class LinearPlan:
                                                        ctypes.byref(size)),
                        "df11_linear_workspace")
                 self._work = _aligned_empty(size.value, self._device)
+                self._streams = {_stream_handle(None)}  # that the allocator knows of
         self._bytes = size.value
 
     @property
@@ -260,10 +262,15 @@ class LinearPlan:
         if torch.cuda.current_device() != self._device.index:
             with torch.cuda.device(self._device):
                 return self.run(err, stream)
+        handle = _stream_handle(stream)
+        if handle not in self._streams and not torch.cuda.is_current_stream_capturing():
+            # a plan dropped while it runs there keeps its workspace until that is done
+            self._work.record_stream(_on_stream(handle))
+            self._streams.add(handle)
         _check(self._lib.df11_decode_linear(self._descs, self._ops, self._n,
                                             self._work.data_ptr(), self._bytes,
-                                            err.data_ptr() if err is not None else None,
-                                            _stream_handle(stream)), "df11_decode_linear")
+                                            err.data_ptr() if err is not None else None, handle),
+               "df11_decode_linear")
         return self._keep[2]
 
 
@@ -271,7 +278,7 @@ def _on_stream(stream):
     """A torch stream to allocate a call's buffers on (None: the current one)."""
     if stream is None or hasattr(stream, "cuda_stream"):
         return stream
-    return torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
 
 
 def decode_linear(ds: Sequence[LinearWeight], xs: Sequence[torch.Tensor],

@@ -184,6 +184,38 @@ def test_plan_in_a_captured_graph_reads_the_ids_of_the_replay():
             assert torch.equal(_bits(out.cpu()), _bits(w[want.long()]))
 
 
+def test_a_table_of_nearly_two_to_the_32_elements():
+    rows, dim = 65500, 65500
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.empty(rows, dim, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, rows, 5000):
+        n = min(5000, rows - i)
+        w[i:i + n] = torch.randn(n, dim, generator=g, device="cuda").mul_(0.02)
+    d = df11.compress_on_device(w)
+    ids = torch.cat([torch.arange(3), torch.arange(32700, 32860), torch.arange(rows - 9, rows)])
+    want = w[ids.cuda()].cpu()
+    del w
+    got = _lookup(d, ids)
+    assert torch.equal(_bits(got), _bits(want))
+    del d
+    torch.cuda.empty_cache()
+
+
+def test_streams_by_object_and_handle():
+    w = _table(300, 256)
+    d = df11.compress_on_device(w.cuda())
+    ids = _ids(64, 300, 1)
+    dev_ids, grad = ids.cuda(), torch.randn(64, 256, generator=torch.Generator().manual_seed(1)).cuda()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream, 0, None):
+        out = df11.decode_embedding(d, dev_ids, stream=stream)
+        dw = df11.embedding_gradient(dev_ids, grad, 300, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(_bits(out.cpu()), _bits(w[ids]))
+        _check_gradient(ids, grad, 300, dw)
+
+
 # ---- gradient -----------------------------------------------------------------
 
 
@@ -215,7 +247,7 @@ def _gradient(ids, grad, rows, **kw):
     return out
 
 
-GRADS = [(1, 1, 1), (1000, 1, 1), (300, 5003, 333), (8192, 200, 64), (4096, 50000, 40),
+GRADS = [(70000, 152000, 8), (2000, 511, 40), (2000, 512, 40), (1025, 262143, 4), (1, 1, 1), (1000, 1, 1), (300, 5003, 333), (8192, 200, 64), (4096, 50000, 40),
          (5000, 3, 130), (33, 1000, 4096), (20000, 151936, 16), (64, 64, 8192), (9000, 300, 24)]
 
 

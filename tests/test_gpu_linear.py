@@ -86,7 +86,8 @@ def _run(ds, xs, **kw):
 
 SIZES = [(16, 64, 1), (1, 1, 1), (37, 131, 3), (1000, 2048, 8), (4096, 4096, 1), (777, 1411, 9),
          (512, 12288, 17), (300, 400, 32), (33, 48, 33), (1013, 1411, 77), (256, 256, 128),
-         (130, 640, 129), (1024, 4096, 300), (520, 64, 1000), (2048, 1024, 24), (4100, 96, 5)]
+         (130, 640, 129), (1024, 4096, 300), (520, 64, 1000), (2048, 1024, 24), (4100, 96, 5),
+         (20000, 64, 2), (40, 20000, 3), (5000, 300, 33), (16, 40000, 20), (530, 260, 32)]
 
 
 @pytest.mark.parametrize("rows,cols,tokens", SIZES)
@@ -443,3 +444,63 @@ def test_long_sums_do_not_drift(tokens):
     want = x.cpu().double() @ w.double().T
     rel = ((y.cpu().double() - want) / want).abs()
     assert float(rel.max()) <= 32 * 2.0 ** -23 + 200 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("tokens", [2, 50])
+def test_activations_of_special_values(tokens):
+    # a weight of one: the products are x itself
+    w = torch.zeros(16, 64, dtype=torch.bfloat16)
+    w[0, 0] = 1.0
+    d = df11.compress_linear(w.cuda())
+    x = torch.zeros(tokens, 64, dtype=torch.bfloat16)
+    x[1, 0] = float("nan")
+    for v in (-3e38, -200.0, 200.0, 3e38):
+        x[0, 0] = v
+        for act, want in (("relu", max(v, 0.0)), ("gelu", max(v, 0.0)), ("gelu_tanh", max(v, 0.0)),
+                          ("silu", max(v, 0.0))):
+            y, = _run([d], [x.cuda()], activations=[act], out_dtype=torch.float32)
+            got = float(y[0, 0])
+            assert got == float(torch.tensor(want).to(torch.bfloat16)), (act, v, got)
+            assert torch.isnan(y[1, 0]), act
+
+
+def test_streams_by_object_and_handle_and_dropped_plans():
+    w = _bf16((512, 768), 0.05, 1)
+    side = torch.cuda.Stream()
+    wc, x = w.cuda(), _bf16((5, 768), 1.0, 2).cuda()
+    torch.cuda.synchronize()
+    c = df11.compress_linear(wc, stream=side)
+    for stream in (side, side.cuda_stream, 0, None):
+        ys = [torch.empty(5, 512, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        for y in ys:      # a plan of its own for each, dropped while it may still run
+            df11.LinearPlan([c], [x], [y]).run(stream=stream)
+            torch.empty(1 << 20, device="cuda").fill_(float("nan"))
+        torch.cuda.synchronize()
+        for y in ys:
+            _check(w, x, y)
+
+
+def test_words_as_activations_and_other_word_types():
+    w = _bf16((64, 128), 0.1, 1)
+    x = _bf16((3, 128), 1.0, 2).cuda()
+    c = df11.compress_linear(w.cuda().view(torch.uint16))
+    y, = _run([c], [x.view(torch.int16)], out_dtype=torch.float32)
+    _check(w, x, y)
+
+
+@pytest.mark.parametrize("tokens", [3, 40])
+def test_a_weight_of_more_than_two_to_the_31_elements(tokens):
+    rows, cols = 45000, 49152
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, rows, 5000):
+        w[i:i + 5000] = torch.randn(5000, cols, generator=g, device="cuda").mul_(cols ** -0.5)
+    c = df11.compress_linear(w)
+    x = _bf16((tokens, cols), 1.0, 2).cuda()
+    y, = _run([c], [x], out_dtype=torch.float32)
+    pick = torch.cat([torch.arange(40), torch.arange(21800, 21860), torch.arange(rows - 40, rows)])
+    _check(w[pick.cuda()], x, y[:, pick.cuda()])
+    assert torch.isfinite(y).all()
+    del w, c
+    torch.cuda.empty_cache()
