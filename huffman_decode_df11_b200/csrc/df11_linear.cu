@@ -3,15 +3,15 @@
 //
 // The weight has a compressed form of its own (df11_linear_weight_begin): like the decode
 // kernels' format a Huffman code of the exponents, with sign and mantissa kept as a byte,
-// but limited to 8-bit codewords and cut by elements instead of bits.  The matrix, padded with zeros
-// to whole tiles of 16 rows and 64 columns, is taken in units of four tiles along a
-// block of 16 rows (the last one may be shorter).  One warp decodes a unit: lane l has a bitstream of its own
-// with the 32 elements of every tile that belong to it, rows l/4 and l/4 + 8 and the 16
-// columns from 16 (l mod 4) on.  Those are the A fragments of four m16n8k16 products,
-// so a decoded weight goes from the table to the tensor core in registers: no
-// chunk counts, scans, shared-memory exponents or exchange between lanes.  The
-// lanes' streams of a unit are stored word by word across the lanes, each padded to the
-// longest of the 32 (about 0.3 bits per weight; chunk counts and gaps cost 0.2).
+// but limited to 8-bit codewords and cut by elements instead of bits.  The matrix, padded
+// with zeros to whole tiles of 16 rows and 64 columns, is taken in units of four tiles
+// along a block of 16 rows (the last one may be shorter).  One warp decodes a unit: lane l
+// has a bitstream of its own with the 32 elements of every tile that belong to it, rows
+// l/4 and l/4 + 8 and the 16 columns from 16 (l mod 4) on.  Those are the A fragments of
+// four m16n8k16 products, so a decoded weight goes from the table to the tensor core in
+// registers: no chunk counts, scans, shared-memory exponents or exchange between lanes.
+// The lanes' streams of a unit are stored word by word across the lanes, each padded to
+// the longest of the 32 (about 0.3 bits per weight; chunk counts and gaps cost 0.2).
 //
 // Two paths, chosen by the number of tokens (see kFusedMax):
 //   few tokens    one kernel decodes the weight and multiplies it from registers; the
@@ -395,6 +395,14 @@ __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, ui
 }
 
 // ---- few tokens: decode and multiply in one kernel ----------------------------------
+//
+// 2 cols operations per weight and token on 1.35 bytes per weight: up to 32 tokens the
+// least time is that of reading the compressed weight.  What bounds the kernel is not the
+// memory but the decoding's chain of four lookups, each waiting for the one before, over
+// the 32 warps that an SM's registers hold: 151936 x 4096 and 8 tokens in 262 us, half of
+// the copy bandwidth (16 warps: 335 us; a table of pairs shared by the lanes, which has
+// half as many lookups but 3.4 wavefronts each: 285 us).  12288 x 4096 and 24 tokens take
+// 49 us, 6144 x 4096 and one token 21 us, of which 4 us are the second kernel and its launch.
 
 struct LTensor {
   LWeight w;
@@ -565,6 +573,8 @@ __global__ void __launch_bounds__(kFinishThreads)
 }
 
 // ---- decoding into tiles --------------------------------------------------------------
+//
+// The same walk with stores in place of products: 4096 x 12288 in 34 us, 3.35 bytes per weight.
 
 struct UArgs {
   LWeight w[DF11_MAX_BATCH];
@@ -749,10 +759,14 @@ __global__ void __launch_bounds__(1024) linear_rows_kernel(uint32_t *unit_rows, 
 // products, eight move finished accumulators (two, in turn) out through the
 // epilogue: a lane is a token, its columns consecutive rows of W, two warps
 // taking groups of 16 in turn.
-//   For fp32 outputs the accumulators are moved out every kPart steps and added in
-// registers (SUMS), because the tensor cores cut off what an addition leaves below their
-// accumulator: at 12288 columns that drifts by 1e-5, which a BF16 output does not
-// show.  Tiles are then at most 128 rows wide.
+//   For fp32 outputs, and for rows longer than kPlainSteps steps, the accumulators are
+// moved out every kPart steps and added in registers (SUMS), because the tensor cores cut
+// off what an addition leaves below their accumulator: at 12288 columns that drifts by
+// 1e-5, which a BF16 output (half a step: 2e-3 to 4e-3) does not show.  Tiles are then at
+// most 128 rows wide.
+//   4096 x 12288 and 2048 tokens take 167 us, 1.23 PFLOP/s, with the clocks that a kernel
+// by itself has; the pipe of the tensor cores bounds it, and the power limit where calls
+// follow one another for seconds.
 constexpr int kGemmTokens = 128;
 constexpr int kEpilogueWarps = 8;  // warps 0-7: epilogue, 8: copies, 9: products
 constexpr int kGemmThreads = (kEpilogueWarps + 2) * 32;
@@ -770,6 +784,7 @@ struct GemmArgs {
 constexpr uint32_t kXBytes = kGemmTokens * 128;
 constexpr uint32_t kPart = 8;      // steps of 64 columns between accumulators (SUMS)
 constexpr uint32_t kSumRows = 128; // rows of a tile whose sums are in registers (SUMS)
+constexpr uint32_t kPlainSteps = 1024;  // without SUMS, for BF16 outputs: 65536 columns
 constexpr uint32_t kMaxStages = 8;
 // barriers: full and empty per stage, two accumulators' full and empty; the tensor-memory
 // address
@@ -1419,7 +1434,7 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
   // and what 32 more would for reading x and emptying the accumulator; the wider one of two
   // (4096 rows and 2048 tokens on 148 SMs: 240 rows, 288 tiles in two rounds)
   uint64_t cost = ~0ull;
-  const bool sums = op.y_type == DF11_F32 && ga.ncg > kPart;
+  const bool sums = ga.ncg > (op.y_type == DF11_F32 ? kPart : kPlainSteps);
   for (uint32_t bn = sums ? kSumRows : 256; bn >= 16; bn -= 16) {
     const uint64_t tiles = (uint64_t)ga.tiles_m * ((rows + bn - 1) / bn);
     const uint64_t c = (tiles + sms - 1) / sms * (bn + 32);

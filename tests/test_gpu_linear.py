@@ -504,3 +504,15 @@ def test_a_weight_of_more_than_two_to_the_31_elements(tokens):
     assert torch.isfinite(y).all()
     del w, c
     torch.cuda.empty_cache()
+
+
+def test_bf16_outputs_of_long_rows():
+    # beyond 65536 columns BF16 outputs too are summed in parts of 512 columns (a part's own
+    # error at most 32 2^-23, the parts' 160 additions half a unit each), then rounded once
+    cols = 80000
+    w = _bf16((48, cols), 0.02, 1).abs()
+    x = _bf16((40, cols), 1.0, 2).abs().cuda()
+    y, = _run([df11.compress_linear(w.cuda())], [x])
+    want = x.cpu().double() @ w.double().T
+    rel = ((y.cpu().double() - want) / want).abs()
+    assert float(rel.max()) <= 2.0 ** -8 + 32 * 2.0 ** -23 + 160 * 2.0 ** -24
