@@ -9,6 +9,11 @@
 // it from the chunk counts, and walks 32 chunks at a time, one per lane, as the
 // decode kernel does.
 //
+// It reads a fraction of the table and writes the rows.  What bounds it is the walk, as
+// in the decode kernels: 8192 rows of 4096 in 44 us, 0.76 weights per ns, where decoding
+// all of a tensor gives 1.35, since a row begins and ends inside a chunk and a warp has to
+// find its place first.  Four rows: 6 us, one pass over the chain of dependent loads.
+//
 // Gradient (df11_embedding_gradient): dW[v] = scale * sum of grad[t] over the
 // tokens t with ids[t] = v.  The tokens are sorted by id (a stable radix sort by one
 // cluster of thread blocks), so a row's tokens are a run of the sorted list.  The
@@ -16,6 +21,9 @@
 // a run that crosses pieces is put together by a second kernel from the pieces'
 // partial sums, in order: nothing depends on scheduling, and a token that
 // half of the batch shares costs no more than any other.
+//   It reads the gradients once and writes the whole table: bound by memory for a large table
+// (151936 x 4096 in BF16 and 32768 tokens: 254 us, 92% of the copy bandwidth), so the
+// zeros are written beside the steps that wait for latency, the sort and the join.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -382,6 +390,10 @@ struct SortShared {
   uint32_t own[kMaxDigits], base[kMaxDigits], warp_total[kMaxDigits / 32];
 };
 
+// Bytes that a thread block of the sort's kernel sets to zero: few enough that clusters
+// which find no place at first do not end late, and more than their start costs.
+constexpr uint64_t kZeroBytes = 256 * 1024;
+
 // Rows zero_from .. rows - 1 set to zero by thread block `block` of `blocks`, 16 bytes at a
 // time where the rows follow one another or start on 16-byte boundaries.
 __device__ void zero_rows(const SortArgs &a, uint32_t block, uint32_t blocks) {
@@ -544,46 +556,34 @@ struct RunArgs {
   void *out;
   const uint32_t *key, *tok;  // sorted
   const uint32_t *touched;    // a bit per row that has tokens
-  uint32_t zero_rows;         // rows below this without one are set to zero here
+  uint32_t zero_rows, zero_step;  // rows below this without one are set to zero, some per thread block
   uint32_t *crossing;         // their number, then the pieces where runs begin that cross pieces
   float *head, *tail;         // per piece: sums of the run that began before it / that goes on
   uint64_t grad_stride, out_stride;
   uint32_t tokens, rows, dim, piece, pieces, col_tiles, part_stride;
+  uint32_t join_blocks;       // thread blocks of the second kernel that put runs together
   uint32_t accumulate;
   float scale;
+  int32_t *err;
+  uint32_t spin_limit;
 };
 
+// V columns of a gradient's row, 16 bytes, or one
 template <typename G, int V>
-struct Row;
-template <>
-struct Row<float, 4> {
-  static __device__ __forceinline__ void load(const float *p, float (&v)[4]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  }
-};
-template <>
-struct Row<uint16_t, 8> {
-  static __device__ __forceinline__ void load(const uint16_t *p, float (&v)[8]) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void add_row(const uint4 &a, float (&acc)[V]) {
+  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = bf16_lo(u[j]);
-      v[2 * j + 1] = bf16_hi(u[j]);
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(G) == 4) {
+      acc[j] += __uint_as_float(u[j]);
+    } else {
+      acc[2 * j] += bf16_lo(u[j]);
+      acc[2 * j + 1] += bf16_hi(u[j]);
     }
   }
-};
-template <>
-struct Row<float, 1> {
-  static __device__ __forceinline__ void load(const float *p, float (&v)[1]) { v[0] = __ldg(p); }
-};
-template <>
-struct Row<uint16_t, 1> {
-  static __device__ __forceinline__ void load(const uint16_t *p, float (&v)[1]) {
-    v[0] = bf16_lo(__ldg(p));
-  }
-};
+}
+__device__ __forceinline__ float load_one(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float load_one(const uint16_t *p) { return bf16_lo(__ldg(p)); }
 
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(uint16_t v) { return bf16_lo(v); }
@@ -610,9 +610,16 @@ __device__ __forceinline__ void write_row(const RunArgs &a, uint32_t row, uint32
       *reinterpret_cast<float4 *>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
   } else {
 #pragma unroll
-    for (int j = 0; j < V; j += 4)
-      *reinterpret_cast<uint2 *>(p + j) =
-          make_uint2(bf16_pair(v[j], v[j + 1]), bf16_pair(v[j + 2], v[j + 3]));
+    for (int j = 0; j < V; j += 4) {
+      const uint2 u = make_uint2(bf16_pair(v[j], v[j + 1]), bf16_pair(v[j + 2], v[j + 3]));
+      if (V % 8 == 0) {
+        if (j % 8) continue;
+        *reinterpret_cast<uint4 *>(p + j) = make_uint4(
+            u.x, u.y, bf16_pair(v[j + 4], v[j + 5]), bf16_pair(v[j + 6], v[j + 7]));
+      } else {
+        *reinterpret_cast<uint2 *>(p + j) = u;
+      }
+    }
   }
 }
 
@@ -627,34 +634,26 @@ __device__ __forceinline__ void write_part(float *p, const float (&s)[V]) {
   }
 }
 
-// Thread blocks below pieces * col_tiles: the runs of one piece of the sorted list,
-// kRunThreads * V columns.  The others: 32 rows each, those without a token set to zero.
+// A thread block: the runs of one piece of the sorted list, kRunThreads * V columns.  The
+// piece's rows are all asked for at once, by bulk copies into shared memory (V > 1), since
+// what bounds this is how much is on its way (32768 tokens of 4096 columns in BF16: 67 us,
+// with four rows ahead in registers 100); kGroup rows have a barrier.
+constexpr uint32_t kGroup = 8;
+constexpr uint32_t kRowBytes = 16 * kRunThreads;
 template <typename G, typename O, int V>
 __global__ void __launch_bounds__(kRunThreads) embedding_runs_kernel(const __grid_constant__ RunArgs a) {
   __shared__ uint32_t key_s[kMaxPiece + 2], tok_s[kMaxPiece];
-  const uint32_t tid = threadIdx.x;
-  pdl_wait();
-  const uint32_t run_blocks = a.pieces * a.col_tiles;
-  if (blockIdx.x >= run_blocks) {
-    const uint32_t word = blockIdx.x - run_blocks;
-    const uint32_t bits = __ldg(a.touched + word);
-    for (uint32_t r = 0; r < 32; ++r) {
-      const uint32_t row = 32u * word + r;
-      if (row >= a.zero_rows) break;
-      if ((bits >> r) & 1u) continue;
-      O *p = static_cast<O *>(a.out) + (size_t)row * a.out_stride;
-      if constexpr (V == 1) {
-        for (uint32_t c = tid; c < a.dim; c += kRunThreads) p[c] = O(0);
-      } else {
-        constexpr uint32_t per = 16 / sizeof(O);  // dim is a multiple of V, and of per
-        for (uint32_t c = tid * per; c < a.dim; c += kRunThreads * per)
-          *reinterpret_cast<uint4 *>(p + c) = make_uint4(0, 0, 0, 0);
-      }
-    }
-    return;
-  }
+  __shared__ uint64_t bar_s[kMaxPiece / kGroup];
+  extern __shared__ __align__(128) uint8_t rows_s[];
+  const uint32_t tid = threadIdx.x, lane = tid & 31;
   const uint32_t piece = blockIdx.x / a.col_tiles, ct = blockIdx.x - piece * a.col_tiles;
   const uint32_t i0 = piece * a.piece, i1 = min(i0 + a.piece, a.tokens), n = i1 - i0;
+  const uint32_t bars = smem_addr(bar_s), rows = smem_addr(rows_s);
+  if (V > 1 && tid == 0) {
+    for (uint32_t i = 0; i < kMaxPiece / kGroup; ++i) mbar_init(bars + 8u * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
   // key_s[0]: the key before the piece, then the piece, then the key after it
   // (no row: beyond every key)
   if (tid < n) {
@@ -664,48 +663,87 @@ __global__ void __launch_bounds__(kRunThreads) embedding_runs_kernel(const __gri
   if (tid == 32) key_s[0] = i0 ? __ldcg(a.key + i0 - 1) : 0xFFFFFFFFu;
   if (tid == 33) key_s[n + 1] = i1 < a.tokens ? __ldcg(a.key + i1) : 0xFFFFFFFFu;
   __syncthreads();
+  const uint32_t col0 = ct * kRunThreads * V;
+  // without the ids outside the table, at the list's end; bit i of `ends`: a run's last token
+  const uint32_t valid = __popc(__ballot_sync(0xFFFFFFFFu, lane < n && key_s[lane + 1] < a.rows));
+  const uint32_t ends =
+      __ballot_sync(0xFFFFFFFFu, lane < n && (lane + 1 == n || key_s[lane + 2] != key_s[lane + 1]));
+  if (V > 1 && tid < valid) {
+    const uint32_t bytes = min((uint32_t)(kRunThreads * V), a.dim - col0) * (uint32_t)sizeof(G);
+    const uint32_t bar = bars + 8u * (tid / kGroup);
+    if (tid % kGroup == 0) mbar_arrive_expect_tx(bar, min(kGroup, valid - tid) * bytes);
+    __syncwarp(valid == 32 ? 0xFFFFFFFFu : (1u << valid) - 1u);
+    bulk_g2s(rows + tid * kRowBytes,
+             static_cast<const G *>(a.grad) + (size_t)tok_s[tid] * a.grad_stride + col0, bytes, bar);
+  }
   // the piece's last run goes on and began here: the next kernel puts it together (in any
   // order, since every run is by itself)
   if (ct == 0 && tid == 0 && key_s[n] < a.rows && key_s[n + 1] == key_s[n] && key_s[0] != key_s[n])
     a.crossing[1 + atomicAdd(a.crossing, 1u)] = piece;
-  const uint32_t col = (ct * kRunThreads + tid) * V;
-  if (col >= a.dim) return;
-  const G *g = static_cast<const G *>(a.grad) + col;
+  const uint32_t col = col0 + tid * V;
+  const bool here = col < a.dim;
   float acc[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) acc[j] = 0.f;
-  uint32_t run = 0;  // where the current run begins in the piece
-  constexpr uint32_t kAhead = 4;
-  for (uint32_t i = 0; i < n; i += kAhead) {
-    float v[kAhead][V];
-#pragma unroll
-    for (uint32_t u = 0; u < kAhead; ++u)
-      if (i + u < n && key_s[i + u + 1] < a.rows)
-        Row<G, V>::load(g + (size_t)tok_s[i + u] * a.grad_stride, v[u]);
-#pragma unroll
-    for (uint32_t u = 0; u < kAhead; ++u) {
-      if (i + u >= n) break;
-      const uint32_t key = key_s[i + u + 1];
-      if (key >= a.rows) break;  // ids outside the table, at the list's end
-#pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] += v[u][j];
-      const bool last = i + u + 1 == n;
-      if (key_s[i + u + 2] == key && !last) continue;
-      const bool before = run == 0 && key_s[0] == key;
-      const bool after = last && key_s[n + 1] == key;
+  bool first = true;  // the current run is the piece's first
+  auto end_run = [&](uint32_t i) {
+    const uint32_t key = key_s[i + 1];
+    const bool before = first && key_s[0] == key, after = key_s[i + 2] == key;
+    if (here) {
       if (!before && !after) write_row<O, V>(a, key, col, acc);
       else write_part<V>((before ? a.head : a.tail) + (size_t)piece * a.part_stride + col, acc);
+    }
 #pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] = 0.f;
-      run = i + u + 1;
+    for (int j = 0; j < V; ++j) acc[j] = 0.f;
+    first = false;
+  };
+  if constexpr (V > 1) {
+    for (uint32_t i = 0; i < valid; i += kGroup) {
+      if (!mbar_wait(bars + 8u * (i / kGroup), 0, a.spin_limit)) {
+        if (tid == 0) {  // the copies may still come: leave once they have, or not
+          report(a.err, DF11_DEV_ERR_TIMEOUT);
+          for (uint32_t g = i; g < valid; g += kGroup) mbar_wait(bars + 8u * (g / kGroup), 0, a.spin_limit);
+        }
+        break;
+      }
+      const uint32_t at = rows + i * kRowBytes + 16u * tid;
+      uint4 v[kGroup];
+#pragma unroll
+      for (uint32_t u = 0; u < kGroup; ++u)
+        if (i + u < valid) v[u] = lds128(at + u * kRowBytes);
+#pragma unroll
+      for (uint32_t u = 0; u < kGroup; ++u) {
+        if (i + u >= valid) break;
+        add_row<G, V>(v[u], acc);
+        if ((ends >> (i + u)) & 1u) end_run(i + u);
+      }
+    }
+  } else {
+    const G *g = static_cast<const G *>(a.grad) + col;
+    constexpr uint32_t kAhead = 4;
+    for (uint32_t i = 0; i < valid; i += kAhead) {
+      float v[kAhead];
+#pragma unroll
+      for (uint32_t u = 0; u < kAhead; ++u)
+        v[u] = here && i + u < valid ? load_one(g + (size_t)tok_s[i + u] * a.grad_stride) : 0.f;
+#pragma unroll
+      for (uint32_t u = 0; u < kAhead; ++u) {
+        if (i + u >= valid) break;
+        acc[0] += v[u];
+        if ((ends >> (i + u)) & 1u) end_run(i + u);
+      }
     }
   }
 }
 
-// A run that crosses pieces: its tail in the piece where it begins and the heads of the
-// pieces after it, 32 V columns per thread block.  Each of the four warps adds every fourth
-// head, and their sums follow the tail in order.
+// Thread blocks below join_blocks: runs that cross pieces.  The tail in the piece where
+// a run begins and the heads of the pieces after it, 32 V columns at a time; each of the four
+// warps adds every fourth head, and their sums follow the tail in order.
+// The others, which write while those wait for their sums: zero_step rows each, those
+// without a token set to zero.
 constexpr uint32_t kJoinWarps = kRunThreads / 32;
+constexpr uint32_t kJoinBlocks = 148 * 12;
+constexpr uint64_t kZeroStep = 16 * 1024;
 template <typename O, int V>
 __global__ void __launch_bounds__(kRunThreads, 12) embedding_join_kernel(const __grid_constant__ RunArgs a) {
   __shared__ uint32_t stop_s[kJoinWarps];
@@ -713,9 +751,27 @@ __global__ void __launch_bounds__(kRunThreads, 12) embedding_join_kernel(const _
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_launch_dependents();
+  if (blockIdx.x >= a.join_blocks) {
+    const uint32_t row0 = (blockIdx.x - a.join_blocks) * a.zero_step;
+    const uint32_t bits = __ldg(a.touched + (row0 >> 5)) >> (row0 & 31u);
+    for (uint32_t r = 0; r < a.zero_step; ++r) {
+      const uint32_t row = row0 + r;
+      if (row >= a.zero_rows) break;
+      if ((bits >> r) & 1u) continue;
+      O *p = static_cast<O *>(a.out) + (size_t)row * a.out_stride;
+      if constexpr (V == 1) {
+        for (uint32_t c = tid; c < a.dim; c += kRunThreads) p[c] = O(0);
+      } else {
+        constexpr uint32_t per = 16 / sizeof(O);  // dim is a multiple of 8
+        for (uint32_t c = tid * per; c < a.dim; c += kRunThreads * per)
+          *reinterpret_cast<uint4 *>(p + c) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    return;
+  }
   const uint32_t tiles = (a.dim + 32 * V - 1) / (32 * V);
   const uint64_t work = (uint64_t)__ldcg(a.crossing) * tiles;
-  for (uint64_t u = blockIdx.x; u < work; u += gridDim.x) {
+  for (uint64_t u = blockIdx.x; u < work; u += a.join_blocks) {
     const uint32_t piece = __ldcg(a.crossing + 1 + u / tiles), tile = (uint32_t)(u % tiles);
     const uint32_t key = __ldcg(a.key + (piece + 1) * a.piece);
     // the run's last piece: the first one after this whose next token has another key; a
@@ -878,16 +934,30 @@ df11_status check_grad(const df11_embedding_grad *op) {
 }
 
 template <typename G, typename O, int V>
-df11_status launch_runs(const RunArgs &a, cudaStream_t s) {
-  const uint32_t blocks = a.pieces * a.col_tiles + (a.zero_rows + 31) / 32;
-  if (blocks == 0) return DF11_OK;
-  df11_status st = launch_pdl(embedding_runs_kernel<G, O, V>, dim3(blocks), kRunThreads, 0, s, a);
-  if (st != DF11_OK || a.pieces < 2) return st;
+df11_status launch_runs(RunArgs a, cudaStream_t s) {
+  if (a.pieces) {
+    const size_t smem = V > 1 ? a.piece * kRowBytes : 0;
+    df11_status st = DF11_OK;
+    if (V > 1) {
+      uint64_t budget = 0;
+      st = prepare(embedding_runs_kernel<G, O, V>, kRunThreads, kMaxPiece * kRowBytes,
+                   82 + 2 * (sizeof(G) / 4) + sizeof(O) / 4, budget);
+      if (st != DF11_OK) return st;
+    }
+    st = launch_pdl(embedding_runs_kernel<G, O, V>, dim3(a.pieces * a.col_tiles), kRunThreads, smem, s, a);
+    if (st != DF11_OK) return st;
+  }
   // four columns per thread at most: more threads on the few rows that many tokens share
   constexpr int J = V == 1 ? 1 : 4;
-  const uint64_t most = (uint64_t)a.pieces * ((a.dim + 32 * J - 1) / (32 * J));
-  return launch_pdl(embedding_join_kernel<O, J>, dim3((uint32_t)(most < 148 * 12 ? most : 148 * 12)),
-                    kRunThreads, 0, s, a);
+  const uint64_t most = a.pieces < 2 ? 0 : (uint64_t)a.pieces * ((a.dim + 32 * J - 1) / (32 * J));
+  a.join_blocks = (uint32_t)(most < kJoinBlocks ? most : kJoinBlocks);
+  // rows per thread block: up to 16 KB, so that all of them write close to one another
+  // (151936 x 4096 in BF16: 254 us, with 64 KB 259, with 256 KB 271)
+  a.zero_step = 32;
+  while (a.zero_step > 1 && (uint64_t)a.zero_step * a.dim * sizeof(O) > kZeroStep) a.zero_step /= 2;
+  const uint32_t blocks = a.join_blocks + (a.zero_rows + a.zero_step - 1) / a.zero_step;
+  if (blocks == 0) return DF11_OK;
+  return launch_pdl(embedding_join_kernel<O, J>, dim3(blocks), kRunThreads, 0, s, a);
 }
 
 template <typename O>
@@ -993,8 +1063,8 @@ df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspa
   st = prepare(embedding_sort_kernel, kSortThreads, sizeof(SortShared), 81, budget);
   if (st != DF11_OK) return st;
   // Rows set to zero beside the sort, as many as it leaves time for: it takes about 10 us, and
-  // 1 us per 1300 tokens, and the other SMs write 4.5 MB per us (measured).  The rest
-  // is set to zero beside the runs, where rows with tokens are left out.
+  // 1 us per 1300 tokens, and the other SMs write 5 MB per us (measured).  The rest is set
+  // to zero beside the join, where rows with tokens are left out.
   uint32_t grid = ctas;
   if (!op->accumulate) {
     so.touched = reinterpret_cast<uint32_t *>(ws + p.touched);
@@ -1002,11 +1072,10 @@ df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspa
     so.out = op->out;
     so.out_stride = op->out_stride * type_bytes(op->out_type);
     so.row_bytes = (uint32_t)(op->dim * type_bytes(op->out_type));
-    uint64_t beside = (10 + op->tokens / 1300) * 4500000ull / so.row_bytes;
+    uint64_t beside = (10 + op->tokens / 1300) * 5000000ull / so.row_bytes;
     if (beside > op->rows) beside = op->rows;
     so.zero_from = (uint32_t)(op->rows - beside);
-    uint64_t blocks = (beside * so.row_bytes + 65535) / 65536;
-    if (blocks > budget) blocks = budget;
+    const uint64_t blocks = (beside * so.row_bytes + kZeroBytes - 1) / kZeroBytes;
     grid += (uint32_t)round_up(blocks, ctas);
   }
   st = launch_cluster(embedding_sort_kernel, grid, ctas, kSortThreads, sizeof(SortShared), s, so);
@@ -1032,6 +1101,8 @@ df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspa
   r.part_stride = p.part_stride;
   r.accumulate = op->accumulate ? 1 : 0;
   r.scale = op->scale;
+  r.err = d_err;
+  r.spin_limit = kSpinLimit;
   const bool gf = op->grad_type == DF11_F32, vec = p.v > 1;
   return op->out_type == DF11_F32 ? launch_runs_for<float>(r, gf, vec, s)
                                   : launch_runs_for<uint16_t>(r, gf, vec, s);

@@ -389,3 +389,29 @@ def test_lookup_linear_and_gradient_together():
     updated = (table.float().cuda() - 1e-3 * dw).to(torch.bfloat16)
     d2 = df11.compress_on_device(updated)
     assert torch.equal(_bits(_lookup(d2, torch.arange(rows))), _bits(updated.cpu()))
+
+
+@pytest.mark.parametrize("rows,dim,tokens", [(20011, 1000, 9000), (3, 16384, 100), (40000, 136, 1)])
+def test_rows_without_tokens_are_zero_in_every_part(rows, dim, tokens):
+    # the table's first and last rows are set to zero beside different steps: ids in all parts,
+    # and gaps between output rows that stay as they were
+    ids = _ids(tokens, rows, 5)
+    ids[0], ids[-1] = rows - 1, 0
+    grad = torch.randn(tokens, dim, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    wide = torch.full((rows, dim + 8), 7.0, device="cuda")
+    df11.embedding_gradient(ids.cuda(), grad, rows, out=wide[:, :dim])
+    _check_gradient(ids, grad, rows, wide[:, :dim])
+    assert bool((wide[:, dim:] == 7.0).all())
+    full = torch.full((rows, dim), 7.0, device="cuda")
+    df11.embedding_gradient(ids.cuda(), grad, rows, out=full)
+    assert torch.equal(full, wide[:, :dim])
+
+
+def test_gradient_rows_that_end_inside_a_tile():
+    # BF16 and fp32 rows of which the last column tile has 8 columns, in pieces of every size
+    for tokens in (1, 7, 8, 9, 33, 600):
+        for dtype in (torch.bfloat16, torch.float32):
+            ids = _ids(tokens, 37, tokens)
+            grad = torch.randn(tokens, 1032, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+            dw = df11.embedding_gradient(ids.cuda(), grad, 37)
+            _check_gradient(ids, grad, 37, dw)
