@@ -119,17 +119,29 @@ __device__ __forceinline__ float activate(float v, uint32_t act) {
   }
 }
 
-__device__ __forceinline__ float finish(const Epilogue &e, float v, uint32_t token, uint32_t row) {
-  if (e.bias) v += load_any(e.bias, row, e.flags & kBiasF32);
-  v = activate(v, e.act);
-  if (e.mul) v *= load_any(e.mul, (size_t)token * e.mul_stride + row, e.flags & kMulF32);
+// An output's operands, and the epilogue on a sum.  The loads stand before what they wait
+// beside.
+struct Operands {
+  float bias = 0.f, mul = 0.f, res = 0.f;
+};
+__device__ __forceinline__ Operands load_operands(const Epilogue &e, uint32_t token, uint32_t row) {
+  Operands o;
+  if (e.bias) o.bias = load_any(e.bias, row, e.flags & kBiasF32);
+  if (e.mul) o.mul = load_any(e.mul, (size_t)token * e.mul_stride + row, e.flags & kMulF32);
   if (e.res) {
     // the residual may be the output itself: a plain load
     const size_t i = (size_t)token * e.res_stride + row;
-    v += e.flags & kResF32
-             ? static_cast<const float *>(e.res)[i]
-             : __uint_as_float((uint32_t)static_cast<const uint16_t *>(e.res)[i] << 16);
+    o.res = e.flags & kResF32
+                ? static_cast<const float *>(e.res)[i]
+                : __uint_as_float((uint32_t)static_cast<const uint16_t *>(e.res)[i] << 16);
   }
+  return o;
+}
+__device__ __forceinline__ float finish(const Epilogue &e, float v, const Operands &o) {
+  if (e.bias) v += o.bias;
+  v = activate(v, e.act);
+  if (e.mul) v *= o.mul;
+  if (e.res) v += o.res;
   return v;
 }
 
@@ -149,15 +161,26 @@ struct PackArgs {
   uint64_t x_stride;
 };
 
-// rows of x into rows of out_cols columns, zeros past the last column
+// rows of x into rows of out_cols columns, zeros past the last column: 256 columns of a row
+// per step of a warp, all loads before the first store
+__device__ __forceinline__ void pack_rows(const PackArgs &a, uint64_t warp, uint64_t warps) {
+  const uint32_t lane = threadIdx.x & 31, segs = (a.out_cols + 255u) / 256u;
+  for (uint64_t i = warp; i < (uint64_t)a.batch * segs; i += warps) {
+    const uint32_t b = (uint32_t)(i / segs), c0 = 256u * (uint32_t)(i - (uint64_t)b * segs) + lane;
+    const uint16_t *x = a.x + b * a.x_stride;
+    uint16_t *out = a.out + (uint64_t)b * a.out_cols;
+    uint16_t v[8];
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) v[j] = c0 + 32u * j < a.cols ? x[c0 + 32u * j] : (uint16_t)0;
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j)
+      if (c0 + 32u * j < a.out_cols) out[c0 + 32u * j] = v[j];
+  }
+}
 __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant__ PackArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  const uint64_t all = (uint64_t)a.batch * a.out_cols;
-  for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < all; i += gridDim.x * 256ull) {
-    const uint32_t b = (uint32_t)(i / a.out_cols), c = (uint32_t)(i - (uint64_t)b * a.out_cols);
-    a.out[i] = c < a.cols ? a.x[b * a.x_stride + c] : (uint16_t)0;
-  }
+  pack_rows(a, (blockIdx.x * 256ull + threadIdx.x) / 32, gridDim.x * 8ull);
 }
 
 // ---- one lane's stream -------------------------------------------------------------
@@ -559,6 +582,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   pdl_wait();
   pdl_launch_dependents();
   if (!here) return;
+  const Operands o = load_operands(ft.e, token, row);
   float sum = __ldcg(p + c0 * stride + slot * fb.warps * per_warp);
   constexpr uint32_t kAhead = 8;  // loads before the first addition
   for (uint32_t c = c0 + 1; c <= c1; c += kAhead) {
@@ -569,7 +593,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     for (uint32_t j = 0; j < kAhead; ++j)
       if (c + j <= c1) sum += v[j];
   }
-  store_any(ft.e, finish(ft.e, sum, token, row), token, row);
+  store_any(ft.e, finish(ft.e, sum, o), token, row);
 }
 
 // ---- decoding into tiles --------------------------------------------------------------
@@ -580,6 +604,7 @@ struct UArgs {
   LWeight w[DF11_MAX_BATCH];
   uint16_t *out[DF11_MAX_BATCH];  // tiles of 16 rows x 64 columns, along the rows
   uint32_t cta_begin[DF11_MAX_BATCH + 1];
+  PackArgs x[DF11_MAX_BATCH];     // activations to pack beside; batch 0: none
   int32_t *err;
   int count;
   uint32_t spin_limit;
@@ -607,13 +632,15 @@ __global__ void __launch_bounds__(32 * W, 1)
   int ti = 0;
   for (int i = 1; i < ua.count; ++i)
     if (blockIdx.x >= ua.cta_begin[i]) ti = i;
-  auto start = [&]() {  // the previous kernel may still read the output
+  auto start = [&]() {  // the previous kernel may still read the output, or write x
     pdl_wait();
     pdl_launch_dependents();
+    for (int i = 0; i < ua.count; ++i)
+      pack_rows(ua.x[i], (uint64_t)blockIdx.x * W + threadIdx.x / 32, (uint64_t)gridDim.x * W);
   };
   decode_units<W>(ua.w[ti], blockIdx.x - ua.cta_begin[ti], ua.cta_begin[ti + 1] - ua.cta_begin[ti],
                   ua.err, ua.spin_limit, smem, start, StoreTile{ua.out[ti], ua.w[ti].ncg, threadIdx.x & 31u},
-               [](uint32_t) {});
+                  [](uint32_t) {});
 }
 
 // ---- building the compressed form --------------------------------------------------------
@@ -756,19 +783,21 @@ __global__ void __launch_bounds__(1024) linear_rows_kernel(uint32_t *unit_rows, 
 // caller's rows), B the decoded tiles (bn rows; a 16 x 64 tile is 16 rows of 128
 // bytes, so a TMA box of bn/16 row blocks is bn rows of 64 columns), both in the
 // 128-byte swizzle, K in steps of 64.  One warp issues the copies, one the
-// products, eight move finished accumulators (two, in turn) out through the
-// epilogue: a lane is a token, its columns consecutive rows of W, two warps
-// taking groups of 16 in turn.
+// products, twelve move finished accumulators (two, in turn) out through the
+// epilogue: a lane is a token, its columns consecutive rows of W, three warps
+// taking groups of 16 in turn (with eight warps the epilogue takes longer than the product
+// of 4096 columns where an activation is in it).
 //   For fp32 outputs, and for rows longer than kPlainSteps steps, the accumulators are
 // moved out every kPart steps and added in registers (SUMS), because the tensor cores cut
 // off what an addition leaves below their accumulator: at 12288 columns that drifts by
 // 1e-5, which a BF16 output (half a step: 2e-3 to 4e-3) does not show.  Tiles are then at
-// most 128 rows wide.
-//   4096 x 12288 and 2048 tokens take 167 us, 1.23 PFLOP/s, with the clocks that a kernel
-// by itself has; the pipe of the tensor cores bounds it, and the power limit where calls
-// follow one another for seconds.
+// most 144 rows wide.
+//   4096 x 12288 and 2048 tokens take 150 us, 1.37 PFLOP/s, and 12288 x 4096 144 us, 1.43,
+// with the clocks that a kernel by itself has; the copies of the next stages bound it (four
+// of 240 rows fit), and the power limit where calls follow one another for seconds.
 constexpr int kGemmTokens = 128;
-constexpr int kEpilogueWarps = 8;  // warps 0-7: epilogue, 8: copies, 9: products
+constexpr int kEpilogueWarps = 12;  // then a warp for the copies and one for the products
+constexpr uint32_t kColStep = 4 * kEpilogueWarps;  // columns from one group of 16 of a warp to its next
 constexpr int kGemmThreads = (kEpilogueWarps + 2) * 32;
 
 struct GemmArgs {
@@ -776,6 +805,7 @@ struct GemmArgs {
   uint32_t tokens, rows, ncg;         // ncg: 64-column steps
   uint32_t bn, stages, tmem_cols;     // rows of W per tile, stages of shared memory
   uint32_t tiles_m, tiles;            // token tiles, all tiles
+  uint32_t x_bytes;                   // of x per stage: the rows that a tile of tokens has at most
   uint32_t vec;                       // rows of y, multiplier and residual take 16-byte accesses
   int32_t *err;
   uint32_t spin_limit;
@@ -783,30 +813,68 @@ struct GemmArgs {
 
 constexpr uint32_t kXBytes = kGemmTokens * 128;
 constexpr uint32_t kPart = 8;      // steps of 64 columns between accumulators (SUMS)
-constexpr uint32_t kSumRows = 128; // rows of a tile whose sums are in registers (SUMS)
+constexpr uint32_t kSumRows = 144; // rows of a tile whose sums are in registers (SUMS)
 constexpr uint32_t kPlainSteps = 1024;  // without SUMS, for BF16 outputs: 65536 columns
 constexpr uint32_t kMaxStages = 8;
+// an epilogue warp's buffer of 32 tokens and 16 rows: 16 bytes more per token, so that no
+// two accesses meet in a bank
+constexpr uint32_t kBufRow = 80, kBufBytes = 32 * kBufRow;
 // barriers: full and empty per stage, two accumulators' full and empty; the tensor-memory
 // address
 constexpr uint32_t kGemmTail = 8 * (2 * kMaxStages + 4) + 16;
-constexpr uint32_t gemm_smem(uint32_t bn, uint32_t stages) {
-  return 1024 + stages * (kXBytes + bn * 128) + kGemmTail;
+static_assert(kGemmTail % 16 == 0, "the epilogue's buffers stand behind");
+constexpr uint32_t gemm_smem(uint32_t bn, uint32_t stages, bool buffers) {
+  return 1024 + stages * (kXBytes + bn * 128) + kGemmTail + (buffers ? kEpilogueWarps * kBufBytes : 0);
 }
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                            uint32_t bar) {
+// The warps that issue copies and products run their loops as whole warps, and one elected lane
+// issues, by a predicate: operands that are known to be the same in every lane come from
+// uniform registers, where a branch for one lane moves each of them there anew (4096 x 4096
+// and 40 tokens: 17 us for the product, with branches 29 us).
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void expect_tx(uint32_t elected, uint32_t bar, uint32_t bytes) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-      "[%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+      " @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
+      "r"(bytes), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                            int z, int w, uint32_t bar) {
+__device__ __forceinline__ void tma_load_2d(uint32_t elected, uint32_t dst, const CUtensorMap *map,
+                                            int x, int y, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-      "%4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
+      " @q cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];\n}\n" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t elected, uint32_t dst, const CUtensorMap *map,
+                                            int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %7, 0;\n"
+      " @q cp.async.bulk.tensor.4d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4, %5}], [%6];\n}\n" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void umma(uint32_t elected, uint32_t d, uint64_t a, uint64_t b,
+                                     uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(elected)
       : "memory");
 }
 
@@ -816,20 +884,9 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
          (2ull << 61);
 }
 
-// `n` (at most 16) consecutive rows of one token, all loads before their first use: 16 bytes
-// at a time where whole and aligned
-template <bool VEC>
-__device__ __forceinline__ void load16(const void *p, size_t i, bool f32, uint32_t n,
-                                       float (&v)[16]) {
-  if (!VEC) {
-#pragma unroll
-    for (uint32_t j = 0; j < 16; ++j) {
-      v[j] = 0.f;
-      if (j < n)
-        v[j] = f32 ? static_cast<const float *>(p)[i + j]
-                   : __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i + j] << 16);
-    }
-  } else if (f32) {
+// The epilogue of a lane's token and 16 rows, 16 bytes at a time, its operands asked for first.
+__device__ __forceinline__ void load16(const void *p, size_t i, bool f32, float (&v)[16]) {
+  if (f32) {
     const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -850,17 +907,14 @@ __device__ __forceinline__ void load16(const void *p, size_t i, bool f32, uint32
     }
   }
 }
-
-template <bool VEC>
-__device__ __forceinline__ void finish16(const Epilogue &e, float (&v)[16], uint32_t token,
-                                         uint32_t row, uint32_t n) {
+__device__ __forceinline__ void epilogue16(const Epilogue &e, float (&v)[16], uint32_t token,
+                                           uint32_t row) {
   float m[16], r[16];
-  if (e.mul) load16<VEC>(e.mul, (size_t)token * e.mul_stride + row, e.flags & kMulF32, n, m);
-  if (e.res) load16<VEC>(e.res, (size_t)token * e.res_stride + row, e.flags & kResF32, n, r);
+  if (e.mul) load16(e.mul, (size_t)token * e.mul_stride + row, e.flags & kMulF32, m);
+  if (e.res) load16(e.res, (size_t)token * e.res_stride + row, e.flags & kResF32, r);
   if (e.bias) {
 #pragma unroll
-    for (uint32_t j = 0; j < 16; ++j)
-      if (VEC || j < n) v[j] += load_any(e.bias, row + j, e.flags & kBiasF32);
+    for (uint32_t j = 0; j < 16; ++j) v[j] += load_any(e.bias, row + j, e.flags & kBiasF32);
   }
   if (e.act != DF11_ACT_NONE) {
 #pragma unroll
@@ -875,11 +929,7 @@ __device__ __forceinline__ void finish16(const Epilogue &e, float (&v)[16], uint
     for (int j = 0; j < 16; ++j) v[j] += r[j];
   }
   const size_t i = (size_t)token * e.y_stride + row;
-  if (!VEC) {
-#pragma unroll
-    for (uint32_t j = 0; j < 16; ++j)
-      if (j < n) store_any(e, v[j], token, row + j);
-  } else if (e.flags & kOutF32) {
+  if (e.flags & kOutF32) {
     float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(e.y) + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -891,6 +941,88 @@ __device__ __forceinline__ void finish16(const Epilogue &e, float (&v)[16], uint
       q[j] = make_uint4(bf16_pair(v[8 * j], v[8 * j + 1]), bf16_pair(v[8 * j + 2], v[8 * j + 3]),
                         bf16_pair(v[8 * j + 4], v[8 * j + 5]), bf16_pair(v[8 * j + 6], v[8 * j + 7]));
   }
+}
+
+// The epilogue where rows are not on 16-byte boundaries or end early, and where sums take the
+// registers: 32 tokens and 16 rows, which lie in the warp's buffer, so that the lanes'
+// accesses are next to one another.  A lane
+// has four consecutive rows of every eighth token (4099 x 4096 and 1024 tokens with multiplier
+// and residual: 108 us; a token per lane, one value at a time: 186 us).
+__device__ __forceinline__ void sts128(uint32_t a, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w)
+               : "memory");
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  const uint4 v = lds128(a);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                     __uint_as_float(v.w));
+}
+
+// `n` (0 to 4) consecutive values of a row, one access where `vec`
+__device__ __forceinline__ float4 load4(const void *p, size_t i, bool f32, bool vec, uint32_t n) {
+  if (vec) {
+    if (f32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+  }
+  float v[4];
+#pragma unroll
+  for (uint32_t j = 0; j < 4; ++j) {
+    v[j] = 0.f;
+    if (j < n)
+      v[j] = f32 ? static_cast<const float *>(p)[i + j]
+                 : __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i + j] << 16);
+  }
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ void epilogue_block(const Epilogue &e, uint32_t buf, uint32_t token0,
+                                               uint32_t row0, uint32_t tokens, uint32_t rows,
+                                               bool vec) {
+  const uint32_t lane = threadIdx.x & 31, row = row0 + 4u * (lane & 3u);
+  const uint32_t n = row < rows ? min(rows - row, 4u) : 0u;
+  const uint32_t at = buf + (lane >> 2) * kBufRow + 16u * (lane & 3u);
+  vec = vec && n == 4;
+  __syncwarp();  // the buffer is written
+  float4 m[4], r[4], b = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k) {
+    const uint32_t token = token0 + 8u * k + (lane >> 2);
+    m[k] = r[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n && token < tokens) {
+      if (e.mul) m[k] = load4(e.mul, (size_t)token * e.mul_stride + row, e.flags & kMulF32, vec, n);
+      if (e.res) r[k] = load4(e.res, (size_t)token * e.res_stride + row, e.flags & kResF32, vec, n);
+    }
+  }
+  if (e.bias && n) b = load4(e.bias, row, e.flags & kBiasF32, false, n);
+  if (e.act != DF11_ACT_NONE) {
+#pragma unroll 1
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint32_t p = at + 8u * k * kBufRow;
+      const float4 v = lds_f4(p);
+      sts128(p, activate(v.x + b.x, e.act), activate(v.y + b.y, e.act), activate(v.z + b.z, e.act),
+             activate(v.w + b.w, e.act));
+    }
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k) {
+    const uint32_t token = token0 + 8u * k + (lane >> 2);
+    if (n == 0 || token >= tokens) continue;
+    float4 v = lds_f4(at + 8u * k * kBufRow);
+    if (e.bias && e.act == DF11_ACT_NONE) v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
+    if (e.mul) v.x *= m[k].x, v.y *= m[k].y, v.z *= m[k].z, v.w *= m[k].w;
+    if (e.res) v.x += r[k].x, v.y += r[k].y, v.z += r[k].z, v.w += r[k].w;
+    if (vec && (e.flags & kOutF32)) {
+      *reinterpret_cast<float4 *>(static_cast<float *>(e.y) + (size_t)token * e.y_stride + row) = v;
+      continue;
+    }
+    store_any(e, v.x, token, row);
+    if (n > 1) store_any(e, v.y, token, row + 1);
+    if (n > 2) store_any(e, v.z, token, row + 2);
+    if (n > 3) store_any(e, v.w, token, row + 3);
+  }
+  __syncwarp();  // the buffer may be written again
 }
 
 template <bool SUMS>
@@ -934,36 +1066,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   bool failed = false;
 
   if (warp == kEpilogueWarps) {
-    if (lane == 0) {
-      uint32_t k = 0, s = 0, par = 0;  // copies so far; the stage, and its uses' parity
-      for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
-        const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m;
-        for (uint32_t c = 0; c < ga.ncg; ++c, ++k) {
-          if (!mbar_wait(empty(s), par ^ 1u, ga.spin_limit)) {
-            failed = true;
-            break;
-          }
-          mbar_arrive_expect_tx(full(s), stage_bytes);
-          tma_load_2d(base + s * stage_bytes, &map_x, (int)(64u * c), (int)(tm * kGemmTokens),
-                      full(s));
-          tma_load_4d(base + s * stage_bytes + kXBytes, &map_w, 0, 0, (int)c,
-                      (int)(tn * (bn / 16)), full(s));
-          if (++s == S) {
-            s = 0;
-            par ^= 1u;
-          }
+    const uint32_t elected = elect();
+    uint32_t k = 0, s = 0, par = 0;  // copies so far; the stage, and its uses' parity
+    for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
+      const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m;
+      for (uint32_t c = 0; c < ga.ncg; ++c, ++k) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty(s), par ^ 1u, ga.spin_limit))) {
+          failed = true;
+          break;
+        }
+        const uint32_t dst = base + s * stage_bytes;
+        expect_tx(elected, full(s), ga.x_bytes + bn * 128u);
+        tma_load_2d(elected, dst, &map_x, (int)(64u * c), (int)(tm * kGemmTokens), full(s));
+        tma_load_4d(elected, dst + kXBytes, &map_w, 0, 0, (int)c, (int)(tn * (bn / 16)), full(s));
+        if (++s == S) {
+          s = 0;
+          par ^= 1u;
         }
       }
-      pdl_launch_dependents();
-      // no copy in flight into this thread block's shared memory when it ends
-      for (uint32_t j = k > S ? k - S : 0; j < k; ++j)
-        if (!mbar_wait(full(j % S), (j / S) & 1u, ga.spin_limit)) failed = true;
-      if (failed) report(ga.err, DF11_DEV_ERR_TIMEOUT);
     }
+    pdl_launch_dependents();
+    // no copy in flight into this thread block's shared memory when it ends
+    for (uint32_t j = k > S ? k - S : 0; j < k; ++j)
+      if (!mbar_wait(full(j % S), (j / S) & 1u, ga.spin_limit)) failed = true;
+    if (failed && lane == 0) report(ga.err, DF11_DEV_ERR_TIMEOUT);
   } else if (warp == kEpilogueWarps + 1) {
     // fp32 accumulators, BF16 operands, both K-major
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((bn / 8) << 17) |
                            ((kGemmTokens / 16) << 24);
+    const uint32_t elected = elect();
     uint32_t k = 0, n = 0, s = 0, par = 0;
     for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
       uint32_t d = 0;
@@ -984,29 +1115,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           break;
         }
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t ad = sw128_desc(base + s * stage_bytes);
-          const uint64_t bd = sw128_desc(base + s * stage_bytes + kXBytes);
+        const uint64_t ad = sw128_desc(base + s * stage_bytes);
+        const uint64_t bd = sw128_desc(base + s * stage_bytes + kXBytes);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // K = 16: 32 bytes on
-            const uint32_t add = !first || j ? 1u : 0u;
-            asm volatile(
-                "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-                "l"(ad + 2u * j), "l"(bd + 2u * j), "r"(idesc), "r"(add)
-                : "memory");
-          }
-          asm volatile(
-              "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                  empty(s))
-              : "memory");
-          if (last)
-            asm volatile(
-                "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                    acc_full(n & 1))
-                : "memory");
-        }
-        __syncwarp();
+        for (int j = 0; j < 4; ++j)  // K = 16: 32 bytes on
+          umma(elected, d, ad + 2u * j, bd + 2u * j, idesc, !first || j ? 1u : 0u);
+        umma_commit(elected, empty(s));
+        if (last) umma_commit(elected, acc_full(n & 1));
         if (last) ++n;
         if (++s == S) {
           s = 0;
@@ -1037,10 +1152,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(u[j]);
     };
-    auto write16 = [&](float (&v)[16], uint32_t token, uint32_t row) {
-      if (token >= ga.tokens || row >= ga.rows) return;
-      if (ga.vec && row + 16 <= ga.rows) finish16<true>(ga.e, v, token, row, 16u);
-      else finish16<false>(ga.e, v, token, row, min(ga.rows - row, 16u));
+    const uint32_t buf = bars + kGemmTail + kBufBytes * warp;
+    // the epilogue of the warp's 32 tokens and 16 rows, some of them there
+    auto write16 = [&](float (&v)[16], uint32_t token0, uint32_t row) {
+      if (!SUMS && ga.vec && row + 16 <= ga.rows) {
+        if (token0 + lane < ga.tokens) epilogue16(ga.e, v, token0 + lane, row);
+        return;
+      }
+      const uint32_t p = buf + lane * kBufRow;
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j)
+        sts128(p + 16u * j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      epilogue_block(ga.e, buf, token0, row, ga.tokens, ga.rows, SUMS && ga.vec);
     };
     auto acquire = [&]() {
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full(n & 1), (n >> 1) & 1u, ga.spin_limit)))
@@ -1056,32 +1179,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     };
     for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
       const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m;
-      const uint32_t token = tm * kGemmTokens + 32u * quarter + lane;
+      const uint32_t token0 = tm * kGemmTokens + 32u * quarter;
+      const bool some = token0 < ga.tokens;
       if constexpr (SUMS) {
-        float sum[kSumRows / 32][16];
+        float sum[kSumRows / kColStep][16];
         for (uint32_t c0 = 0; c0 < ga.ncg; c0 += kPart) {
           if (!acquire()) break;
 #pragma unroll
-          for (uint32_t g = 0; g < kSumRows / 32; ++g) {
-            if (32u * g + half >= bn) break;
+          for (uint32_t g = 0; g < kSumRows / kColStep; ++g) {
+            if (kColStep * g + half >= bn) break;
             float v[16];
-            read16(lanes + (n & 1u) * bn + 32u * g + half, v);
+            read16(lanes + (n & 1u) * bn + kColStep * g + half, v);
 #pragma unroll
             for (int j = 0; j < 16; ++j) sum[g][j] = c0 ? sum[g][j] + v[j] : v[j];
           }
           release();
         }
         if (failed) break;
+#pragma unroll 1  // one copy of the epilogue
+        for (uint32_t g = 0; some && kColStep * g + half < bn; ++g) {
+          if (tn * bn + kColStep * g + half >= ga.rows) break;
+          float v[16];
 #pragma unroll
-        for (uint32_t g = 0; g < kSumRows / 32; ++g)
-          if (32u * g + half < bn) write16(sum[g], token, tn * bn + 32u * g + half);
+          for (uint32_t k = 0; k < kSumRows / kColStep; ++k)
+            if (k == g) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = sum[k][j];
+            }
+          write16(v, token0, tn * bn + kColStep * g + half);
+        }
       } else {
         if (!acquire()) break;
-        for (uint32_t c = half; c < bn && tn * bn + c < ga.rows; c += 32) {
+        for (uint32_t c = half; c < bn && tn * bn + c < ga.rows; c += kColStep) {
           float v[16];
           read16(lanes + (n & 1u) * bn + c, v);
-          write16(v, token, tn * bn + c);
-          __syncwarp();
+          if (some) write16(v, token0, tn * bn + c);
         }
         release();
       }
@@ -1101,7 +1233,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // ---- host side ------------------------------------------------------------------
 
 // Tokens up to which a call decodes and multiplies in one kernel (12288 x 4096: 48 us for
-// 24 tokens; decoded first, 67 us for 64 and 63 us for 33).
+// 24 tokens; decoded first, the decoding takes 34 us and the product 18).
 constexpr uint32_t kFusedMax = 32;
 
 uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
@@ -1367,9 +1499,9 @@ df11_status launch_fused(const df11_linear_weight *ws, const df11_linear *ops, i
   return launch_pdl(df11_linear_finish_kernel, dim3(blocks), kFinishThreads, 0, s, fb);
 }
 
-// the weights decoded into tiles, one launch
+// the weights decoded into tiles and activations packed, one launch
 df11_status launch_unpack(const df11_linear_weight *ws, int count, uint16_t *const *out,
-                          int32_t *d_err, cudaStream_t s) {
+                          const PackArgs *x, int32_t *d_err, cudaStream_t s) {
   UArgs ua{};
   const uint32_t words = longest_stream(ws, count), warps = warps_for(words);
   const size_t smem = decode_smem(words, warps);
@@ -1386,6 +1518,7 @@ df11_status launch_unpack(const df11_linear_weight *ws, int count, uint16_t *con
   for (int i = 0; i < count; ++i) {
     ua.w[i] = device_weight(ws[i]);
     ua.out[i] = out[i];
+    if (x) ua.x[i] = x[i];
     ua.cta_begin[i + 1] = ua.cta_begin[i] + (uint32_t)ctas[i];
   }
   return launch_pdl(kern, dim3(ua.cta_begin[count]), 32 * warps, smem, s, ua);
@@ -1445,13 +1578,18 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
     }
   }
   ga.stages = kMaxStages;
-  while (gemm_smem(ga.bn, ga.stages) > 200 * 1024) --ga.stages;
+  const bool buffers = sums || !ga.vec || rows % 16;
+  while (gemm_smem(ga.bn, ga.stages, buffers) > 226 * 1024) --ga.stages;
   ga.tmem_cols = 32;
   while (ga.tmem_cols < 2 * ga.bn) ga.tmem_cols *= 2;
   CUtensorMap mx, mw;
   {
     const cuuint64_t dims[2] = {x.cols, op.batch}, strides[1] = {2ull * x.stride};
-    const cuuint32_t box[2] = {64, kGemmTokens}, one[2] = {1, 1};
+    // up to 128 tokens: only the rows that there are.  The others of the tile are whatever the
+    // shared memory holds, and so are the accumulators' lanes of theirs, which nothing reads
+    const uint32_t box_rows = op.batch < kGemmTokens ? (op.batch + 7u) / 8u * 8u : kGemmTokens;
+    const cuuint32_t box[2] = {64, box_rows}, one[2] = {1, 1};
+    ga.x_bytes = box_rows * 128u;
     if (encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(x.x), dims, strides,
                box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
@@ -1468,7 +1606,7 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
         CUDA_SUCCESS)
       return DF11_ERR_CUDA;
   }
-  const size_t smem = gemm_smem(ga.bn, ga.stages);
+  const size_t smem = gemm_smem(ga.bn, ga.stages, buffers);
   uint64_t budget = 0;
   void (*kern)(CUtensorMap, CUtensorMap, GemmArgs) =
       sums ? df11_linear_gemm_kernel<true> : df11_linear_gemm_kernel<false>;
@@ -1614,7 +1752,7 @@ df11_status df11_linear_unpack(const df11_linear_weight *weight, uint16_t *tiles
   const void *ptrs[] = {tiles, weight->streams, weight->unit_rows, weight->sign_mantissa, weight->table};
   st = check_device_pointers(ptrs, 5);
   if (st != DF11_OK) return st;
-  return launch_unpack(weight, 1, &tiles, d_err, (cudaStream_t)stream);
+  return launch_unpack(weight, 1, &tiles, nullptr, d_err, (cudaStream_t)stream);
 }
 
 df11_status df11_linear_workspace(const df11_linear_weight *weights, const df11_linear *ops,
@@ -1658,11 +1796,12 @@ df11_status df11_decode_linear(const df11_linear_weight *weights, const df11_lin
     if (r != DF11_OK) return r;
     uint8_t *work = static_cast<uint8_t *>(workspace);
     Activations x[DF11_MAX_BATCH];
+    PackArgs packs[DF11_MAX_BATCH] = {};
     for (int i = 0; i < m; ++i) {
       const uint32_t cols = w[i].params.cols;
       x[i] = Activations{o[i].x, o[i].x_stride, cols};
       if (!needs_pack(o[i], cols)) continue;
-      PackArgs pa{};
+      PackArgs &pa = packs[i];
       pa.x = o[i].x;
       pa.out = reinterpret_cast<uint16_t *>(work + pl.packed[i]);
       pa.cols = cols;
@@ -1670,14 +1809,15 @@ df11_status df11_decode_linear(const df11_linear_weight *weights, const df11_lin
       pa.batch = o[i].batch;
       pa.x_stride = o[i].x_stride;
       x[i] = Activations{pa.out, pa.out_cols, pa.out_cols};
-      const uint64_t blocks = ((uint64_t)pa.batch * pa.out_cols + 255) / 256;
+      if (!pl.fused) continue;  // beside the decoding
+      const uint64_t blocks = ((uint64_t)pa.batch * ((pa.out_cols + 255) / 256) + 7) / 8;
       r = launch_pdl(linear_pack_kernel, dim3((uint32_t)(blocks < 592 ? blocks : 592)), 256, 0, s, pa);
       if (r != DF11_OK) return r;
     }
     if (pl.fused) return launch_fused(w, o, m, pl, work, x, d_err, s);
     uint16_t *tiles[DF11_MAX_BATCH];
     for (int i = 0; i < m; ++i) tiles[i] = reinterpret_cast<uint16_t *>(work + pl.part[i]);
-    r = launch_unpack(w, m, tiles, d_err, s);
+    r = launch_unpack(w, m, tiles, packs, d_err, s);
     for (int i = 0; i < m && r == DF11_OK; ++i)
       r = launch_gemm(o[i], w[i].params.rows, w[i].params.cols, tiles[i], x[i], d_err, s);
     return r;
