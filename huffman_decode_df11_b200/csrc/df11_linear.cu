@@ -958,6 +958,18 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
                      __uint_as_float(v.w));
 }
 
+// four values in another thread block's shared memory
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n"
+      " ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
 // `n` (0 to 4) consecutive values of a row, one access where `vec`
 __device__ __forceinline__ float4 load4(const void *p, size_t i, bool f32, bool vec, uint32_t n) {
   if (vec) {
@@ -1025,7 +1037,10 @@ __device__ __forceinline__ void epilogue_block(const Epilogue &e, uint32_t buf, 
   __syncwarp();  // the buffer may be written again
 }
 
-template <bool SUMS>
+// SPLIT: a cluster of thread blocks shares a tile, each with a part of the columns of x; the
+// parts' sums meet in shared memory, and each thread block adds a share of the tile's rows
+// of W over the cluster, in order, for the epilogue.
+template <bool SUMS, bool SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     df11_linear_gemm_kernel(const __grid_constant__ CUtensorMap map_x,
                             const __grid_constant__ CUtensorMap map_w,
@@ -1064,13 +1079,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t tmem = lds32(taddr_s);
   pdl_wait();  // the decoded weight, and x, come from the kernels before
   bool failed = false;
+  // the tiles of this thread block and its steps of 64 columns: asked for where they are used,
+  // so that they stay in uniform registers
+  auto first_tile = [&]() { return SPLIT ? blockIdx.x / cluster_size() : blockIdx.x; };
+  auto tile_step = [&]() { return SPLIT ? ga.tiles : gridDim.x; };
+  auto col_begin = [&]() { return SPLIT ? ga.ncg * cluster_rank() / cluster_size() : 0u; };
+  auto col_end = [&]() { return SPLIT ? ga.ncg * (cluster_rank() + 1) / cluster_size() : ga.ncg; };
 
   if (warp == kEpilogueWarps) {
     const uint32_t elected = elect();
     uint32_t k = 0, s = 0, par = 0;  // copies so far; the stage, and its uses' parity
-    for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
+    for (uint32_t tile = first_tile(); tile < ga.tiles && !failed; tile += tile_step()) {
       const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m;
-      for (uint32_t c = 0; c < ga.ncg; ++c, ++k) {
+      for (uint32_t c = col_begin(); c < col_end(); ++c, ++k) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty(s), par ^ 1u, ga.spin_limit))) {
           failed = true;
           break;
@@ -1096,11 +1117,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                            ((kGemmTokens / 16) << 24);
     const uint32_t elected = elect();
     uint32_t k = 0, n = 0, s = 0, par = 0;
-    for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
+    for (uint32_t tile = first_tile(); tile < ga.tiles && !failed; tile += tile_step()) {
       uint32_t d = 0;
-      for (uint32_t c = 0; c < ga.ncg; ++c, ++k) {
-        const bool first = SUMS ? c % kPart == 0 : c == 0;  // into the other accumulator
-        const bool last = c + 1 == ga.ncg || (SUMS && (c + 1) % kPart == 0);
+      for (uint32_t c = col_begin(); c < col_end(); ++c, ++k) {
+        const uint32_t cb = col_begin(), ce = col_end();
+        const bool first = SUMS ? (c - cb) % kPart == 0 : c == cb;  // into the other accumulator
+        const bool last = c + 1 == ce || (SUMS && (c + 1 - cb) % kPart == 0);
         if (first) {
           if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_empty(n & 1), ((n >> 1) & 1u) ^ 1u,
                                                   ga.spin_limit))) {
@@ -1177,13 +1199,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (lane == 0) mbar_arrive(acc_empty(n & 1));
       ++n;
     };
-    for (uint32_t tile = blockIdx.x; tile < ga.tiles && !failed; tile += gridDim.x) {
+    for (uint32_t tile = first_tile(); tile < ga.tiles && !failed; tile += tile_step()) {
       const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m;
       const uint32_t token0 = tm * kGemmTokens + 32u * quarter;
       const bool some = token0 < ga.tokens;
       if constexpr (SUMS) {
         float sum[kSumRows / kColStep][16];
-        for (uint32_t c0 = 0; c0 < ga.ncg; c0 += kPart) {
+        const uint32_t cb = col_begin();
+        for (uint32_t c0 = cb; c0 < col_end(); c0 += kPart) {
           if (!acquire()) break;
 #pragma unroll
           for (uint32_t g = 0; g < kSumRows / kColStep; ++g) {
@@ -1191,22 +1214,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             float v[16];
             read16(lanes + (n & 1u) * bn + kColStep * g + half, v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum[g][j] = c0 ? sum[g][j] + v[j] : v[j];
+            for (int j = 0; j < 16; ++j) sum[g][j] = c0 > cb ? sum[g][j] + v[j] : v[j];
           }
           release();
         }
         if (failed) break;
+        if constexpr (SPLIT) {
+          // every product is done, so the stages' memory is free: [token][row], 4 rows more
+#pragma unroll
+          for (uint32_t g = 0; g < kSumRows / kColStep; ++g) {
+            if (kColStep * g + half >= bn) break;
+            const uint32_t p = base + 4u * ((32u * quarter + lane) * (bn + 4u) + kColStep * g + half);
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+              sts128(p + 16u * j, sum[g][4 * j], sum[g][4 * j + 1], sum[g][4 * j + 2], sum[g][4 * j + 3]);
+          }
+        } else {
 #pragma unroll 1  // one copy of the epilogue
-        for (uint32_t g = 0; some && kColStep * g + half < bn; ++g) {
-          if (tn * bn + kColStep * g + half >= ga.rows) break;
-          float v[16];
+          for (uint32_t g = 0; some && kColStep * g + half < bn; ++g) {
+            if (tn * bn + kColStep * g + half >= ga.rows) break;
+            float v[16];
 #pragma unroll
-          for (uint32_t k = 0; k < kSumRows / kColStep; ++k)
-            if (k == g) {
+            for (uint32_t k = 0; k < kSumRows / kColStep; ++k)
+              if (k == g) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = sum[k][j];
-            }
-          write16(v, token0, tn * bn + kColStep * g + half);
+                for (int j = 0; j < 16; ++j) v[j] = sum[k][j];
+              }
+            write16(v, token0, tn * bn + kColStep * g + half);
+          }
         }
       } else {
         if (!acquire()) break;
@@ -1219,6 +1254,36 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
     }
     if (failed && lane == 0) report(ga.err, DF11_DEV_ERR_TIMEOUT);
+  }
+  if constexpr (SPLIT) {
+    cluster_sync();
+    if (warp < kEpilogueWarps) {
+      const uint32_t buf = bars + kGemmTail + kBufBytes * warp;
+      const uint32_t ctas = cluster_size(), rank = cluster_rank(), tile = first_tile();
+      const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m, share = bn / ctas;
+      for (uint32_t b = warp; b < 4u * (share / 16u); b += kEpilogueWarps) {
+        const uint32_t t0 = 32u * (b & 3u), c0 = rank * share + 16u * (b >> 2);
+        if (tm * kGemmTokens + t0 >= ga.tokens || tn * bn + c0 >= ga.rows) continue;
+        const uint32_t p = base + 4u * ((t0 + (lane >> 2)) * (bn + 4u) + c0 + 4u * (lane & 3u));
+        float4 sum[4];
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint32_t r = 0; r < ctas; ++r) {
+          float4 v[4];
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k) v[k] = ld_cluster_f4(p + 32u * k * (bn + 4u), r);
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k)
+            sum[k].x += v[k].x, sum[k].y += v[k].y, sum[k].z += v[k].z, sum[k].w += v[k].w;
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+          sts128(buf + (8u * k + (lane >> 2)) * kBufRow + 16u * (lane & 3u), sum[k].x, sum[k].y, sum[k].z,
+                 sum[k].w);
+        epilogue_block(ga.e, buf, tm * kGemmTokens + t0, tn * bn + c0, ga.tokens, ga.rows, ga.vec);
+      }
+    }
+    cluster_sync();  // nobody reads this thread block's sums any more
   }
   // every warp is here before the tensor memory goes
   tc_fence_before();
@@ -1563,22 +1628,31 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
   ga.vec = vec_ok(op.y, op.y_stride, op.y_type) &&
            vec_ok(op.multiplier, op.multiplier_stride, op.multiplier_type) &&
            vec_ok(op.residual, op.residual_stride, op.residual_type);
-  // the tile width whose rounds over the SMs cost least: a round costs about its tile's rows,
-  // and what 32 more would for reading x and emptying the accumulator; the wider one of two
-  // (4096 rows and 2048 tokens on 148 SMs: 240 rows, 288 tiles in two rounds)
+  // The tile width and the number of thread blocks that share a tile for which the rounds over
+  // the SMs cost least, in cycles: a step of 64 columns takes about 250 and two per row
+  // (measured from 32 to 240 rows), a tile 1000 and 20 per row for its epilogue, and a
+  // shared one 10000 more.  The wider and less shared one of two.  (500 x 8192 and 40 tokens:
+  // 12 us with shared tiles, 27 without; 4096 x 4096 and 256 tokens: 25 and 19.)
   uint64_t cost = ~0ull;
   const bool sums = ga.ncg > (op.y_type == DF11_F32 ? kPart : kPlainSteps);
-  for (uint32_t bn = sums ? kSumRows : 256; bn >= 16; bn -= 16) {
-    const uint64_t tiles = (uint64_t)ga.tiles_m * ((rows + bn - 1) / bn);
-    const uint64_t c = (tiles + sms - 1) / sms * (bn + 32);
-    if (c < cost) {
-      cost = c;
-      ga.bn = bn;
-      ga.tiles = (uint32_t)tiles;
+  uint32_t split = 1;
+  for (uint32_t ctas = 1; ctas <= 8; ctas *= 2) {
+    for (uint32_t bn = ctas > 1 ? 128 : (sums ? kSumRows : 256); bn >= 16 * ctas; bn -= 16 * ctas) {
+      const uint64_t tiles = (uint64_t)ga.tiles_m * ((rows + bn - 1) / bn);
+      // whole clusters do not reach every SM
+      if (ctas > 1 && (tiles * ctas > (uint64_t)sms * 7 / 8 || ga.ncg < 4 * ctas)) break;
+      const uint64_t steps = (ga.ncg + ctas - 1) / ctas, rounds = (tiles * ctas + sms - 1) / sms;
+      const uint64_t c = rounds * (steps * (250 + 2 * bn) + 1000 + 20 * bn) + (ctas > 1 ? 10000 : 0);
+      if (c < cost) {
+        cost = c;
+        split = ctas;
+        ga.bn = bn;
+        ga.tiles = (uint32_t)tiles;
+      }
     }
   }
   ga.stages = kMaxStages;
-  const bool buffers = sums || !ga.vec || rows % 16;
+  const bool buffers = sums || split > 1 || !ga.vec || rows % 16;
   while (gemm_smem(ga.bn, ga.stages, buffers) > 226 * 1024) --ga.stages;
   ga.tmem_cols = 32;
   while (ga.tmem_cols < 2 * ga.bn) ga.tmem_cols *= 2;
@@ -1609,9 +1683,12 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
   const size_t smem = gemm_smem(ga.bn, ga.stages, buffers);
   uint64_t budget = 0;
   void (*kern)(CUtensorMap, CUtensorMap, GemmArgs) =
-      sums ? df11_linear_gemm_kernel<true> : df11_linear_gemm_kernel<false>;
-  const df11_status st = prepare(kern, kGemmThreads, smem, sums ? 75 : 76, budget);
+      split > 1 ? df11_linear_gemm_kernel<true, true>
+                : (sums ? df11_linear_gemm_kernel<true, false> : df11_linear_gemm_kernel<false, false>);
+  const df11_status st = prepare(kern, kGemmThreads, smem, split > 1 ? 77 : (sums ? 75 : 76), budget);
   if (st != DF11_OK) return st;
+  if (split > 1)
+    return launch_cluster(kern, ga.tiles * split, split, kGemmThreads, smem, s, mx, mw, ga);
   const uint32_t grid = ga.tiles < (uint32_t)sms ? ga.tiles : (uint32_t)sms;
   return launch_pdl(kern, dim3(grid), kGemmThreads, smem, s, mx, mw, ga);
 }

@@ -516,3 +516,20 @@ def test_bf16_outputs_of_long_rows():
     want = x.cpu().double() @ w.double().T
     rel = ((y.cpu().double() - want) / want).abs()
     assert float(rel.max()) <= 2.0 ** -8 + 32 * 2.0 ** -23 + 160 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("rows,cols,tokens", [(4096, 4096, 40), (4096, 12288, 128), (500, 8192, 130),
+                                              (1013, 1411, 77), (96, 5000, 33), (2064, 2048, 260),
+                                              (16, 12288, 1100), (7000, 640, 50)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_tiles_that_thread_blocks_share(rows, cols, tokens, out):
+    w = _bf16((rows, cols), cols ** -0.5, 1)
+    x = _bf16((tokens, cols), 1.0, 2).cuda()
+    bias = _bf16((rows,), 1.0, 3)
+    mul, res = _bf16((tokens, rows), 1.0, 4), _bf16((tokens, rows), 1.0, 5)
+    d = df11.compress_linear(w.cuda())
+    kw = dict(biases=[bias.cuda()], multipliers=[mul.cuda()], residuals=[res.cuda()], out_dtype=out)
+    y, = _run([d], [x], **kw)
+    again, = _run([d], [x], **kw)
+    assert torch.equal(y.view(torch.uint8), again.view(torch.uint8))
+    _check(w, x, y, bias=bias, multiplier=mul, residual=res)
