@@ -85,6 +85,7 @@ struct Epilogue {
   uint32_t flags;                // kBiasF32 ...
 };
 constexpr uint32_t kBiasF32 = 1, kMulF32 = 2, kResF32 = 4, kOutF32 = 8;
+constexpr uint32_t kBiasVec = 16;  // the bias starts on a 16-byte boundary
 
 __device__ __forceinline__ float load_any(const void *p, size_t i, bool f32) {
   return f32 ? __ldg(static_cast<const float *>(p) + i)
@@ -105,16 +106,18 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 
 // The activations in fp32.  gelu through the complementary error function and
 // the tanh form as a logistic function: neither loses digits in the negative
-// tail, where 1 + erf and 1 + tanh cancel.
+// tail, where 1 + erf and 1 + tanh cancel.  The quotients take the approximate division (two
+// units in the last place; divisors here are at least 1, and beyond 2^126 it gives the zero that
+// the quotient is next to): the exact one is half of an epilogue's instructions.
 __device__ __forceinline__ float activate(float v, uint32_t act) {
   switch (act) {
     case DF11_ACT_RELU: return v < 0.f ? 0.f : v;  // NaN stays
     case DF11_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
     case DF11_ACT_GELU_TANH: {
       const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
-      return v / (1.f + expf(-2.f * u));
+      return __fdividef(v, 1.f + expf(-2.f * u));
     }
-    case DF11_ACT_SILU: return v / (1.f + expf(-v));
+    case DF11_ACT_SILU: return __fdividef(v, 1.f + expf(-v));
     default: return v;
   }
 }
@@ -913,8 +916,15 @@ __device__ __forceinline__ void epilogue16(const Epilogue &e, float (&v)[16], ui
   if (e.mul) load16(e.mul, (size_t)token * e.mul_stride + row, e.flags & kMulF32, m);
   if (e.res) load16(e.res, (size_t)token * e.res_stride + row, e.flags & kResF32, r);
   if (e.bias) {
+    float b[16];
+    if (e.flags & kBiasVec) {
+      load16(e.bias, row, e.flags & kBiasF32, b);
+    } else {
 #pragma unroll
-    for (uint32_t j = 0; j < 16; ++j) v[j] += load_any(e.bias, row + j, e.flags & kBiasF32);
+      for (uint32_t j = 0; j < 16; ++j) b[j] = load_any(e.bias, row + j, e.flags & kBiasF32);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += b[j];
   }
   if (e.act != DF11_ACT_NONE) {
 #pragma unroll
@@ -1433,7 +1443,8 @@ Epilogue make_epilogue(const df11_linear &op) {
   e.act = (uint32_t)op.activation;
   e.flags = (op.bias_type == DF11_F32 ? kBiasF32 : 0u) |
             (op.multiplier_type == DF11_F32 ? kMulF32 : 0u) |
-            (op.residual_type == DF11_F32 ? kResF32 : 0u) | (op.y_type == DF11_F32 ? kOutF32 : 0u);
+            (op.residual_type == DF11_F32 ? kResF32 : 0u) | (op.y_type == DF11_F32 ? kOutF32 : 0u) |
+            (aligned(op.bias, 16) ? kBiasVec : 0u);
   return e;
 }
 
