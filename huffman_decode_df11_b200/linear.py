@@ -218,7 +218,8 @@ class LinearPlan:
     (tokens x rows): per weight a float32 or BF16 tensor or None.
     `activations`: per weight "none", "relu", "gelu", "gelu_tanh" or "silu".
     Rows of all of them must be contiguous, at any distance of a row's length
-    or more.  A residual may be the output itself.  Runs of one plan share its
+    or more.  A residual may be the output itself; no weight's output may be what
+    another one reads, since they run at the same time.  Runs of one plan share its
     workspace and must not overlap on the GPU, graphs that captured them
     included; for several streams at once, make a plan for each."""
 

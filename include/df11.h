@@ -350,7 +350,8 @@ typedef struct df11_linear {
  *   `workspace`: df11_linear_workspace bytes of device memory, 256-byte aligned,
  * that no other work uses until this call's work is done; nothing is kept in
  * it between calls.  y may not overlap x, the multiplier (unless it is the same
- * memory with the same stride and type) or the workspace.
+ * memory with the same stride and type), the workspace or what another weight of the
+ * call reads or writes: the weights of a call run at the same time.
  *   Same conventions as df11_decode_batched otherwise (asynchronous, no
  * allocation, device-detected errors in d_err).  DF11_ERR_INVALID for sizes,
  * strides, types or activations outside the rules and for a workspace that is
