@@ -196,6 +196,6 @@ def _embedding_gradient(ids, grad, rows, out, scale, accumulate, out_dtype, err)
     work = _aligned_empty(size.value, dev)
     _check(L.df11_embedding_gradient(ref, work.data_ptr(), size.value,
                                      err.data_ptr() if err is not None else None,
-                                     torch.cuda.current_stream().cuda_stream),
+                                     _stream_handle(None)),
            "df11_embedding_gradient")
     return out
