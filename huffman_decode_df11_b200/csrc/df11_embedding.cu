@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "df11.h"
 #include "df11_device.cuh"
@@ -51,6 +52,12 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// two BF16 products, rounded once: what the fp32 product, exact here, is rounded to
+__device__ __forceinline__ uint32_t bf16_product(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
@@ -66,6 +73,7 @@ struct EmbedArgs {
   uint32_t segs, seg_len;   // a row's segments, and elements per segment
   uint32_t ids64, out_f32, scaled;
   float scale;
+  uint32_t scale2;          // the scale twice in BF16 where it is a BF16 value, or 0
   uint32_t vec;             // rows of 16-element groups on 16-byte boundaries
   uint32_t region_bytes;
   uint32_t spin_limit;
@@ -292,8 +300,10 @@ __global__ void __launch_bounds__(kWarps * 32)
               uint32_t r[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                r[j] = a.scaled ? bf16_pair(scaled_value(a, u[j] & 0xFFFFu), scaled_value(a, u[j] >> 16))
-                                : u[j];
+                r[j] = !a.scaled ? u[j]
+                       : a.scale2
+                           ? bf16_product(u[j], a.scale2)
+                           : bf16_pair(scaled_value(a, u[j] & 0xFFFFu), scaled_value(a, u[j] >> 16));
               uint4 *q = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + o);
               q[0] = make_uint4(r[0], r[1], r[2], r[3]);
               q[1] = make_uint4(r[4], r[5], r[6], r[7]);
@@ -994,6 +1004,9 @@ df11_status df11_decode_embedding(const df11_tensor *table, const df11_embedding
   a.out_f32 = op->out_type == DF11_F32;
   a.scaled = op->scale != 1.0f;
   a.scale = op->scale;
+  uint32_t bits;
+  memcpy(&bits, &op->scale, sizeof(bits));
+  a.scale2 = bits & 0xFFFFu ? 0u : bits | bits >> 16;
   a.vec = op->dim % 16 == 0 && aligned(op->out, 16) &&
           op->out_stride * type_bytes(op->out_type) % 16 == 0;
   a.spin_limit = kSpinLimit;

@@ -415,3 +415,26 @@ def test_gradient_rows_that_end_inside_a_tile():
             grad = torch.randn(tokens, 1032, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
             dw = df11.embedding_gradient(ids.cuda(), grad, 37)
             _check_gradient(ids, grad, 37, dw)
+
+
+@pytest.mark.parametrize("scale", [64.0, -1.5, 2.0 ** -60, 2.0 ** 60, 1.0078125, 0.1])
+def test_scaled_words_of_every_kind(scale):
+    # every BF16 word, infinities, NaN and subnormal ones among them: the product in 64 bits,
+    # rounded once (half a unit of the smallest subnormal, 2^-134, where that is all there is)
+    w = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).reshape(256, 256)
+    d = df11.compress_on_device(w.cuda())
+    ids = torch.arange(256)
+    got = _lookup(d, ids, scale=scale)
+    want = w.double() * float(np.float32(scale))
+    nan = want.isnan()
+    assert torch.equal(got.cpu().isnan(), nan)
+    near = want.float().to(torch.bfloat16)  # exact in fp32 for two factors of 8 bits
+    tiny = want.abs() < 2.0 ** -126
+    if scale != 0.1:
+        same = ~nan & ~tiny
+        assert torch.equal(got.cpu()[same], near[same])
+    else:
+        fin = ~nan & ~tiny & (want.abs() < 3e38)
+        err = (got.cpu().double() - want).abs()[fin]
+        assert torch.all(err <= 2.0 ** -8 * want.abs()[fin] * (1 + 2.0 ** -15))
+    assert torch.all((got.cpu().double() - want).abs()[tiny] <= 2.0 ** -134 * (1 + 2.0 ** -8))
