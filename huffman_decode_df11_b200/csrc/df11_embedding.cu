@@ -7,10 +7,10 @@
 // that holds the segment's first element (the positions are close to even, so
 // 32 probes around the proportional guess nearly always hold it), the chunk in
 // it from the chunk counts, and walks 32 chunks at a time, one per lane, as the
-// decode kernel does.
+// decode kernel does.  Many short rows take a part of a warp each (launch_lookup).
 //
 // It reads a fraction of the table and writes the rows.  What bounds it is the walk, as
-// in the decode kernels: 8192 rows of 4096 in 44 us, 0.76 weights per ns, where decoding
+// in the decode kernels: 8192 rows of 4096 in 42 us, 0.8 weights per ns, where decoding
 // all of a tensor gives 1.35, since a row begins and ends inside a chunk and a warp has to
 // find its place first.  Four rows: 6 us, one pass over the chain of dependent loads.
 //
@@ -113,6 +113,22 @@ __device__ __forceinline__ uint32_t find_block(const KTensor &k, uint32_t e, int
   return first;
 }
 
+// The same by one lane: a bracket of 32 blocks around the proportional guess where it holds
+// the element, halved.
+__device__ __forceinline__ uint32_t find_block_alone(const KTensor &k, uint32_t e, uint32_t &at) {
+  const uint32_t guess = (uint32_t)((uint64_t)e * k.num_blocks / k.n);
+  uint32_t first = guess > 15u ? guess - 15u : 0u, last = min(first + 32u, k.num_blocks);
+  if (first && __ldg(k.block_out_pos + first) > e) first = 0;
+  if (last < k.num_blocks && __ldg(k.block_out_pos + last) <= e) last = k.num_blocks;
+  while (last - first > 1u) {
+    const uint32_t mid = first + ((last - first) >> 1);
+    if (__ldg(k.block_out_pos + mid) <= e) first = mid;
+    else last = mid;
+  }
+  at = __ldg(k.block_out_pos + first);
+  return first;
+}
+
 // What a lane needs of its chunk: the codewords that start in it, its words and the next one
 // (as they are in memory), and the gap fields of it and the next one from bit 31 down.
 template <int C>
@@ -138,17 +154,20 @@ struct Chunk {
   }
 };
 
-template <int C>
+// G lanes per segment: a warp, or for many short rows a part of it, whose rows go side by side.
+template <int C, int G>
 __global__ void __launch_bounds__(kWarps * 32)
     df11_embedding_kernel(const __grid_constant__ EmbedArgs a) {
   constexpr int NW = C / 4 + 1;
   extern __shared__ __align__(128) uint8_t smem[];
   const KTensor &tk = a.k;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kGroups = 32 / G;  // per warp
+  const int tid = threadIdx.x, lane = tid & (G - 1), group = tid / G;
+  const uint32_t gm = G == 32 ? 0xFFFFFFFFu : ((1u << (G & 31)) - 1u) << (tid & 31 & ~(G - 1));
   uint8_t *lens_s = smem + kOffLens;
   uint32_t *lut0_s = reinterpret_cast<uint32_t *>(smem + kOffLut0);
   const uint32_t wide = smem_addr(smem + kOffWide);
-  uint8_t *region_p = smem + kOffStages + warp * a.region_bytes;
+  uint8_t *region_p = smem + kOffStages + group * a.region_bytes;
   const uint32_t region = smem_addr(region_p);
   const uint32_t tbar = smem_addr(smem);
   if (tid == 0) {
@@ -157,15 +176,15 @@ __global__ void __launch_bounds__(kWarps * 32)
     mbar_arrive_expect_tx(tbar, DF11_DECODE_TABLE_BYTES);
     bulk_g2s(smem_addr(lens_s), tk.decode_table, DF11_DECODE_TABLE_BYTES, tbar);
   }
-  for (uint32_t i = lane; i < a.region_bytes / 16; i += 32)
+  for (uint32_t i = lane; i < a.region_bytes / 16; i += G)
     reinterpret_cast<uint4 *>(region_p)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();  // the barrier is initialised
   pdl_wait();       // the ids may come from the previous kernel, which may read the output
   pdl_launch_dependents();
   bool table = false;
   const uint64_t items = (uint64_t)a.tokens * a.segs;
-  for (uint64_t item = blockIdx.x + (uint64_t)gridDim.x * warp; item < items;
-       item += (uint64_t)gridDim.x * kWarps) {
+  for (uint64_t item = blockIdx.x + (uint64_t)gridDim.x * group; item < items;
+       item += (uint64_t)gridDim.x * kWarps * kGroups) {
     const uint32_t token = (uint32_t)(item / a.segs), seg = (uint32_t)(item - (uint64_t)token * a.segs);
     const uint32_t c_first = seg * a.seg_len, c_last = min(c_first + a.seg_len, a.dim);
     const int64_t id = a.ids64 ? static_cast<const int64_t *>(a.ids)[token]
@@ -173,7 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     const size_t out0 = (size_t)token * a.out_stride;
     if (id < 0 || id >= (int64_t)a.rows) {
       if (lane == 0) report(a.err, DF11_DEV_ERR_INDEX);
-      for (uint32_t c = c_first + lane; c < c_last; c += 32) {
+      for (uint32_t c = c_first + lane; c < c_last; c += G) {
         if (a.out_f32) static_cast<float *>(a.out)[out0 + c] = 0.f;
         else static_cast<uint16_t *>(a.out)[out0 + c] = 0;
       }
@@ -182,12 +201,12 @@ __global__ void __launch_bounds__(kWarps * 32)
     const uint32_t row0 = (uint32_t)id * a.dim;  // elements of a tensor: below 2^32
     const uint32_t e0 = row0 + c_first, e1 = row0 + c_last;
     uint32_t P, chunk0;
-    const uint32_t b = find_block(tk, e0, lane, P);
+    const uint32_t b = G == 32 ? find_block(tk, e0, lane, P) : find_block_alone(tk, e0, P);
     if (P > e0) {  // inconsistent positions
       if (lane == 0) report(a.err, DF11_DEV_ERR_COUNT);
       continue;
     }
-    {
+    if constexpr (G == 32) {
       // the chunk of block b that holds e0: the last whose first element is at
       // or before it
       const uint2 cv = __ldg(reinterpret_cast<const uint2 *>(tk.chunk_counts + (size_t)b * kT) + lane);
@@ -212,26 +231,61 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
       P += __shfl_sync(0xFFFFFFFFu, before, src);
       chunk0 = b * kT + 8u * src + __shfl_sync(0xFFFFFFFFu, j, src);
+    } else {
+      // the same, by 16 counts, then 4, then one
+      const uint4 *q = reinterpret_cast<const uint4 *>(tk.chunk_counts + (size_t)b * kT);
+      const uint32_t off = e0 - P;
+      uint32_t before = 0, j = 0;
+      uint4 v = __ldg(q);
+      auto sum4 = [](uint32_t c) { return __dp4a(c, 0x01010101u, 0u); };
+      for (uint32_t i = 0; i < kT / 16 - 1; ++i) {
+        const uint32_t sum = sum4(v.x) + sum4(v.y) + sum4(v.z) + sum4(v.w);
+        if (before + sum > off) break;
+        before += sum;
+        j += 16;
+        v = __ldg(q + i + 1);
+      }
+      const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+      uint32_t c = v.x;
+#pragma unroll
+      for (uint32_t i = 0; i < 3; ++i) {
+        const uint32_t sum = sum4(w4[i]);
+        if ((j & 15u) == 4 * i && before + sum <= off) {
+          before += sum;
+          j += 4;
+          c = w4[i + 1];
+        }
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < 3; ++i) {
+        const uint32_t n = (c >> (8 * i)) & 0xFFu;
+        if ((j & 3u) == i && before + n <= off) {
+          before += n;
+          ++j;
+        }
+      }
+      P += before;
+      chunk0 = b * kT + j;
     }
     Chunk<C> next;
     next.load(tk, (uint64_t)chunk0 + lane);
-    for (uint64_t c0 = chunk0; P < e1; c0 += 32) {
+    for (uint64_t c0 = chunk0; P < e1; c0 += G) {
       const uint64_t chunk = c0 + lane;
       Chunk<C> ck = next;
       const uint32_t cnt = ck.cnt;
       uint32_t incl = cnt;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      for (int d = 1; d < G; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(gm, incl, d, G);
         if (lane >= d) incl += v;
       }
-      const uint32_t total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-      if (total == 0 || total > tk.n - P || __any_sync(0xFFFFFFFFu, cnt > tk.max_chunk_elems)) {
+      const uint32_t total = __shfl_sync(gm, incl, G - 1, G);
+      if (total == 0 || total > tk.n - P || __any_sync(gm, cnt > tk.max_chunk_elems)) {
         if (lane == 0) report(a.err, DF11_DEV_ERR_COUNT);
         break;
       }
       // the next 32 chunks, and the first sign/mantissa bytes, arrive during the walk
-      if (P + total < e1) next.load(tk, chunk + 32);
+      if (P + total < e1) next.load(tk, chunk + G);
       const uint32_t E = P + incl - cnt, base = P & ~15u;
       const bool need = cnt && E < e1 && E + cnt > e0;
       // elements [lo, hi) past `base` are the row's, element i at byte i of the region
@@ -257,7 +311,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         }
       }
       if (!table) {
-        table = __all_sync(0xFFFFFFFFu, mbar_wait(tbar, 0, a.spin_limit));
+        table = __all_sync(gm, mbar_wait(tbar, 0, a.spin_limit));
         if (!table) {
           if (lane == 0) report(a.err, DF11_DEV_ERR_TIMEOUT);
           break;
@@ -277,13 +331,13 @@ __global__ void __launch_bounds__(kWarps * 32)
         if (!bad && got != cnt) bad = DF11_DEV_ERR_COUNT;
         if (bad) report(a.err, bad);
       }
-      __syncwarp();
+      __syncwarp(gm);
       const size_t out_base = out0 + base - row0;  // may wrap below the row: base is before it
       if (a.vec) {
-        for (uint32_t i = (lo & ~15u) + 16u * lane; i < hi; i += 512u) {
+        for (uint32_t i = (lo & ~15u) + 16u * lane; i < hi; i += 16u * G) {
           const uint4 rv = lds128(region + i);
           const uint4 cur = sv;  // the next group's bytes ahead
-          if (i + 512u < hi) sv = __ldg(reinterpret_cast<const uint4 *>(sm + i + 512u));
+          if (i + 16u * G < hi) sv = __ldg(reinterpret_cast<const uint4 *>(sm + i + 16u * G));
           const uint2 p0 = fuse4(cur.x, rv.x), p1 = fuse4(cur.y, rv.y);
           const uint2 p2 = fuse4(cur.z, rv.z), p3 = fuse4(cur.w, rv.w);
           const uint32_t u[8] = {p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
@@ -317,21 +371,21 @@ __global__ void __launch_bounds__(kWarps * 32)
         }
       } else {
         constexpr uint32_t kAhead = 8;  // loads before the first store
-        for (uint32_t i = lo + lane; i < hi; i += 32 * kAhead) {
+        for (uint32_t i = lo + lane; i < hi; i += G * kAhead) {
           uint32_t v[kAhead];
 #pragma unroll
-          for (uint32_t j = 0; j < kAhead; ++j) v[j] = i + 32 * j < hi ? __ldg(sm + i + 32 * j) : 0u;
+          for (uint32_t j = 0; j < kAhead; ++j) v[j] = i + G * j < hi ? __ldg(sm + i + G * j) : 0u;
 #pragma unroll
           for (uint32_t j = 0; j < kAhead; ++j)
-            if (i + 32 * j < hi)
-              embed_store(a, out_base + i + 32 * j, fuse1(v[j], lds8(region + i + 32 * j)));
+            if (i + G * j < hi)
+              embed_store(a, out_base + i + G * j, fuse1(v[j], lds8(region + i + G * j)));
         }
       }
-      __syncwarp();
+      __syncwarp(gm);
       // the region zero again (a walk over corrupt data may write 7 bytes more)
-      for (uint32_t i = lane; i < (P - base + total + 8u + 15u) >> 4; i += 32)
+      for (uint32_t i = lane; i < (P - base + total + 8u + 15u) >> 4; i += G)
         sts128_zero(region + 16u * i);
-      __syncwarp();
+      __syncwarp(gm);
       P += total;
     }
   }
@@ -839,30 +893,49 @@ uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 bool known_type(int32_t t) { return t == DF11_BF16 || t == DF11_F32; }
 uintptr_t type_bytes(int32_t t) { return t == DF11_F32 ? 4 : 2; }
 
-template <int C>
-df11_status launch_embedding(EmbedArgs &a, size_t smem, int instance, cudaStream_t s) {
-  auto kern = df11_embedding_kernel<C>;
+// `per_pass`: elements of a row that G chunks hold on average
+template <int C, int G>
+df11_status launch_embedding(EmbedArgs &a, uint64_t per_pass, int instance, cudaStream_t s) {
+  auto kern = df11_embedding_kernel<C, G>;
+  // G chunks from any chunk on: first element's offset, elements, the walk's slack
+  a.region_bytes = (uint32_t)round_up(15 + (uint64_t)G * a.k.max_chunk_elems + 8, 16);
+  const size_t smem = kOffStages + (size_t)kWarps * (32 / G) * a.region_bytes;
   uint64_t budget = 0;
   const df11_status st = prepare(kern, kWarps * 32, smem, instance, budget);
   if (st != DF11_OK) return st;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DF11_ERR_CUDA;
-  const uint64_t sms = device_info(dev).sms;
-  // A row in segments that 32 chunks hold on average (30, since a row begins and ends inside
-  // a chunk), while there are fewer rows than warps; more of a row per warp otherwise, which
-  // then finds its place in the stream once.
-  const uint64_t per_pass = 30ull * a.k.n / ((uint64_t)a.k.num_blocks * kT) + 1;
+  const uint64_t sms = device_info(dev).sms, groups = kWarps * (32 / G);
+  // A row in segments that one pass holds, while there are fewer rows than warps; more of a row
+  // per warp otherwise, which then finds its place in the stream once.
   const uint64_t most = (a.dim + per_pass - 1) / per_pass;
-  uint64_t segs = budget * kWarps / a.tokens;
-  segs = segs < 1 ? 1 : (segs > most ? most : segs);
+  uint64_t segs = budget * groups / a.tokens;
+  segs = segs < 1 || G < 32 ? 1 : (segs > most ? most : segs);
   a.seg_len = (uint32_t)round_up((a.dim + segs - 1) / segs, 16);
   a.segs = (a.dim + a.seg_len - 1) / a.seg_len;
   // every SM, then every warp of a thread block, then more thread blocks per SM
   const uint64_t items = (uint64_t)a.tokens * a.segs;
-  uint64_t grid = (items + kWarps - 1) / kWarps;
+  uint64_t grid = (items + groups - 1) / groups;
   if (grid < sms) grid = items < sms ? items : sms;
   if (grid > budget) grid = budget;
   return launch_pdl(kern, dim3((uint32_t)grid), kWarps * 32, smem, s, a);
+}
+
+// Lanes per row: a warp's 32, unless there are more rows than the device holds warps and a row
+// takes a few chunks only (3591 x 64 and 144534 tokens: 28 us with two lanes per row, 226 with a
+// warp; 50000 x 256 and 20000 tokens: 18 with eight, 36).
+template <int C>
+df11_status launch_lookup(EmbedArgs &a, int instance, cudaStream_t s) {
+  const uint64_t chunks = (uint64_t)a.k.num_blocks * kT;
+  const bool many = a.tokens > 148u * 4 * kWarps;
+  // chunks that a row begins in or reaches, 64 times
+  const uint64_t row = 64ull * a.dim * chunks / a.k.n + 64;
+  if (many && row <= 2 * 64) return launch_embedding<C, 2>(a, 1, instance + 1, s);
+  if (many && row <= 4 * 64) return launch_embedding<C, 4>(a, 1, instance + 2, s);
+  if (many && row <= 8 * 64) return launch_embedding<C, 8>(a, 1, instance + 3, s);
+  if (many && row <= 16 * 64) return launch_embedding<C, 16>(a, 1, instance + 4, s);
+  // 32 chunks hold 30 chunks' elements of a row, since it begins and ends inside a chunk
+  return launch_embedding<C, 32>(a, 30ull * a.k.n / chunks + 1, instance, s);
 }
 
 struct GradPlan {
@@ -1010,13 +1083,10 @@ df11_status df11_decode_embedding(const df11_tensor *table, const df11_embedding
   a.vec = op->dim % 16 == 0 && aligned(op->out, 16) &&
           op->out_stride * type_bytes(op->out_type) % 16 == 0;
   a.spin_limit = kSpinLimit;
-  // 32 chunks from any chunk on: first element's offset, elements, the walk's slack
-  a.region_bytes = (uint32_t)round_up(15 + 32ull * p.max_chunk_elems + 8, 16);
-  const size_t smem = kOffStages + (size_t)kWarps * a.region_bytes;
   cudaStream_t s = (cudaStream_t)stream;
-  if (p.chunk_bytes == 24) return launch_embedding<24>(a, smem, 78, s);
-  if (p.chunk_bytes == 16) return launch_embedding<16>(a, smem, 79, s);
-  return launch_embedding<8>(a, smem, 80, s);
+  if (p.chunk_bytes == 24) return launch_lookup<24>(a, 86, s);
+  if (p.chunk_bytes == 16) return launch_lookup<16>(a, 91, s);
+  return launch_lookup<8>(a, 96, s);
 }
 
 df11_status df11_embedding_gradient_workspace(const df11_embedding_grad *op, size_t *bytes) {

@@ -438,3 +438,39 @@ def test_scaled_words_of_every_kind(scale):
         err = (got.cpu().double() - want).abs()[fin]
         assert torch.all(err <= 2.0 ** -8 * want.abs()[fin] * (1 + 2.0 ** -15))
     assert torch.all((got.cpu().double() - want).abs()[tiny] <= 2.0 ** -134 * (1 + 2.0 ** -8))
+
+
+@pytest.mark.parametrize("chunk_bytes", [8, 16, 24])
+@pytest.mark.parametrize("dim", [1, 5, 48, 64, 100, 160, 256, 371, 512, 1003, 1024])
+def test_many_short_rows(dim, chunk_bytes):
+    # more rows than the device holds warps: a few lanes each
+    rows = 40000 // dim + 3
+    w = _table(rows, dim)
+    d = df11.compress_on_device(w.cuda(), chunk_bytes=chunk_bytes)
+    ids = _ids(9001, rows, 1)
+    ids[:3], ids[-3:] = rows - 1, 0
+    assert torch.equal(_bits(_lookup(d, ids)), _bits(w[ids]))
+    got = _lookup(d, ids.to(torch.int32), scale=0.3, out_dtype=torch.float32).cpu()
+    assert torch.equal(got, w[ids].float() * float(np.float32(0.3)))
+    wide = torch.full((9001, dim + 3), 5.0, dtype=torch.bfloat16, device="cuda")
+    df11.decode_embedding(d, ids.cuda(), out=wide[:, :dim])
+    assert torch.equal(_bits(wide[:, :dim].cpu()), _bits(w[ids])) and bool((wide[:, dim:] == 5).all())
+    ids[100], ids[8000] = -1, rows
+    err = df11.new_error_word()
+    got = df11.decode_embedding(d, ids.cuda(), err=err).cpu()
+    want = w[ids.clamp(0, rows - 1)].clone()
+    want[100], want[8000] = 0, 0
+    assert torch.equal(_bits(got), _bits(want))
+    with pytest.raises(Exception):
+        df11.check_device_error(err)
+
+
+def test_many_short_rows_of_long_codes():
+    # words whose codes differ most in length, and blocks far from the proportional guess
+    g = torch.Generator().manual_seed(3)
+    easy = torch.full((30000, 24), 1.0, dtype=torch.bfloat16)
+    hard = torch.randint(-32768, 32767, (6000, 24), generator=g, dtype=torch.int32).to(torch.int16)
+    w = torch.cat([easy, hard.view(torch.bfloat16), easy[:500]])
+    d = df11.compress_on_device(w.cuda())
+    ids = torch.cat([torch.arange(29000, 36500), _ids(3000, len(w), 2)])
+    assert torch.equal(_bits(_lookup(d, ids)), _bits(w[ids]))
