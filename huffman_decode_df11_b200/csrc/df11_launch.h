@@ -54,7 +54,7 @@ inline df11_status validate(const df11_tensor &t) {
 // Per-device launch state, indexed by kernel instance: the warp-specialised
 // kernels use 3 * i + mode with i = 3-8 (decode with counts), 12-14 (fused
 // matrix-vector product) and 15-20 (decode without counts); the
-// tensor-core product 64-65, the linear product 66-69, 71-72 and 75-77, the embedding's
+// tensor-core product 64-65, the linear product 66-69 and 71-78, the embedding's
 // gradient 81-85 and its lookup 86-100.
 constexpr int kInstances = 104;
 struct DeviceInfo {

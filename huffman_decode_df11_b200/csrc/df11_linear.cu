@@ -109,17 +109,27 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 // tail, where 1 + erf and 1 + tanh cancel.  The quotients take the approximate division (two
 // units in the last place; divisors here are at least 1, and beyond 2^126 it gives the zero that
 // the quotient is next to): the exact one is half of an epilogue's instructions.
-__device__ __forceinline__ float activate(float v, uint32_t act) {
+__device__ __forceinline__ float relu(float v) { return v < 0.f ? 0.f : v; }  // NaN stays
+__device__ __forceinline__ float gelu(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
+__device__ __forceinline__ float gelu_tanh(float v) {
+  const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
+  return __fdividef(v, 1.f + expf(-2.f * u));
+}
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + expf(-v)); }
+// one branch for all values, so that their chains of instructions run side by side
+template <int N>
+__device__ __forceinline__ void activate(float *v, uint32_t act) {
+#define DF11_EACH(f)            \
+  _Pragma("unroll") for (int j = 0; j < N; ++j) v[j] = f(v[j]); \
+  break
   switch (act) {
-    case DF11_ACT_RELU: return v < 0.f ? 0.f : v;  // NaN stays
-    case DF11_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
-    case DF11_ACT_GELU_TANH: {
-      const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
-      return __fdividef(v, 1.f + expf(-2.f * u));
-    }
-    case DF11_ACT_SILU: return __fdividef(v, 1.f + expf(-v));
-    default: return v;
+    case DF11_ACT_RELU: DF11_EACH(relu);
+    case DF11_ACT_GELU: DF11_EACH(gelu);
+    case DF11_ACT_GELU_TANH: DF11_EACH(gelu_tanh);
+    case DF11_ACT_SILU: DF11_EACH(silu);
+    default: break;
   }
+#undef DF11_EACH
 }
 
 // An output's operands, and the epilogue on a sum.  The loads stand before what they wait
@@ -140,12 +150,17 @@ __device__ __forceinline__ Operands load_operands(const Epilogue &e, uint32_t to
   }
   return o;
 }
-__device__ __forceinline__ float finish(const Epilogue &e, float v, const Operands &o) {
-  if (e.bias) v += o.bias;
-  v = activate(v, e.act);
-  if (e.mul) v *= o.mul;
-  if (e.res) v += o.res;
-  return v;
+template <int N>
+__device__ __forceinline__ void finish(const Epilogue &e, float (&v)[N], const Operands (&o)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    if (e.bias) v[j] += o[j].bias;
+  activate<N>(v, e.act);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if (e.mul) v[j] *= o[j].mul;
+    if (e.res) v[j] += o[j].res;
+  }
 }
 
 __device__ __forceinline__ void store_any(const Epilogue &e, float v, uint32_t token,
@@ -585,7 +600,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   pdl_wait();
   pdl_launch_dependents();
   if (!here) return;
-  const Operands o = load_operands(ft.e, token, row);
+  const Operands o[1] = {load_operands(ft.e, token, row)};
   float sum = __ldcg(p + c0 * stride + slot * fb.warps * per_warp);
   constexpr uint32_t kAhead = 8;  // loads before the first addition
   for (uint32_t c = c0 + 1; c <= c1; c += kAhead) {
@@ -596,7 +611,9 @@ __global__ void __launch_bounds__(kFinishThreads)
     for (uint32_t j = 0; j < kAhead; ++j)
       if (c + j <= c1) sum += v[j];
   }
-  store_any(ft.e, finish(ft.e, sum, o), token, row);
+  float v[1] = {sum};
+  finish(ft.e, v, o);
+  store_any(ft.e, v[0], token, row);
 }
 
 // ---- decoding into tiles --------------------------------------------------------------
@@ -790,18 +807,34 @@ __global__ void __launch_bounds__(1024) linear_rows_kernel(uint32_t *unit_rows, 
 // epilogue: a lane is a token, its columns consecutive rows of W, three warps
 // taking groups of 16 in turn (with eight warps the epilogue takes longer than the product
 // of 4096 columns where an activation is in it).
-//   For fp32 outputs, and for rows longer than kPlainSteps steps, the accumulators are
-// moved out every kPart steps and added in registers (SUMS), because the tensor cores cut
-// off what an addition leaves below their accumulator: at 12288 columns that drifts by
-// 1e-5, which a BF16 output (half a step: 2e-3 to 4e-3) does not show.  Tiles are then at
-// most 144 rows wide.
-//   4096 x 12288 and 2048 tokens take 150 us, 1.37 PFLOP/s, and 12288 x 4096 144 us, 1.43,
-// with the clocks that a kernel by itself has; the copies of the next stages bound it (four
-// of 240 rows fit), and the power limit where calls follow one another for seconds.
+//   Of more than kPart steps the accumulators are moved out every kPart steps and added in
+// registers (SUMS), because the tensor cores cut off what an addition leaves below their
+// accumulator: one chain drifts by 1e-5 at 12288 columns and in proportion to the length, which a
+// BF16 output shows as well, as values next to a border and where a residual cancels the sum.
+// Tiles are then at most 240 rows wide: 80 sums of a thread in registers, for which the
+// epilogue's threads take registers from the issuing ones.  What that costs is the epilogue, of
+// which only two parts' products run ahead (4096 x 12288, 2048 tokens and a residual: 190 us for
+// the call against 187 with one chain; 12288 x 4096 with silu and a multiplier: 198 and 190).
+//   The copies of the next stages bound it (four of 240 rows fit), and the power limit where
+// calls follow one another for seconds.
 constexpr int kGemmTokens = 128;
 constexpr int kEpilogueWarps = 12;  // then a warp for the copies and one for the products
 constexpr uint32_t kColStep = 4 * kEpilogueWarps;  // columns from one group of 16 of a warp to its next
-constexpr int kGemmThreads = (kEpilogueWarps + 2) * 32;
+constexpr int kGemmThreads = (kEpilogueWarps + 4) * 32;  // whole groups of four warps
+// Registers of a thread while the roles run (SUMS): the launch's 128 shared out so that an
+// epilogue thread's 80 sums and what it works with fit.  Spilled ones go past what the shared
+// memory leaves of L1 and cost as much as the product.
+constexpr int kLaunchRegs = 128, kSumRegs = 160, kIssueRegs = 32;
+static_assert(kEpilogueWarps * kSumRegs + 4 * kIssueRegs <= (kEpilogueWarps + 4) * kLaunchRegs,
+              "registers given out");
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 struct GemmArgs {
   Epilogue e;
@@ -809,15 +842,14 @@ struct GemmArgs {
   uint32_t bn, stages, tmem_cols;     // rows of W per tile, stages of shared memory
   uint32_t tiles_m, tiles;            // token tiles, all tiles
   uint32_t x_bytes;                   // of x per stage: the rows that a tile of tokens has at most
-  uint32_t vec;                       // rows of y, multiplier and residual take 16-byte accesses
   int32_t *err;
   uint32_t spin_limit;
 };
 
 constexpr uint32_t kXBytes = kGemmTokens * 128;
 constexpr uint32_t kPart = 8;      // steps of 64 columns between accumulators (SUMS)
-constexpr uint32_t kSumRows = 144; // rows of a tile whose sums are in registers (SUMS)
-constexpr uint32_t kPlainSteps = 1024;  // without SUMS, for BF16 outputs: 65536 columns
+constexpr uint32_t kSumRows = 240; // rows of a tile whose sums are in registers (SUMS)
+constexpr uint32_t kSplitRows = 128;  // of a tile that thread blocks share
 constexpr uint32_t kMaxStages = 8;
 // an epilogue warp's buffer of 32 tokens and 16 rows: 16 bytes more per token, so that no
 // two accesses meet in a bank
@@ -926,10 +958,7 @@ __device__ __forceinline__ void epilogue16(const Epilogue &e, float (&v)[16], ui
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] += b[j];
   }
-  if (e.act != DF11_ACT_NONE) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = activate(v[j], e.act);
-  }
+  activate<16>(v, e.act);
   if (e.mul) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] *= m[j];
@@ -955,9 +984,9 @@ __device__ __forceinline__ void epilogue16(const Epilogue &e, float (&v)[16], ui
 
 // The epilogue where rows are not on 16-byte boundaries or end early, and where sums take the
 // registers: 32 tokens and 16 rows, which lie in the warp's buffer, so that the lanes'
-// accesses are next to one another.  A lane
-// has four consecutive rows of every eighth token (4099 x 4096 and 1024 tokens with multiplier
-// and residual: 108 us; a token per lane, one value at a time: 186 us).
+// accesses are next to one another.  A lane has four consecutive rows of every eighth token
+// (4099 x 4096 and 1024 tokens with silu, multiplier and residual: 62 us for the call; with
+// operands widened as each arrives and a branch per activation 82).
 __device__ __forceinline__ void sts128(uint32_t a, float x, float y, float z, float w) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w)
                : "memory");
@@ -980,69 +1009,105 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// `n` (0 to 4) consecutive values of a row, one access where `vec`
-__device__ __forceinline__ float4 load4(const void *p, size_t i, bool f32, bool vec, uint32_t n) {
-  if (vec) {
-    if (f32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
-                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
-  }
-  float v[4];
+// A lane's four values of each of its four tokens as they are in memory, and what they stand
+// for: what widens them waits for them, so it stands behind all of the loads.  VEC: 16-byte
+// boundaries and all four there; otherwise the first `n`, one by one.
+template <bool VEC>
+struct Quads {
+  uint32_t w[4][4];
+  // `there`: bit k for token k
+  __device__ __forceinline__ void load(const void *p, size_t i, size_t step, bool f32, uint32_t there,
+                                       uint32_t n) {
+    const uint8_t *q = static_cast<const uint8_t *>(p) + (f32 ? 4 * i : 2 * i);
+    step *= f32 ? 4 : 2;
+    if (!VEC) {
 #pragma unroll
-  for (uint32_t j = 0; j < 4; ++j) {
-    v[j] = 0.f;
-    if (j < n)
-      v[j] = f32 ? static_cast<const float *>(p)[i + j]
-                 : __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i + j] << 16);
+      for (uint32_t k = 0; k < 4; ++k, q += step)
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j)
+          if (j < n && there >> k & 1u)
+            w[k][j] = f32 ? reinterpret_cast<const uint32_t *>(q)[j] : reinterpret_cast<const uint16_t *>(q)[j];
+    } else if (f32) {
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k, q += step)
+        if (there >> k & 1u) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(q);
+          w[k][0] = u.x, w[k][1] = u.y, w[k][2] = u.z, w[k][3] = u.w;
+        }
+    } else {
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k, q += step)
+        if (there >> k & 1u) {
+          const uint2 u = *reinterpret_cast<const uint2 *>(q);
+          w[k][0] = u.x, w[k][1] = u.y;
+        }
+    }
   }
-  return make_float4(v[0], v[1], v[2], v[3]);
-}
+  template <typename F>
+  __device__ __forceinline__ void each(bool f32, F f) const {
+    if (VEC && !f32) {
+#pragma unroll
+      for (uint32_t j = 0; j < 16; ++j)
+        f(j, __uint_as_float(j % 2 ? w[j / 4][j % 4 / 2] & 0xFFFF0000u : w[j / 4][j % 4 / 2] << 16));
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < 16; ++j) f(j, __uint_as_float(w[j / 4][j % 4] << (f32 ? 0 : 16)));
+    }
+  }
+};
 
+template <bool VEC>
 __device__ __forceinline__ void epilogue_block(const Epilogue &e, uint32_t buf, uint32_t token0,
-                                               uint32_t row0, uint32_t tokens, uint32_t rows,
-                                               bool vec) {
-  const uint32_t lane = threadIdx.x & 31, row = row0 + 4u * (lane & 3u);
-  const uint32_t n = row < rows ? min(rows - row, 4u) : 0u;
+                                               uint32_t row0, uint32_t tokens, uint32_t rows) {
+  const uint32_t lane = threadIdx.x & 31, row = row0 + 4u * (lane & 3u), token = token0 + (lane >> 2);
   const uint32_t at = buf + (lane >> 2) * kBufRow + 16u * (lane & 3u);
-  vec = vec && n == 4;
+  const uint32_t n = row < rows ? (VEC ? 4u : min(rows - row, 4u)) : 0u;
+  const bool mul32 = e.flags & kMulF32, res32 = e.flags & kResF32;
+  uint32_t there = 0;
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k) there |= n && token + 8u * k < tokens ? 1u << k : 0u;
+  Quads<VEC> m, r;
+  if (e.mul) m.load(e.mul, (size_t)token * e.mul_stride + row, 8ull * e.mul_stride, mul32, there, n);
+  if (e.res) r.load(e.res, (size_t)token * e.res_stride + row, 8ull * e.res_stride, res32, there, n);
   __syncwarp();  // the buffer is written
-  float4 m[4], r[4], b = make_float4(0.f, 0.f, 0.f, 0.f);
+  float v[16];
 #pragma unroll
   for (uint32_t k = 0; k < 4; ++k) {
-    const uint32_t token = token0 + 8u * k + (lane >> 2);
-    m[k] = r[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (n && token < tokens) {
-      if (e.mul) m[k] = load4(e.mul, (size_t)token * e.mul_stride + row, e.flags & kMulF32, vec, n);
-      if (e.res) r[k] = load4(e.res, (size_t)token * e.res_stride + row, e.flags & kResF32, vec, n);
-    }
+    const float4 q = lds_f4(at + 8u * k * kBufRow);
+    v[4 * k] = q.x, v[4 * k + 1] = q.y, v[4 * k + 2] = q.z, v[4 * k + 3] = q.w;
   }
-  if (e.bias && n) b = load4(e.bias, row, e.flags & kBiasF32, false, n);
-  if (e.act != DF11_ACT_NONE) {
-#pragma unroll 1
-    for (uint32_t k = 0; k < 4; ++k) {
-      const uint32_t p = at + 8u * k * kBufRow;
-      const float4 v = lds_f4(p);
-      sts128(p, activate(v.x + b.x, e.act), activate(v.y + b.y, e.act), activate(v.z + b.z, e.act),
-             activate(v.w + b.w, e.act));
-    }
-  }
+  if (e.bias) {
+    float b[4];
 #pragma unroll
-  for (uint32_t k = 0; k < 4; ++k) {
-    const uint32_t token = token0 + 8u * k + (lane >> 2);
-    if (n == 0 || token >= tokens) continue;
-    float4 v = lds_f4(at + 8u * k * kBufRow);
-    if (e.bias && e.act == DF11_ACT_NONE) v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
-    if (e.mul) v.x *= m[k].x, v.y *= m[k].y, v.z *= m[k].z, v.w *= m[k].w;
-    if (e.res) v.x += r[k].x, v.y += r[k].y, v.z += r[k].z, v.w += r[k].w;
-    if (vec && (e.flags & kOutF32)) {
-      *reinterpret_cast<float4 *>(static_cast<float *>(e.y) + (size_t)token * e.y_stride + row) = v;
-      continue;
+    for (uint32_t j = 0; j < 4; ++j) b[j] = j < n ? load_any(e.bias, row + j, e.flags & kBiasF32) : 0.f;
+#pragma unroll
+    for (uint32_t j = 0; j < 16; ++j) v[j] += b[j & 3u];
+  }
+  activate<8>(v, e.act);
+  activate<8>(v + 8, e.act);
+  if (e.mul) m.each(mul32, [&](uint32_t j, float f) { v[j] *= f; });
+  if (e.res) r.each(res32, [&](uint32_t j, float f) { v[j] += f; });
+  uint8_t *p = static_cast<uint8_t *>(e.y);
+  const size_t i = (size_t)token * e.y_stride + row;
+  p += e.flags & kOutF32 ? 4 * i : 2 * i;
+  const size_t step = e.flags & kOutF32 ? 32ull * e.y_stride : 16ull * e.y_stride;
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k, p += step) {
+    if (!(there >> k & 1u)) continue;
+    const float *q = v + 4 * k;
+    if (e.flags & kOutF32) {
+      float *y = reinterpret_cast<float *>(p);
+      if (VEC) *reinterpret_cast<float4 *>(y) = make_float4(q[0], q[1], q[2], q[3]);
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j)
+        if (!VEC && j < n) y[j] = q[j];
+    } else {
+      uint16_t *y = reinterpret_cast<uint16_t *>(p);
+      if (VEC) *reinterpret_cast<uint2 *>(y) = make_uint2(bf16_pair(q[0], q[1]), bf16_pair(q[2], q[3]));
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j)
+        if (!VEC && j < n) y[j] = (uint16_t)bf16_bits(q[j]);
     }
-    store_any(e, v.x, token, row);
-    if (n > 1) store_any(e, v.y, token, row + 1);
-    if (n > 2) store_any(e, v.z, token, row + 2);
-    if (n > 3) store_any(e, v.w, token, row + 3);
   }
   __syncwarp();  // the buffer may be written again
 }
@@ -1050,7 +1115,8 @@ __device__ __forceinline__ void epilogue_block(const Epilogue &e, uint32_t buf, 
 // SPLIT: a cluster of thread blocks shares a tile, each with a part of the columns of x; the
 // parts' sums meet in shared memory, and each thread block adds a share of the tile's rows
 // of W over the cluster, in order, for the epilogue.
-template <bool SUMS, bool SPLIT>
+// VEC: rows of y, multiplier and residual take 16-byte accesses, and W's end with a group of four.
+template <bool SUMS, bool SPLIT, bool VEC>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     df11_linear_gemm_kernel(const __grid_constant__ CUtensorMap map_x,
                             const __grid_constant__ CUtensorMap map_w,
@@ -1096,76 +1162,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   auto col_begin = [&]() { return SPLIT ? ga.ncg * cluster_rank() / cluster_size() : 0u; };
   auto col_end = [&]() { return SPLIT ? ga.ncg * (cluster_rank() + 1) / cluster_size() : ga.ncg; };
 
-  if (warp == kEpilogueWarps) {
-    const uint32_t elected = elect();
-    uint32_t k = 0, s = 0, par = 0;  // copies so far; the stage, and its uses' parity
-    for (uint32_t tile = first_tile(); tile < ga.tiles && !failed; tile += tile_step()) {
-      const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m;
-      for (uint32_t c = col_begin(); c < col_end(); ++c, ++k) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty(s), par ^ 1u, ga.spin_limit))) {
-          failed = true;
-          break;
-        }
-        const uint32_t dst = base + s * stage_bytes;
-        expect_tx(elected, full(s), ga.x_bytes + bn * 128u);
-        tma_load_2d(elected, dst, &map_x, (int)(64u * c), (int)(tm * kGemmTokens), full(s));
-        tma_load_4d(elected, dst + kXBytes, &map_w, 0, 0, (int)c, (int)(tn * (bn / 16)), full(s));
-        if (++s == S) {
-          s = 0;
-          par ^= 1u;
-        }
-      }
+  constexpr bool kShare = SUMS && !SPLIT;
+  auto leave = [&]() {  // every warp is here before the tensor memory goes
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kEpilogueWarps + 1) {
+      tc_fence_after();
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(ga.tmem_cols)
+                   : "memory");
     }
-    pdl_launch_dependents();
-    // no copy in flight into this thread block's shared memory when it ends
-    for (uint32_t j = k > S ? k - S : 0; j < k; ++j)
-      if (!mbar_wait(full(j % S), (j / S) & 1u, ga.spin_limit)) failed = true;
-    if (failed && lane == 0) report(ga.err, DF11_DEV_ERR_TIMEOUT);
-  } else if (warp == kEpilogueWarps + 1) {
-    // fp32 accumulators, BF16 operands, both K-major
-    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((bn / 8) << 17) |
-                           ((kGemmTokens / 16) << 24);
-    const uint32_t elected = elect();
-    uint32_t k = 0, n = 0, s = 0, par = 0;
-    for (uint32_t tile = first_tile(); tile < ga.tiles && !failed; tile += tile_step()) {
-      uint32_t d = 0;
-      for (uint32_t c = col_begin(); c < col_end(); ++c, ++k) {
-        const uint32_t cb = col_begin(), ce = col_end();
-        const bool first = SUMS ? (c - cb) % kPart == 0 : c == cb;  // into the other accumulator
-        const bool last = c + 1 == ce || (SUMS && (c + 1 - cb) % kPart == 0);
-        if (first) {
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_empty(n & 1), ((n >> 1) & 1u) ^ 1u,
-                                                  ga.spin_limit))) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          d = tmem + (n & 1u) * bn;
-        }
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(full(s), par, ga.spin_limit))) {
-          failed = true;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t ad = sw128_desc(base + s * stage_bytes);
-        const uint64_t bd = sw128_desc(base + s * stage_bytes + kXBytes);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)  // K = 16: 32 bytes on
-          umma(elected, d, ad + 2u * j, bd + 2u * j, idesc, !first || j ? 1u : 0u);
-        umma_commit(elected, empty(s));
-        if (last) umma_commit(elected, acc_full(n & 1));
-        if (last) ++n;
-        if (++s == S) {
-          s = 0;
-          par ^= 1u;
-        }
-      }
-    }
-    // no product in flight when the tensor memory goes
-    for (uint32_t j = k > S ? k - S : 0; j < k; ++j)
-      if (!mbar_wait(empty(j % S), (j / S) & 1u, ga.spin_limit)) failed = true;
-    if (failed && lane == 0) report(ga.err, DF11_DEV_ERR_TIMEOUT);
-  } else {
+  };
+  if (warp < kEpilogueWarps) {
+    if constexpr (kShare) more_registers<kSumRegs>();
     uint32_t n = 0;
     const uint32_t quarter = warp & 3, half = 16u * (warp >> 2);
     const uint32_t lanes = tmem + ((32u * quarter) << 16);
@@ -1187,15 +1196,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t buf = bars + kGemmTail + kBufBytes * warp;
     // the epilogue of the warp's 32 tokens and 16 rows, some of them there
     auto write16 = [&](float (&v)[16], uint32_t token0, uint32_t row) {
-      if (!SUMS && ga.vec && row + 16 <= ga.rows) {
+      if (!SUMS && VEC && row + 16 <= ga.rows) {
         if (token0 + lane < ga.tokens) epilogue16(ga.e, v, token0 + lane, row);
-        return;
-      }
-      const uint32_t p = buf + lane * kBufRow;
+      } else {
+        const uint32_t p = buf + lane * kBufRow;
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j)
-        sts128(p + 16u * j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      epilogue_block(ga.e, buf, token0, row, ga.tokens, ga.rows, SUMS && ga.vec);
+        for (uint32_t j = 0; j < 4; ++j)
+          sts128(p + 16u * j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        epilogue_block<VEC>(ga.e, buf, token0, row, ga.tokens, ga.rows);
+      }
     };
     auto acquire = [&]() {
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full(n & 1), (n >> 1) & 1u, ga.spin_limit)))
@@ -1214,17 +1223,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t token0 = tm * kGemmTokens + 32u * quarter;
       const bool some = token0 < ga.tokens;
       if constexpr (SUMS) {
-        float sum[kSumRows / kColStep][16];
+        // groups of 16 rows of W that a warp has
+        constexpr uint32_t kGroups = ((SPLIT ? kSplitRows : kSumRows) + kColStep - 1) / kColStep;
+        float sum[kGroups][16];
         const uint32_t cb = col_begin();
+#pragma unroll
+        for (uint32_t g = 0; g < kGroups; ++g)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[g][j] = 0.f;
         for (uint32_t c0 = cb; c0 < col_end(); c0 += kPart) {
           if (!acquire()) break;
 #pragma unroll
-          for (uint32_t g = 0; g < kSumRows / kColStep; ++g) {
+          for (uint32_t g = 0; g < kGroups; ++g) {
             if (kColStep * g + half >= bn) break;
             float v[16];
             read16(lanes + (n & 1u) * bn + kColStep * g + half, v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum[g][j] = c0 > cb ? sum[g][j] + v[j] : v[j];
+            for (int j = 0; j < 16; ++j) sum[g][j] += v[j];
           }
           release();
         }
@@ -1232,7 +1247,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if constexpr (SPLIT) {
           // every product is done, so the stages' memory is free: [token][row], 4 rows more
 #pragma unroll
-          for (uint32_t g = 0; g < kSumRows / kColStep; ++g) {
+          for (uint32_t g = 0; g < kGroups; ++g) {
             if (kColStep * g + half >= bn) break;
             const uint32_t p = base + 4u * ((32u * quarter + lane) * (bn + 4u) + kColStep * g + half);
 #pragma unroll
@@ -1240,17 +1255,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               sts128(p + 16u * j, sum[g][4 * j], sum[g][4 * j + 1], sum[g][4 * j + 2], sum[g][4 * j + 3]);
           }
         } else {
-#pragma unroll 1  // one copy of the epilogue
-          for (uint32_t g = 0; some && kColStep * g + half < bn; ++g) {
-            if (tn * bn + kColStep * g + half >= ga.rows) break;
-            float v[16];
+#pragma unroll 1  // one copy of the epilogue, the sums moved to its registers
+          for (uint32_t c = half; some && c < bn && tn * bn + c < ga.rows; c += kColStep) {
+            write16(sum[0], token0, tn * bn + c);
 #pragma unroll
-            for (uint32_t k = 0; k < kSumRows / kColStep; ++k)
-              if (k == g) {
+            for (uint32_t g = 0; g + 1 < kGroups; ++g)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = sum[k][j];
-              }
-            write16(v, token0, tn * bn + kColStep * g + half);
+              for (int j = 0; j < 16; ++j) sum[g][j] = sum[g + 1][j];
           }
         }
       } else {
@@ -1264,6 +1275,81 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
     }
     if (failed && lane == 0) report(ga.err, DF11_DEV_ERR_TIMEOUT);
+    // in the branch: code behind it would have to do with the fewer registers
+    if constexpr (kShare) leave();
+  } else {  // one group of four warps, two of them without work
+    if constexpr (kShare) fewer_registers<kIssueRegs>();
+    if (warp == kEpilogueWarps) {
+      const uint32_t elected = elect();
+      uint32_t k = 0, s = 0, par = 0;  // copies so far; the stage, and its uses' parity
+      for (uint32_t tile = first_tile(); tile < ga.tiles && !failed; tile += tile_step()) {
+        const uint32_t tn = tile / ga.tiles_m, tm = tile - tn * ga.tiles_m;
+        for (uint32_t c = col_begin(); c < col_end(); ++c, ++k) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty(s), par ^ 1u, ga.spin_limit))) {
+            failed = true;
+            break;
+          }
+          const uint32_t dst = base + s * stage_bytes;
+          expect_tx(elected, full(s), ga.x_bytes + bn * 128u);
+          tma_load_2d(elected, dst, &map_x, (int)(64u * c), (int)(tm * kGemmTokens), full(s));
+          tma_load_4d(elected, dst + kXBytes, &map_w, 0, 0, (int)c, (int)(tn * (bn / 16)), full(s));
+          if (++s == S) {
+            s = 0;
+            par ^= 1u;
+          }
+        }
+      }
+      pdl_launch_dependents();
+      // no copy in flight into this thread block's shared memory when it ends
+      for (uint32_t j = k > S ? k - S : 0; j < k; ++j)
+        if (!mbar_wait(full(j % S), (j / S) & 1u, ga.spin_limit)) failed = true;
+      if (failed && lane == 0) report(ga.err, DF11_DEV_ERR_TIMEOUT);
+    } else if (warp == kEpilogueWarps + 1) {
+      // fp32 accumulators, BF16 operands, both K-major
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((bn / 8) << 17) |
+                             ((kGemmTokens / 16) << 24);
+      const uint32_t elected = elect();
+      uint32_t k = 0, n = 0, s = 0, par = 0;
+      for (uint32_t tile = first_tile(); tile < ga.tiles && !failed; tile += tile_step()) {
+        uint32_t d = 0;
+        for (uint32_t c = col_begin(); c < col_end(); ++c, ++k) {
+          const uint32_t cb = col_begin(), ce = col_end();
+          const bool first = SUMS ? (c - cb) % kPart == 0 : c == cb;  // into the other accumulator
+          const bool last = c + 1 == ce || (SUMS && (c + 1 - cb) % kPart == 0);
+          if (first) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_empty(n & 1), ((n >> 1) & 1u) ^ 1u,
+                                                    ga.spin_limit))) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+            d = tmem + (n & 1u) * bn;
+          }
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(full(s), par, ga.spin_limit))) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = sw128_desc(base + s * stage_bytes);
+          const uint64_t bd = sw128_desc(base + s * stage_bytes + kXBytes);
+  #pragma unroll
+          for (int j = 0; j < 4; ++j)  // K = 16: 32 bytes on
+            umma(elected, d, ad + 2u * j, bd + 2u * j, idesc, !first || j ? 1u : 0u);
+          umma_commit(elected, empty(s));
+          if (last) umma_commit(elected, acc_full(n & 1));
+          if (last) ++n;
+          if (++s == S) {
+            s = 0;
+            par ^= 1u;
+          }
+        }
+      }
+      // no product in flight when the tensor memory goes
+      for (uint32_t j = k > S ? k - S : 0; j < k; ++j)
+        if (!mbar_wait(empty(j % S), (j / S) & 1u, ga.spin_limit)) failed = true;
+      if (failed && lane == 0) report(ga.err, DF11_DEV_ERR_TIMEOUT);
+    }
+    if constexpr (kShare) leave();
   }
   if constexpr (SPLIT) {
     cluster_sync();
@@ -1290,19 +1376,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (uint32_t k = 0; k < 4; ++k)
           sts128(buf + (8u * k + (lane >> 2)) * kBufRow + 16u * (lane & 3u), sum[k].x, sum[k].y, sum[k].z,
                  sum[k].w);
-        epilogue_block(ga.e, buf, tm * kGemmTokens + t0, tn * bn + c0, ga.tokens, ga.rows, ga.vec);
+        epilogue_block<VEC>(ga.e, buf, tm * kGemmTokens + t0, tn * bn + c0, ga.tokens, ga.rows);
       }
     }
     cluster_sync();  // nobody reads this thread block's sums any more
   }
-  // every warp is here before the tensor memory goes
-  tc_fence_before();
-  __syncthreads();
-  if (warp == kEpilogueWarps + 1) {
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(ga.tmem_cols)
-                 : "memory");
-  }
+  if constexpr (!kShare) leave();
 }
 
 // ---- host side ------------------------------------------------------------------
@@ -1618,6 +1697,14 @@ EncodeTiled encode_tiled() {
   return f;
 }
 
+using GemmKernel = void (*)(CUtensorMap, CUtensorMap, GemmArgs);
+// variant: one chain per tile, sums in parts, tiles shared by a cluster
+GemmKernel pick_gemm(int variant, bool vec) {
+  if (variant == 2) return vec ? df11_linear_gemm_kernel<true, true, true> : df11_linear_gemm_kernel<true, true, false>;
+  if (variant == 1) return vec ? df11_linear_gemm_kernel<true, false, true> : df11_linear_gemm_kernel<true, false, false>;
+  return vec ? df11_linear_gemm_kernel<false, false, true> : df11_linear_gemm_kernel<false, false, false>;
+}
+
 df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, const uint16_t *w,
                         const Activations &x, int32_t *d_err, cudaStream_t s) {
   const EncodeTiled encode = encode_tiled();
@@ -1636,7 +1723,7 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
   auto vec_ok = [](const void *p, uint32_t stride, int32_t type) {
     return !p || (aligned(p, 16) && stride * type_bytes(type) % 16 == 0);
   };
-  ga.vec = vec_ok(op.y, op.y_stride, op.y_type) &&
+  const bool vec = rows % 4 == 0 && vec_ok(op.y, op.y_stride, op.y_type) &&
            vec_ok(op.multiplier, op.multiplier_stride, op.multiplier_type) &&
            vec_ok(op.residual, op.residual_stride, op.residual_type);
   // The tile width and the number of thread blocks that share a tile for which the rounds over
@@ -1645,10 +1732,10 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
   // shared one 10000 more.  The wider and less shared one of two.  (500 x 8192 and 40 tokens:
   // 12 us with shared tiles, 27 without; 4096 x 4096 and 256 tokens: 25 and 19.)
   uint64_t cost = ~0ull;
-  const bool sums = ga.ncg > (op.y_type == DF11_F32 ? kPart : kPlainSteps);
+  const bool sums = ga.ncg > kPart;
   uint32_t split = 1;
   for (uint32_t ctas = 1; ctas <= 8; ctas *= 2) {
-    for (uint32_t bn = ctas > 1 ? 128 : (sums ? kSumRows : 256); bn >= 16 * ctas; bn -= 16 * ctas) {
+    for (uint32_t bn = ctas > 1 ? kSplitRows : (sums ? kSumRows : 256); bn >= 16 * ctas; bn -= 16 * ctas) {
       const uint64_t tiles = (uint64_t)ga.tiles_m * ((rows + bn - 1) / bn);
       // whole clusters do not reach every SM
       if (ctas > 1 && (tiles * ctas > (uint64_t)sms * 7 / 8 || ga.ncg < 4 * ctas)) break;
@@ -1663,7 +1750,7 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
     }
   }
   ga.stages = kMaxStages;
-  const bool buffers = sums || split > 1 || !ga.vec || rows % 16;
+  const bool buffers = sums || split > 1 || !vec || rows % 16;
   while (gemm_smem(ga.bn, ga.stages, buffers) > 226 * 1024) --ga.stages;
   ga.tmem_cols = 32;
   while (ga.tmem_cols < 2 * ga.bn) ga.tmem_cols *= 2;
@@ -1693,10 +1780,9 @@ df11_status launch_gemm(const df11_linear &op, uint32_t rows, uint32_t cols, con
   }
   const size_t smem = gemm_smem(ga.bn, ga.stages, buffers);
   uint64_t budget = 0;
-  void (*kern)(CUtensorMap, CUtensorMap, GemmArgs) =
-      split > 1 ? df11_linear_gemm_kernel<true, true>
-                : (sums ? df11_linear_gemm_kernel<true, false> : df11_linear_gemm_kernel<false, false>);
-  const df11_status st = prepare(kern, kGemmThreads, smem, split > 1 ? 77 : (sums ? 75 : 76), budget);
+  const int variant = split > 1 ? 2 : (sums ? 1 : 0);
+  const GemmKernel kern = pick_gemm(variant, vec);
+  const df11_status st = prepare(kern, kGemmThreads, smem, 73 + 2 * variant + vec, budget);
   if (st != DF11_OK) return st;
   if (split > 1)
     return launch_cluster(kern, ga.tiles * split, split, kGemmThreads, smem, s, mx, mw, ga);
