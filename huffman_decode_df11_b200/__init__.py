@@ -160,6 +160,10 @@ def lib():
     L.df11_decode_linear.restype = ctypes.c_int
     L.df11_linear_workspace.argtypes = [vp, vp, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
     L.df11_linear_workspace.restype = ctypes.c_int
+    L.df11_capture_id.argtypes = [vp]
+    L.df11_capture_id.restype = ctypes.c_uint64
+    L.df11_event_done.argtypes = [vp]
+    L.df11_event_done.restype = ctypes.c_int
     L.df11_linear_sizes.argtypes = [u32, u32, ctypes.POINTER(u64), ctypes.POINTER(u64)]
     L.df11_linear_sizes.restype = ctypes.c_int
     L.df11_linear_weight_begin.argtypes = [vp, u32, u32, vp, vp, vp, vp]

@@ -1946,6 +1946,26 @@ df11_status df11_linear_workspace(const df11_linear_weight *weights, const df11_
   return st;
 }
 
+uint64_t df11_capture_id(df11_stream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo((cudaStream_t)stream, &status, &id) != cudaSuccess) {
+    (void)cudaGetLastError();  // the legacy stream beside a capture: not in one
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusNone ? 0 : id;
+}
+
+int df11_event_done(void *event) {
+  if (!event) return -1;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return -1;
+  const cudaError_t e = cudaEventQuery(static_cast<cudaEvent_t>(event));
+  (void)cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) (void)cudaGetLastError();  // clear this call's (non-sticky) error
+  return e == cudaSuccess ? 1 : (e == cudaErrorNotReady ? 0 : -1);
+}
+
 df11_status df11_decode_linear(const df11_linear_weight *weights, const df11_linear *ops, int count,
                                void *workspace, size_t workspace_bytes, int32_t *d_err,
                                df11_stream_t stream) {

@@ -221,7 +221,11 @@ class LinearPlan:
     or more.  A residual may be the output itself; no weight's output may be what
     another one reads, since they run at the same time.  Runs of one plan share its
     workspace and must not overlap on the GPU, graphs that captured them
-    included; for several streams at once, make a plan for each."""
+    included; for several streams at once, make a plan for each.  The first run on a
+    stream other than the one the plan was made on, or a captured one, is ordered
+    behind the work that was queued there by then (the workspace's memory may have
+    been in use by it).  A graph that captured a run keeps neither the plan nor its
+    workspace alive: the plan has to outlive the graph, like the buffers."""
 
     def __init__(self, ds: Sequence[LinearWeight], xs: Sequence[torch.Tensor],
                  ys: Sequence[torch.Tensor], biases=None, activations=None, multipliers=None,
@@ -246,8 +250,19 @@ class LinearPlan:
                                                        ctypes.byref(size)),
                        "df11_linear_workspace")
                 self._work = _aligned_empty(size.value, self._device)
-                self._streams = {_stream_handle(None)}  # that the allocator knows of
+                self._streams = {_stream_handle(None)}  # ordered behind, and known to the allocator
+                self._mark()
         self._bytes = size.value
+
+    _born = None
+
+    def _mark(self):
+        """An event behind all that may still use the workspace's memory as somebody else's,
+        until that is known to be done.  Not external in a capture: only its own streams
+        can wait for it, and later runs are the graph's users' to order."""
+        self._capture = self._lib.df11_capture_id(_stream_handle(None))
+        self._born = torch.cuda.Event(external=not self._capture)
+        self._born.record()
 
     @property
     def outs(self) -> List[torch.Tensor]:
@@ -257,6 +272,21 @@ class LinearPlan:
     def workspace_bytes(self) -> int:
         return self._bytes
 
+    def _enter(self, handle):
+        """What a run on a stream needs before it, as long as anything does."""
+        s, capture = _on_stream(handle), self._lib.df11_capture_id(handle)
+        if self._born is not None and (capture != self._capture if self._capture else
+                                       self._lib.df11_event_done(self._born.cuda_event) == 1):
+            self._born = None  # over, for every stream and graph
+        # a graph may be replayed on any stream, so a captured run waits by itself
+        if self._born is not None and (handle not in self._streams or
+                                       capture and not self._capture):
+            s.wait_event(self._born)
+        if not capture and handle not in self._streams:
+            # a plan dropped while it runs there keeps its workspace until that is done
+            self._work.record_stream(s)
+            self._streams.add(handle)
+
     def run(self, err: Optional[torch.Tensor] = None, stream=None) -> List[torch.Tensor]:
         if not self._n:
             return self._keep[2]
@@ -264,15 +294,20 @@ class LinearPlan:
             with torch.cuda.device(self._device):
                 return self.run(err, stream)
         handle = _stream_handle(stream)
-        if handle not in self._streams and not torch.cuda.is_current_stream_capturing():
-            # a plan dropped while it runs there keeps its workspace until that is done
-            self._work.record_stream(_on_stream(handle))
-            self._streams.add(handle)
+        if self._born is not None or handle not in self._streams:
+            self._enter(handle)
         _check(self._lib.df11_decode_linear(self._descs, self._ops, self._n,
                                             self._work.data_ptr(), self._bytes,
                                             err.data_ptr() if err is not None else None, handle),
                "df11_decode_linear")
         return self._keep[2]
+
+
+class _OneRun(LinearPlan):
+    """A plan that runs once, on the stream it is made on."""
+
+    def _mark(self):
+        pass
 
 
 def _on_stream(stream):
@@ -303,4 +338,4 @@ def decode_linear(ds: Sequence[LinearWeight], xs: Sequence[torch.Tensor],
             ys = [torch.empty(x.shape[0], d.shape[0], dtype=out_dtype, device=d.device)
                   for d, x in zip(ds, xs)]
         # the workspace is allocated and freed in the order of the call's stream
-        return LinearPlan(ds, xs, ys, biases, activations, multipliers, residuals).run(err, stream)
+        return _OneRun(ds, xs, ys, biases, activations, multipliers, residuals).run(err, stream)

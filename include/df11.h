@@ -368,6 +368,14 @@ df11_status df11_decode_linear(const df11_linear_weight *weights, const df11_lin
 df11_status df11_linear_workspace(const df11_linear_weight *weights, const df11_linear *ops,
                                   int count, size_t *bytes);
 
+/* For a program that keeps a workspace and runs it on several streams or in graphs, and so
+ * has to know when the earlier use of its memory is over.  df11_event_done: whether the work
+ * recorded before a CUDA event (cudaEvent_t) is done: 1 or 0, -1 for an event that cannot
+ * be asked; unlike cudaEventQuery it may be called while streams are captured.
+ * df11_capture_id: the capture that a stream is in, 0 for none. */
+uint64_t df11_capture_id(df11_stream_t stream);
+int df11_event_done(void *event);
+
 /* ---------------------------------------------------------------------- */
 /* The token embedding on a compressed table, and the table's gradient.    */
 
