@@ -25,6 +25,39 @@ inline uint32_t stage_bytes_for(uint32_t max_block_elems) {
 
 inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// `count` rows of `bytes` bytes, `stride` bytes apart, that do not overlap one another
+struct Rows {
+  const void *p;
+  uint64_t count, bytes, stride;
+};
+
+// whether two sets of rows share a byte (columns of one buffer, say, do not)
+inline bool share_memory(Rows a, Rows b) {
+  if (!a.p || !b.p || !a.count || !b.count) return false;
+  const uint64_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  if (x >= y + (b.count - 1) * b.stride + b.bytes || y >= x + (a.count - 1) * a.stride + a.bytes)
+    return false;
+  if (a.count == 1) a.stride = b.stride;
+  if (b.count == 1) b.stride = a.stride;
+  if (a.count == 1 && b.count == 1) return true;
+  if (a.stride == b.stride) {
+    // a's row i starts r behind b's row q + i, and reaches the one after it or not
+    const int64_t s = (int64_t)a.stride, d = (int64_t)(x - y);
+    const int64_t q = d >= 0 ? d / s : -((s - 1 - d) / s), r = d - q * s;
+    const int64_t na = (int64_t)a.count, nb = (int64_t)b.count;
+    auto meet = [&](int64_t first) {  // some row i of a and row first + i of b
+      return (first < 0 ? -first : 0) < (na < nb - first ? na : nb - first);
+    };
+    return (r < (int64_t)b.bytes && meet(q)) || (r + (int64_t)a.bytes > s && meet(q + 1));
+  }
+  for (uint64_t i = 0; i < a.count; ++i) {  // the row of b at or before the row of a, and the next
+    const uint64_t lo = x + i * a.stride, j = lo > y ? (lo - y) / b.stride : 0;
+    for (uint64_t k = j; k < b.count && k <= j + 1; ++k)
+      if (lo < y + k * b.stride + b.bytes && y + k * b.stride < lo + a.bytes) return true;
+  }
+  return false;
+}
+
 inline df11_status validate(const df11_tensor &t) {
   const df11_params &p = t.params;
   if (p.n == 0) return DF11_OK;

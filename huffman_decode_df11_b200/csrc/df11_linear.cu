@@ -1574,6 +1574,21 @@ df11_status check_op(const df11_linear_weight &w, const df11_linear &op) {
   return DF11_OK;
 }
 
+// y is written while other thread blocks still read x, the bias and the rows of the other
+// operands; those may be y itself, since every element is read by the thread that writes it.
+bool output_is_read(const df11_linear_weight &w, const df11_linear &op) {
+  const uint64_t rows = w.params.rows, yb = type_bytes(op.y_type);
+  const Rows y{op.y, op.batch, rows * yb, op.y_stride * yb};
+  if (share_memory(y, Rows{op.x, op.batch, 2ull * w.params.cols, 2ull * op.x_stride})) return true;
+  if (share_memory(y, Rows{op.bias, 1, rows * type_bytes(op.bias_type), 0})) return true;
+  auto other = [&](const void *p, uint64_t stride, int32_t type) {
+    if (p == op.y && type == op.y_type && (op.batch == 1 || stride == op.y_stride)) return false;
+    return share_memory(y, Rows{p, op.batch, rows * type_bytes(type), stride * type_bytes(type)});
+  };
+  return other(op.multiplier, op.multiplier_stride, op.multiplier_type) ||
+         other(op.residual, op.residual_stride, op.residual_type);
+}
+
 df11_status check_call(const df11_linear_weight *ws, const df11_linear *ops, int count) {
   if (count < 0) return DF11_ERR_INVALID;
   if (count && (!ws || !ops)) return DF11_ERR_NULL;
@@ -1938,6 +1953,8 @@ df11_status df11_linear_workspace(const df11_linear_weight *weights, const df11_
   size_t most = 0;
   st = for_groups(weights, ops, count, [&](const df11_linear_weight *w, const df11_linear *o, int m) {
     Plan pl;
+    for (int i = 0; i < m; ++i)
+      if (output_is_read(w[i], o[i])) return DF11_ERR_INVALID;
     const df11_status r = make_plan(w, o, m, pl);
     if (r == DF11_OK && pl.bytes > most) most = pl.bytes;
     return r;
@@ -1976,6 +1993,8 @@ df11_status df11_decode_linear(const df11_linear_weight *weights, const df11_lin
   // checked for every group before anything is queued
   st = for_groups(weights, ops, count, [&](const df11_linear_weight *w, const df11_linear *o, int m) {
     Plan pl;
+    for (int i = 0; i < m; ++i)
+      if (output_is_read(w[i], o[i])) return DF11_ERR_INVALID;
     df11_status r = make_plan(w, o, m, pl);
     if (r != DF11_OK) return r;
     if (!workspace) return DF11_ERR_NULL;

@@ -23,6 +23,7 @@ LINEAR_MAX_BATCH = 1 << 20
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
+_INVALID = 7  # DF11_ERR_INVALID
 
 
 class LinearParams(ctypes.Structure):
@@ -218,8 +219,9 @@ class LinearPlan:
     (tokens x rows): per weight a float32 or BF16 tensor or None.
     `activations`: per weight "none", "relu", "gelu", "gelu_tanh" or "silu".
     Rows of all of them must be contiguous, at any distance of a row's length
-    or more.  A residual may be the output itself; no weight's output may be what
-    another one reads, since they run at the same time.  Runs of one plan share its
+    or more.  A multiplier or a residual may be the output itself (the same rows and
+    type); otherwise no output may share memory with what its own weight reads (refused) or
+    another one does, since they run at the same time.  Runs of one plan share its
     workspace and must not overlap on the GPU, graphs that captured them
     included; for several streams at once, make a plan for each.  The first run on a
     stream other than the one the plan was made on, or a captured one, is ordered
@@ -246,9 +248,12 @@ class LinearPlan:
         size = ctypes.c_size_t(0)
         if n:
             with torch.cuda.device(self._device):
-                _check(self._lib.df11_linear_workspace(self._descs, self._ops, n,
-                                                       ctypes.byref(size)),
-                       "df11_linear_workspace")
+                status = self._lib.df11_linear_workspace(self._descs, self._ops, n,
+                                                         ctypes.byref(size))
+                if status == _INVALID:  # what is left of that after _linear_op
+                    raise ValueError("an output shares memory with its weight's x, bias, "
+                                     "multiplier or residual")
+                _check(status, "df11_linear_workspace")
                 self._work = _aligned_empty(size.value, self._device)
                 self._streams = {_stream_handle(None)}  # ordered behind, and known to the allocator
                 self._mark()

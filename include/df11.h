@@ -349,13 +349,14 @@ typedef struct df11_linear {
  * the workspace and multiplied on the tensor cores.
  *   `workspace`: df11_linear_workspace bytes of device memory, 256-byte aligned,
  * that no other work uses until this call's work is done; nothing is kept in
- * it between calls.  y may not overlap x, the multiplier (unless it is the same
- * memory with the same stride and type), the workspace or what another weight of the
- * call reads or writes: the weights of a call run at the same time.
+ * it between calls.  y may not overlap x, the bias, the multiplier or the residual
+ * (unless those two are the same memory with the same stride and type; refused), nor the
+ * workspace or what another weight of the call reads or writes: the weights of a call
+ * run at the same time.
  *   Same conventions as df11_decode_batched otherwise (asynchronous, no
  * allocation, device-detected errors in d_err).  DF11_ERR_INVALID for sizes,
- * strides, types or activations outside the rules and for a workspace that is
- * too small, DF11_ERR_FORMAT for parameters that no weight has,
+ * strides, types or activations outside the rules, for an output that its own operands
+ * overlap and for a workspace that is too small, DF11_ERR_FORMAT for parameters that no weight has,
  * DF11_ERR_TOO_LARGE above DF11_LINEAR_MAX_BATCH.
  */
 df11_status df11_decode_linear(const df11_linear_weight *weights, const df11_linear *ops, int count,
