@@ -1716,7 +1716,8 @@ df11_status df11_build_decode_table(const uint32_t *luts, const uint8_t *code_le
   if (st != DF11_OK) return st;
   df11_table_kernel<<<1, 256, 0, (cudaStream_t)stream>>>(luts, code_lengths, num_luts,
                                                            reinterpret_cast<uint4 *>(out));
-  return cudaGetLastError() == cudaSuccess ? DF11_OK : DF11_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return DF11_ERR_CUDA;
+  return queue_after_writes((cudaStream_t)stream);  // a decode may be the next launch
 }
 
 df11_status df11_test_withhold_copies(int launches, uint32_t spin_limit) {

@@ -169,6 +169,15 @@ df11_status launch_pdl(void (*kern)(Args...), dim3 grid, uint32_t threads, size_
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DF11_OK : DF11_ERR_CUDA;
 }
 
+// After a kernel that writes what the library's launches read before they wait for the previous
+// kernel (streams, decode tables): a kernel that does nothing, launched plainly, starts when
+// those writes are done and visible, and is the one that a launch above may overlap.
+static __global__ void after_writes_kernel() {}
+inline df11_status queue_after_writes(cudaStream_t s) {
+  after_writes_kernel<<<1, 32, 0, s>>>();
+  return cudaGetLastError() == cudaSuccess ? DF11_OK : DF11_ERR_CUDA;
+}
+
 // The same for a grid of clusters of `ctas` thread blocks (at most 8).
 template <typename... Args>
 df11_status launch_cluster(void (*kern)(Args...), uint32_t grid, uint32_t ctas, uint32_t threads,

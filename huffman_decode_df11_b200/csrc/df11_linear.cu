@@ -1929,7 +1929,8 @@ df11_status df11_linear_weight_finish(const uint16_t *d_w, const df11_linear_wei
   a.streams = const_cast<uint32_t *>(weight->streams);
   a.sign_mantissa = const_cast<uint8_t *>(weight->sign_mantissa);
   linear_encode_kernel<true><<<encode_grid(a), 256, 0, (cudaStream_t)stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? DF11_OK : DF11_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return DF11_ERR_CUDA;
+  return queue_after_writes((cudaStream_t)stream);  // a product may be the next launch
 }
 
 df11_status df11_linear_unpack(const df11_linear_weight *weight, uint16_t *tiles, int32_t *d_err,

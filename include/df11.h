@@ -307,7 +307,8 @@ df11_status df11_linear_sizes(uint32_t rows, uint32_t cols, uint64_t *unit_rows_
  * faster).  The first call counts the exponents, computes the code, writes
  * unit_rows and the table (device buffers, sizes above) and fills *params; it
  * synchronises the stream.  The second one, with a weight whose buffers have the
- * sizes that params gives, writes streams and sign_mantissa, asynchronously.
+ * sizes that params gives, writes streams and sign_mantissa, asynchronously; the next
+ * launch in the stream may be one that reads them.
  * DF11_ERR_INVALID for an empty matrix, DF11_ERR_TOO_LARGE for 2^32 elements or
  * more after padding.
  */
@@ -319,7 +320,8 @@ df11_status df11_linear_weight_finish(const uint16_t *d_w, const df11_linear_wei
 
 /* Decode a weight into its tiles (BF16, bit-identical): for each block of 16 rows
  * and each group of 64 columns the 16 rows' 64 elements one after another, padding
- * included.  `tiles`: 16-byte aligned device memory.  Asynchronous. */
+ * included.  `tiles`: 16-byte aligned device memory.  Asynchronous; what holds for the
+ * weight in df11_decode_linear holds here. */
 df11_status df11_linear_unpack(const df11_linear_weight *weight, uint16_t *tiles, int32_t *d_err,
                                df11_stream_t stream);
 
@@ -354,7 +356,9 @@ typedef struct df11_linear {
  * workspace or what another weight of the call reads or writes: the weights of a call
  * run at the same time.
  *   Same conventions as df11_decode_batched otherwise (asynchronous, no
- * allocation, device-detected errors in d_err).  DF11_ERR_INVALID for sizes,
+ * allocation, device-detected errors in d_err; the weight may not be written by the previous
+ * kernel in the stream unless it is df11_linear_weight_finish, which sees to the order; x
+ * and the other operands may).  DF11_ERR_INVALID for sizes,
  * strides, types or activations outside the rules, for an output that its own operands
  * overlap and for a workspace that is too small, DF11_ERR_FORMAT for parameters that no weight has,
  * DF11_ERR_TOO_LARGE above DF11_LINEAR_MAX_BATCH.
@@ -404,7 +408,7 @@ typedef struct df11_embedding {
  * d_err.  Needs chunk counts, a decode table, T = 256 and C = 8, 16 or 24;
  * out_bf16 of the tensor is not used (may be NULL).  Same conventions as
  * df11_decode_batched otherwise; the ids may be written by the previous kernel in
- * the stream.
+ * the stream, the table's buffers may not (df11_build_decode_table sees to the order).
  */
 df11_status df11_decode_embedding(const df11_tensor *table, const df11_embedding *op,
                                   int32_t *d_err, df11_stream_t stream);
@@ -448,7 +452,7 @@ df11_status df11_embedding_gradient_workspace(const df11_embedding_grad *op, siz
  * exponent byte rotated right by one bit, and a table of 2^11 entries each
  * holding the codewords that lie wholly inside an 11-bit window.  Passing it
  * in df11_tensor.decode_table saves every thread block of every decode call
- * from deriving it.  Asynchronous on `stream`; DF11_ERR_NULL / _ALIGN /
+ * from deriving it.  Asynchronous on `stream`, and a decode may be the next launch there; DF11_ERR_NULL / _ALIGN /
  * _FORMAT (num_luts outside 1 .. 2^24-1) are returned before anything is
  * queued.
  */
