@@ -186,20 +186,21 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (uint64_t item = blockIdx.x + (uint64_t)gridDim.x * group; item < items;
        item += (uint64_t)gridDim.x * kWarps * kGroups) {
     const uint32_t token = (uint32_t)(item / a.segs), seg = (uint32_t)(item - (uint64_t)token * a.segs);
-    const uint32_t c_first = seg * a.seg_len, c_last = min(c_first + a.seg_len, a.dim);
+    // offsets within the segment, since a row's end may be next to 2^32
+    const uint32_t c_first = seg * a.seg_len, c_count = min(a.seg_len, a.dim - c_first);
     const int64_t id = a.ids64 ? static_cast<const int64_t *>(a.ids)[token]
                                : static_cast<const int32_t *>(a.ids)[token];
     const size_t out0 = (size_t)token * a.out_stride;
     if (id < 0 || id >= (int64_t)a.rows) {
       if (lane == 0) report(a.err, DF11_DEV_ERR_INDEX);
-      for (uint32_t c = c_first + lane; c < c_last; c += G) {
-        if (a.out_f32) static_cast<float *>(a.out)[out0 + c] = 0.f;
-        else static_cast<uint16_t *>(a.out)[out0 + c] = 0;
+      for (uint32_t c = lane; c < c_count; c += G) {
+        if (a.out_f32) static_cast<float *>(a.out)[out0 + c_first + c] = 0.f;
+        else static_cast<uint16_t *>(a.out)[out0 + c_first + c] = 0;
       }
       continue;
     }
     const uint32_t row0 = (uint32_t)id * a.dim;  // elements of a tensor: below 2^32
-    const uint32_t e0 = row0 + c_first, e1 = row0 + c_last;
+    const uint32_t e0 = row0 + c_first, e1 = e0 + c_count;
     uint32_t P, chunk0;
     const uint32_t b = G == 32 ? find_block(tk, e0, lane, P) : find_block_alone(tk, e0, P);
     if (P > e0) {  // inconsistent positions
@@ -893,6 +894,8 @@ uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 bool known_type(int32_t t) { return t == DF11_BF16 || t == DF11_F32; }
 uintptr_t type_bytes(int32_t t) { return t == DF11_F32 ? 4 : 2; }
 
+constexpr uint64_t kMaxSegment = 1u << 31;  // elements: loops over a segment's stay below 2^32
+
 // `per_pass`: elements of a row that G chunks hold on average
 template <int C, int G>
 df11_status launch_embedding(EmbedArgs &a, uint64_t per_pass, int instance, cudaStream_t s) {
@@ -911,8 +914,9 @@ df11_status launch_embedding(EmbedArgs &a, uint64_t per_pass, int instance, cuda
   const uint64_t most = (a.dim + per_pass - 1) / per_pass;
   uint64_t segs = budget * groups / a.tokens;
   segs = segs < 1 || G < 32 ? 1 : (segs > most ? most : segs);
-  a.seg_len = (uint32_t)round_up((a.dim + segs - 1) / segs, 16);
-  a.segs = (a.dim + a.seg_len - 1) / a.seg_len;
+  const uint64_t len = round_up((a.dim + segs - 1) / segs, 16);
+  a.seg_len = (uint32_t)(len < kMaxSegment ? len : kMaxSegment);
+  a.segs = (uint32_t)(((uint64_t)a.dim + a.seg_len - 1) / a.seg_len);
   // every SM, then every warp of a thread block, then more thread blocks per SM
   const uint64_t items = (uint64_t)a.tokens * a.segs;
   uint64_t grid = (items + groups - 1) / groups;
