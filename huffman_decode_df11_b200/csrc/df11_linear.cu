@@ -106,16 +106,21 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 
 // The activations in fp32.  gelu through the complementary error function and
 // the tanh form as a logistic function: neither loses digits in the negative
-// tail, where 1 + erf and 1 + tanh cancel.  The quotients take the approximate division (two
-// units in the last place; divisors here are at least 1, and beyond 2^126 it gives the zero that
-// the quotient is next to): the exact one is half of an epilogue's instructions.
+// tail, where 1 + erf and 1 + tanh cancel.  v / (1 + exp(-t)) is written with exp(-|t|), so that the
+// divisor is between 1 and 2, where the approximate division is within two units in the last
+// place (the exact one is half of an epilogue's instructions; beyond 2^126 the approximate one
+// gives zero, where silu(-88) is still a normal number).
 __device__ __forceinline__ float relu(float v) { return v < 0.f ? 0.f : v; }  // NaN stays
 __device__ __forceinline__ float gelu(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
+__device__ __forceinline__ float logistic(float v, float t) {
+  const float e = expf(-0.5f * fabsf(t));  // squared where it is used: exp(-|t|) loses digits below 2^-126
+  return __fdividef(t < 0.f ? v * e * e : v, 1.f + e * e);
+}
 __device__ __forceinline__ float gelu_tanh(float v) {
   const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
-  return __fdividef(v, 1.f + expf(-2.f * u));
+  return logistic(v, 2.f * u);
 }
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + expf(-v)); }
+__device__ __forceinline__ float silu(float v) { return logistic(v, v); }
 // one branch for all values, so that their chains of instructions run side by side
 template <int N>
 __device__ __forceinline__ void activate(float *v, uint32_t act) {
