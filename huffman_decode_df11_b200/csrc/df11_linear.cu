@@ -677,6 +677,7 @@ struct PackWeight {
   uint32_t *streams;
   uint8_t *sign_mantissa;
   uint32_t rows, cols, rbs, ncg, upr;
+  uint32_t stream_rows;    // that `streams` has
   uint32_t vec;            // rows of the weight on 16-byte boundaries
 };
 
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(256) linear_encode_kernel(const __grid_constan
     const uint32_t cg0 = ku * kUnitTiles, cg1 = min(cg0 + kUnitTiles, a.ncg);
     uint32_t bits = 0;
     uint32_t row = WRITE ? a.unit_rows[u] : 0u;
-    const uint32_t end = WRITE ? a.unit_rows[u + 1] : 0u;
+    const uint32_t end = WRITE ? min(a.unit_rows[u + 1], a.stream_rows) : 0u;
     uint64_t buf = 0;  // the next bits, `bits` of them
     for (uint32_t cg = cg0; cg < cg1; ++cg) {
 #pragma unroll 1
@@ -739,7 +740,8 @@ __global__ void __launch_bounds__(256) linear_encode_kernel(const __grid_constan
             buf |= (uint64_t)code_s[exp] << bits;
             bits += len_s[exp];
             if (bits >= 32) {
-              a.streams[(size_t)row * 32u + lane] = (uint32_t)buf;
+              // within the unit's rows, even if the words are not those that were counted
+              if (row < end) a.streams[(size_t)row * 32u + lane] = (uint32_t)buf;
               ++row;
               buf >>= 32;
               bits -= 32;
@@ -1932,6 +1934,7 @@ df11_status df11_linear_weight_finish(const uint16_t *d_w, const df11_linear_wei
   PackWeight a = pack_weight(d_w, weight->params, const_cast<uint32_t *>(weight->unit_rows),
                              weight->table);
   a.streams = const_cast<uint32_t *>(weight->streams);
+  a.stream_rows = weight->params.stream_rows;
   a.sign_mantissa = const_cast<uint8_t *>(weight->sign_mantissa);
   linear_encode_kernel<true><<<encode_grid(a), 256, 0, (cudaStream_t)stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return DF11_ERR_CUDA;

@@ -307,8 +307,9 @@ df11_status df11_linear_sizes(uint32_t rows, uint32_t cols, uint64_t *unit_rows_
  * faster).  The first call counts the exponents, computes the code, writes
  * unit_rows and the table (device buffers, sizes above) and fills *params; it
  * synchronises the stream.  The second one, with a weight whose buffers have the
- * sizes that params gives, writes streams and sign_mantissa, asynchronously; the next
- * launch in the stream may be one that reads them.
+ * sizes that params gives, writes streams and sign_mantissa from the same words,
+ * asynchronously; the next launch in the stream may be one that reads them.  (Other words
+ * than those counted give a weight that decodes wrongly, but no write past its buffers.)
  * DF11_ERR_INVALID for an empty matrix, DF11_ERR_TOO_LARGE for 2^32 elements or
  * more after padding.
  */
