@@ -1065,6 +1065,10 @@ df11_status df11_decode_embedding(const df11_tensor *table, const df11_embedding
   if (!table->chunk_counts || !table->decode_table || p.threads_per_block != kT ||
       (p.chunk_bytes != 8 && p.chunk_bytes != 16 && p.chunk_bytes != 24))
     return DF11_ERR_UNSUPPORTED;
+  const uint64_t ob = type_bytes(op->out_type), ib = op->ids_type == DF11_IDS_I64 ? 8 : 4;
+  if (share_memory(Rows{op->out, op->tokens, op->dim * ob, op->out_stride * ob},
+                   Rows{op->ids, 1, op->tokens * ib, 0}))
+    return DF11_ERR_INVALID;
   const void *ptrs[] = {table->bitstream, table->sign_mantissa, table->decode_table, op->ids, op->out};
   st = check_device_pointers(ptrs, 5);
   if (st != DF11_OK) return st;
@@ -1110,6 +1114,12 @@ df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspa
   if (!workspace) return DF11_ERR_NULL;
   if (!aligned(workspace, 256)) return DF11_ERR_ALIGN;
   if (workspace_bytes < p.bytes) return DF11_ERR_INVALID;
+  // rows of the gradient are written before the last of grad and of the ids are read
+  const uint64_t ob = type_bytes(op->out_type), gb = type_bytes(op->grad_type);
+  const Rows out{op->out, op->rows, op->dim * ob, op->out_stride * ob};
+  if (share_memory(out, Rows{op->grad, op->tokens, op->dim * gb, op->grad_stride * gb}) ||
+      share_memory(out, Rows{op->ids, 1, op->tokens * (op->ids_type == DF11_IDS_I64 ? 8ull : 4ull), 0}))
+    return DF11_ERR_INVALID;
   const void *ptrs[] = {op->ids, op->grad, op->out, workspace};
   st = check_device_pointers(ptrs, 4);
   if (st != DF11_OK) return st;

@@ -33,7 +33,7 @@ struct Rows {
 
 // whether two sets of rows share a byte (columns of one buffer, say, do not)
 inline bool share_memory(Rows a, Rows b) {
-  if (!a.p || !b.p || !a.count || !b.count) return false;
+  if (!a.p || !b.p || !a.count || !b.count || !a.bytes || !b.bytes) return false;
   const uint64_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
   if (x >= y + (b.count - 1) * b.stride + b.bytes || y >= x + (a.count - 1) * a.stride + a.bytes)
     return false;

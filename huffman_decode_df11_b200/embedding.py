@@ -94,7 +94,7 @@ class EmbeddingPlan:
     """A lookup into fixed buffers (a decode loop's token ids and hidden
     states), prepared once: run() is one library call, and reads the ids as they
     are then.  `out` is float32 or BF16, ids.shape + (dim,) or tokens x dim
-    with any row stride."""
+    with any row stride, on other memory than the ids (refused)."""
 
     def __init__(self, d: Df11Device, ids: torch.Tensor, out: torch.Tensor, scale: float = 1.0):
         self._op = _embedding_op(d, ids, out, scale)
@@ -148,7 +148,8 @@ def embedding_gradient(ids: torch.Tensor, grad: torch.Tensor, rows: int,
     `grad`: float32 or BF16, ids.shape + (dim,), or tokens x dim with any row
     stride.  `out`: float32 or BF16, rows x dim with any row stride, allocated in
     `out_dtype` if None.  With `accumulate` the sums are added to `out`, and rows
-    without a token are not touched; otherwise those are set to zero.  Sums run in
+    without a token are not touched; otherwise those are set to zero.  `out` may not
+    share memory with `grad` or `ids` (refused).  Sums run in
     fp32 in token order within pieces of the sorted list: the same call gives
     the same bits.  An id outside the table adds nothing and flags `err`.
     Asynchronous on `stream` (default: the current stream)."""

@@ -410,6 +410,7 @@ typedef struct df11_embedding {
  * out_bf16 of the tensor is not used (may be NULL).  Same conventions as
  * df11_decode_batched otherwise; the ids may be written by the previous kernel in
  * the stream, the table's buffers may not (df11_build_decode_table sees to the order).
+ * The outputs may not overlap the ids (refused, DF11_ERR_INVALID) nor the table.
  */
 df11_status df11_decode_embedding(const df11_tensor *table, const df11_embedding *op,
                                   int32_t *d_err, df11_stream_t stream);
@@ -435,7 +436,8 @@ typedef struct df11_embedding_grad {
  * a call repeats bit for bit.  An id outside the table adds nothing and sets
  * DF11_DEV_ERR_INDEX.  `workspace`: df11_embedding_gradient_workspace bytes of
  * device memory, 256-byte aligned, that no other work uses until this call's
- * work is done.  Asynchronous, no allocation, three launches.
+ * work is done.  The gradient may not overlap grad or the ids (refused, DF11_ERR_INVALID)
+ * nor the workspace.  Asynchronous, no allocation, three launches.
  */
 df11_status df11_embedding_gradient(const df11_embedding_grad *op, void *workspace,
                                     size_t workspace_bytes, int32_t *d_err, df11_stream_t stream);
