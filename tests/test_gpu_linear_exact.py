@@ -64,3 +64,39 @@ def test_a_weight_of_more_than_two_to_the_31_elements(tokens):
     w = _whole((45000, 49152), 1)
     _check(w, df11.compress_linear(w), _whole((tokens, 49152), 2), outs=(torch.float32,))
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("counts", [(1, 33, 300), (40, 2, 7, 128), (1, 2, 3), (33, 0, 8, 9)])
+def test_token_counts_of_both_paths_in_one_call(counts):
+    w = _whole((272, 1411), 1)
+    ds = [df11.compress_linear(w)] * len(counts)
+    xs = [_whole((t, 1411), t) for t in counts]
+    for out in (torch.float32, torch.bfloat16):
+        ys = df11.decode_linear(ds, xs, out_dtype=out)
+        for x, y in zip(xs, ys):
+            assert torch.equal(y, (x.float() @ w.float().t()).to(out))
+
+
+@pytest.mark.parametrize("tokens", [5, 40, 300])
+@pytest.mark.parametrize("cols", [448, 1024])
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+def test_operands_off_their_16_byte_boundaries_one_at_a_time(tokens, cols, kind):
+    rows = 304
+    w, x = _whole((rows, cols), 1), _whole((tokens, cols), 2)
+    d = df11.compress_linear(w)
+
+    def place(t, off):  # the same values `off` elements into a buffer with 16-byte rows
+        wide = torch.zeros(t.shape[0], t.shape[1] + 16, dtype=t.dtype, device="cuda")
+        view = wide[:, off:off + t.shape[1]]
+        view.copy_(t)
+        return view
+
+    b, m, r = (_whole(s, i, 3).to(kind) for i, s in enumerate(((1, rows), (tokens, rows), (tokens, rows))))
+    want = ((x.float() @ w.float().t() + b.float()).clamp(min=0) * m.float() + r.float()).to(kind)
+    for shifted in (None, "x", "y", "bias", "multiplier", "residual"):
+        def at(name, t):
+            return place(t, 3 if name == shifted else 0)
+        y = at("y", torch.zeros_like(want))
+        df11.decode_linear([d], [at("x", x)], [y], biases=[at("bias", b)[0]], activations=["relu"],
+                           multipliers=[at("multiplier", m)], residuals=[at("residual", r)])
+        assert torch.equal(y, want), shifted
