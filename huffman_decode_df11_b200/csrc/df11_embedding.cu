@@ -52,7 +52,8 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// two BF16 products, rounded once: what the fp32 product, exact here, is rounded to
+// two BF16 products, rounded once: what the fp32 product is rounded to, which is exact from 2^-134
+// on (16 bits above 2^-149), and below gives zero like this
 __device__ __forceinline__ uint32_t bf16_product(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

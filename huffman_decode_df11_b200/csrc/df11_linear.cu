@@ -449,6 +449,7 @@ __device__ __forceinline__ void decode_units(const LWeight &lw, uint32_t cta, ui
 // the copy bandwidth (16 warps: 335 us; a table of pairs shared by the lanes, which has
 // half as many lookups but 3.4 wavefronts each: 285 us).  12288 x 4096 and 24 tokens take
 // 49 us, 6144 x 4096 and one token 21 us, of which 4 us are the second kernel and its launch.
+//   With 32 warps a thread has 64 registers, and the compiler keeps 28 bytes of it in local memory.
 
 struct LTensor {
   LWeight w;
@@ -822,8 +823,9 @@ __global__ void __launch_bounds__(1024) linear_rows_kernel(uint32_t *unit_rows, 
 // epilogue's threads take registers from the issuing ones.  What that costs is the epilogue, of
 // which only two parts' products run ahead (4096 x 12288, 2048 tokens and a residual: 190 us for
 // the call against 187 with one chain; 12288 x 4096 with silu and a multiplier: 198 and 190).
-//   The copies of the next stages bound it (four of 240 rows fit), and the power limit where
-// calls follow one another for seconds.
+//   4096 x 12288 and 2048 tokens: 159 us for this kernel by itself, 1.30 PFLOP/s (one chain, BF16:
+// 152), 190 for the call with the decoding, 224 where calls follow one another for seconds, under
+// the power limit.  The copies of the next stages bound it (four of 240 rows fit).
 constexpr int kGemmTokens = 128;
 constexpr int kEpilogueWarps = 12;  // then a warp for the copies and one for the products
 constexpr uint32_t kColStep = 4 * kEpilogueWarps;  // columns from one group of 16 of a warp to its next

@@ -227,7 +227,9 @@ class LinearPlan:
     stream other than the one the plan was made on, or a captured one, is ordered
     behind the work that was queued there by then (the workspace's memory may have
     been in use by it).  A graph that captured a run keeps neither the plan nor its
-    workspace alive: the plan has to outlive the graph, like the buffers."""
+    workspace alive: the plan has to outlive the graph, like the buffers.  Beyond 32
+    tokens the workspace holds the decoded weights, two bytes each (workspace_bytes);
+    decode_linear allocates it for the call only."""
 
     def __init__(self, ds: Sequence[LinearWeight], xs: Sequence[torch.Tensor],
                  ys: Sequence[torch.Tensor], biases=None, activations=None, multipliers=None,

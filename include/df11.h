@@ -346,7 +346,10 @@ typedef struct df11_linear {
  * The linear product of any number of weights, in launches of DF11_MAX_BATCH.
  *   Sums run in fp32 (products of BF16 are exact there) in an order that the
  * sizes and the device fix, so a call repeats bit for bit; bias, activation,
- * multiplier and residual are applied in fp32 and the result is rounded once.  Up
+ * multiplier and residual are applied in fp32 and the result is rounded once.  The
+ * tensor cores' additions may cut off one unit in the last place instead of rounding: a
+ * chain of them has 64 columns up to 32 tokens and at most 512 beyond, and the chains'
+ * sums are added with rounding (1e-7 to 5e-7 in all, relative to the outputs' size).  Up
  * to 32 tokens (the most of the launch's weights) the weights are decoded
  * and multiplied in one kernel and never written; beyond, they are decoded into
  * the workspace and multiplied on the tensor cores.
