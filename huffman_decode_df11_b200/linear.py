@@ -270,6 +270,7 @@ class LinearPlan:
         self._capture = self._lib.df11_capture_id(_stream_handle(None))
         self._born = torch.cuda.Event(external=not self._capture)
         self._born.record()
+        self._event = self._born  # a graph's wait names it for as long as the graph lives
 
     @property
     def outs(self) -> List[torch.Tensor]:

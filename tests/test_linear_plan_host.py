@@ -123,3 +123,16 @@ def test_the_library_s_answers_without_a_device():
     from huffman_decode_df11_b200 import lib
     assert lib().df11_event_done(None) == -1
     assert lib().df11_capture_id(None) == 0
+
+
+def test_the_event_of_a_graph_s_wait_lives_as_long_as_the_plan(monkeypatch):
+    import weakref
+    f = _Fake(monkeypatch)
+    event = weakref.ref(f.plan._born)
+    f.captures[SIDE] = 5
+    assert ("wait", SIDE) in f.run(SIDE)     # a node of the graph's that names the event
+    f.captures, f.done = {}, 1
+    f.run()
+    assert f.plan._born is None and event() is not None
+    del f.plan
+    assert event() is None
