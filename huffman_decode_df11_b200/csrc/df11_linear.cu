@@ -723,13 +723,13 @@ __global__ void __launch_bounds__(256) linear_encode_kernel(const __grid_constan
     for (uint32_t cg = cg0; cg < cg1; ++cg) {
 #pragma unroll 1
       for (uint32_t h = 0; h < 2; ++h) {
-        uint32_t v[8], sm[4];
+        uint32_t v[8], sm[4] = {};
         load_half(a, 16u * rb + 8u * h + (lane >> 2), 64u * cg + 16u * (lane & 3u), v);
 #pragma unroll
         for (uint32_t j = 0; j < 16; ++j) {
           const uint32_t e16 = (v[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
           const uint32_t exp = (e16 >> 7) & 0xFFu;
-          if (!WRITE) {
+          if constexpr (!WRITE) {
             bits += len_s[exp];
           } else {
             const uint32_t sign = e16 >> 15, man = e16 & 0x7Fu;
